@@ -372,6 +372,107 @@ int dsa_index_host(const dsa_problem* p, const void* q_host, const float* q_scal
 int dsa_quantize_e4m3(const void* x, int32_t x_dtype, int64_t rows, int32_t cols,
                       uint8_t* out, float* out_scale, void* stream);
 
+/* ------------------------------------------------------ a cached DSA layer --
+ * The steps between a layer's projections and the calls above, for serving: rotary
+ * positions, the write into a paged cache, the read from it, and latent attention over
+ * every cached position (dsa_sparse_mla attends to a selection of them). */
+
+/* Frequencies of rotary positions, in radians a position, on the host:
+ *     out[i] = base^(-2 i / rot_dim), i < rot_dim / 2,            DSA_ROPE_PLAIN
+ * divided by `factor` (DSA_ROPE_LINEAR), or only the slow ones (DSA_ROPE_YARN): with
+ * n(r) = rot_dim ln(original_len / (2 pi r)) / (2 ln base), lo = max(floor(n(beta_fast)), 0),
+ * hi = min(ceil(n(beta_slow)), rot_dim - 1) and g = clamp((i - lo) / max(hi - lo, 0.001), 0, 1),
+ *     out[i] = base^(-2 i / rot_dim) (g / factor + 1 - g).
+ * Host only; the caller copies the table to the device once and keeps it. */
+enum { DSA_ROPE_PLAIN = 0, DSA_ROPE_LINEAR = 1, DSA_ROPE_YARN = 2 };
+int dsa_rope_frequencies(int32_t rot_dim, double base, int32_t scaling, double factor,
+                         double original_len, double beta_fast, double beta_slow, double* out);
+
+/* Rotary positions: for each token and head, the pair i of the rot_dim values that start
+ * at `offset` turns by t = pos[token] freq[i],
+ *     y_a = mscale (x_a cos t - x_b sin t),   y_b = mscale (x_b cos t + x_a sin t),
+ * a, b = offset + 2 i, + 2 i + 1 (DSA_FLAG_INTERLEAVED) or offset + i, + i + rot_dim / 2
+ * (default, halves).  DSA_FLAG_INVERSE turns by -t: the transpose, so it is also the
+ * gradient (dx from dy with the same mscale).  The other values are copied.
+ *   x, out: value d of head h of token t at t * token_stride + h * head_stride + d
+ *     (elements); dtype DSA_BF16 or DSA_F32, arithmetic in fp32, one rounding.
+ *   out == x with equal strides works in place and touches the rotated values only;
+ *     otherwise x and out must not overlap, and no two places of out may be the same.
+ *   pos [n_tokens] int32 (any sign), freq [rot_dim / 2] double, both on the device.
+ * Angles are formed in 64 bits and reduced there, so far positions lose nothing.
+ * rot_dim even, 2 .. 512, offset + rot_dim <= dim <= 65536, heads <= 65536. */
+#define DSA_FLAG_INTERLEAVED 16u
+#define DSA_FLAG_INVERSE 32u
+typedef struct {
+  int64_t n_tokens;
+  int32_t heads;
+  int32_t dim;
+  int32_t offset;
+  int32_t rot_dim;
+  int32_t dtype;
+  float mscale;
+  int64_t x_token_stride, x_head_stride;
+  int64_t out_token_stride, out_head_stride;
+  uint32_t flags;
+} dsa_rope_problem;
+
+int dsa_rope(const dsa_rope_problem* p, const void* x, const int32_t* pos, const double* freq,
+             void* out, void* stream);
+
+/* A paged cache of rows of dim_q + dim_raw values.  The first dim_q are held as e4m3
+ * codes in groups of 128 with one fp32 scale a group (value = scale * code), the last
+ * dim_raw as bf16.  Three planes; row r of page p starts at
+ *     codes + p * codes_page_stride + r * dim_q            (bytes)
+ *     scale + p * scale_page_stride + r * (dim_q / 128)    (floats)
+ *     raw   + p * raw_page_stride   + r * dim_raw          (bf16 words)
+ * so a page may lie inside a larger block (other layers beside it).  An indexer key
+ * cache has dim_q = 128, dim_raw = 0; a latent cache dim_q = 512, dim_raw = 64, or
+ * dim_q = 0, dim_raw = 576 unquantised.  dim_q a multiple of 128, dim_raw of 8, both at
+ * most 4096; page_size a power of two in [8, 4096]; codes and raw on 16-byte boundaries with page
+ * strides that keep them there.  A plane whose width is 0 is NULL.
+ * A block table [batch, max_pages] int32 (device) names the page that holds positions
+ * j * page_size .. of a sequence.  Only the entries that cover k_len are read; one
+ * outside [0, n_pages) is never followed: its rows read as zeros. */
+typedef struct {
+  int32_t n_pages;
+  int32_t page_size;
+  int32_t dim_q;
+  int32_t dim_raw;
+  void* codes;
+  float* scale;
+  void* raw;
+  int64_t codes_page_stride, scale_page_stride, raw_page_stride;
+} dsa_cache;
+
+/* Write n_tokens rows into the cache: row t of x (dim_q + dim_raw values of x_dtype
+ * DSA_BF16 or DSA_F32, x_stride elements apart) goes to slots[t] = page * page_size + row
+ * (device int64; a slot outside the cache, such as -1, skips the token).  No two tokens
+ * may have the same slot.  Scales: amax / 448 over the group, as dsa_quantize_e4m3 (an
+ * all-zero group has scale 1), or with DSA_FLAG_POW2_SCALE the least power of two that is
+ * at least that, which makes scale * code exact in bf16 (for dsa_paged_mla).
+ * rope (optional, else NULL with pos and freq NULL): rotates the rot_dim values at
+ * rope->offset of the row before they are stored, from x in fp32 with no rounding
+ * between; offset a multiple of 8, rot_dim of 16; uses offset, rot_dim, mscale and
+ * DSA_FLAG_INTERLEAVED / DSA_FLAG_INVERSE of it, pos [n_tokens], freq [rot_dim / 2]. */
+#define DSA_FLAG_POW2_SCALE 64u
+int dsa_cache_write(const dsa_cache* c, const void* x, int32_t x_dtype, int64_t x_stride,
+                    int64_t n_tokens, const int64_t* slots, const dsa_rope_problem* rope,
+                    const int32_t* pos, const double* freq, uint32_t flags, void* stream);
+
+/* Read positions [0, n_k) of each sequence into contiguous rows; rows at or behind
+ * k_len[b] (device int32, NULL: n_k) are left as they were.  n_k <= max_pages * page_size.
+ *   dsa_cache_read        out [batch, n_k, dim_q + dim_raw] of out_dtype DSA_BF16 (the kv
+ *                         of dsa_sparse_mla) or DSA_F32
+ *   dsa_cache_read_codes  out [batch, n_k, dim_q] e4m3 codes and out_scale [batch, n_k,
+ *                         dim_q / 128] (with dim_q = 128 the k and k_scale of dsa_index);
+ *                         dim_raw must be 0 */
+int dsa_cache_read(const dsa_cache* c, const int32_t* block_table, int32_t batch,
+                   int32_t max_pages, int32_t n_k, const int32_t* k_len, void* out,
+                   int32_t out_dtype, void* stream);
+int dsa_cache_read_codes(const dsa_cache* c, const int32_t* block_table, int32_t batch,
+                         int32_t max_pages, int32_t n_k, const int32_t* k_len, void* out,
+                         float* out_scale, void* stream);
+
 /* Device status word recorded in `workspace` by the last call that used it
  * (DSA_OK, DSA_ERR_TIMEOUT or DSA_ERR_NONFINITE).  Synchronises `stream`. */
 int dsa_read_status(const void* workspace, void* stream);

@@ -24,6 +24,10 @@ DSA_FLAG_CHECK = 1
 DSA_FLAG_SORTED = 2
 DSA_FLAG_BY_POSITION = 4
 DSA_FLAG_DOSA = 8                    # exact bound pruning of the dense scan
+DSA_FLAG_INTERLEAVED = 16            # rotary pairs side by side (default: two halves)
+DSA_FLAG_INVERSE = 32                # rotary positions: the transpose
+DSA_FLAG_POW2_SCALE = 64             # cache write: scales are powers of two
+DSA_ROPE_PLAIN, DSA_ROPE_LINEAR, DSA_ROPE_YARN = 0, 1, 2
 DSA_FLAG_TEST_STALL = 0x80000000   # tests of the timeout path only (see include/dsaidx.h)
 
 
@@ -44,6 +48,21 @@ class DsaMlaProblem(C.Structure):
     _fields_ = [("batch", C.c_int32), ("tokens_per_seq", C.c_int32), ("n_k", C.c_int32),
                 ("heads", C.c_int32), ("dim_qk", C.c_int32), ("dim_v", C.c_int32),
                 ("topk", C.c_int32), ("scale", C.c_float), ("flags", C.c_uint32)]
+
+
+class DsaRopeProblem(C.Structure):
+    _fields_ = [("n_tokens", C.c_int64), ("heads", C.c_int32), ("dim", C.c_int32),
+                ("offset", C.c_int32), ("rot_dim", C.c_int32), ("dtype", C.c_int32),
+                ("mscale", C.c_float), ("x_token_stride", C.c_int64),
+                ("x_head_stride", C.c_int64), ("out_token_stride", C.c_int64),
+                ("out_head_stride", C.c_int64), ("flags", C.c_uint32)]
+
+
+class DsaCache(C.Structure):
+    _fields_ = [("n_pages", C.c_int32), ("page_size", C.c_int32), ("dim_q", C.c_int32),
+                ("dim_raw", C.c_int32), ("codes", C.c_void_p), ("scale", C.c_void_p),
+                ("raw", C.c_void_p), ("codes_page_stride", C.c_int64),
+                ("scale_page_stride", C.c_int64), ("raw_page_stride", C.c_int64)]
 
 
 class DsaError(RuntimeError):
@@ -81,7 +100,15 @@ def _load():
     lib.dsa_quantize_e4m3.argtypes = [vp, i32, i64, i32, vp, vp, vp]
     lib.dsa_sparse_mla.argtypes = [C.POINTER(DsaMlaProblem), vp, vp, vp, vp, vp, vp, sz, vp]
     lib.dsa_indexer_backward.argtypes = [P, vp, vp, vp, vp, vp, vp, vp, vp, vp, sz, vp]
-    for f in ("dsa_read_status", "dsa_read_pruned", "dsa_host_staging_size", "dsa_index_host",
+    f64, K, Z = C.c_double, C.POINTER(DsaCache), C.POINTER(DsaRopeProblem)
+    lib.dsa_rope_frequencies.argtypes = [i32, f64, i32, f64, f64, f64, f64, C.POINTER(f64)]
+    lib.dsa_rope.argtypes = [Z, vp, vp, vp, vp, vp]
+    lib.dsa_cache_write.argtypes = [K, vp, i32, i64, i64, vp, Z, vp, vp, C.c_uint32, vp]
+    lib.dsa_cache_read.argtypes = [K, vp, i32, i32, i32, vp, vp, i32, vp]
+    lib.dsa_cache_read_codes.argtypes = [K, vp, i32, i32, i32, vp, vp, vp, vp]
+    for f in ("dsa_rope_frequencies", "dsa_rope", "dsa_cache_write", "dsa_cache_read",
+              "dsa_cache_read_codes",
+              "dsa_read_status", "dsa_read_pruned", "dsa_host_staging_size", "dsa_index_host",
               "dsa_dosa_bounds",
               "dsa_workspace_size", "dsa_route_chunk_rows", "dsa_index",
               "dsa_index_noalloc",
@@ -407,6 +434,242 @@ def dsa_quantize_e4m3(x: torch.Tensor, stream=None):
     _check(lib.dsa_quantize_e4m3(_ptr(x), _dtype_code(x), rows, cols, _ptr(out), _ptr(sc),
                                  _stream(stream)), "dsa_quantize_e4m3")
     return out, sc
+
+
+# ------------------------------------------------------ a cached DSA layer --
+# Calls of a decode step are short, so their checks are written out: each tensor's
+# dtype, device and layout is looked at once, and the call runs on the tensors' device.
+
+_F64, _I64 = (torch.float64,), (torch.int64,)
+_ROWS = (torch.bfloat16, torch.float32)
+_CODES = (torch.uint8, torch.float8_e4m3fn)
+
+
+def _need(name, t, dtypes, device, strided=False):
+    if not isinstance(t, torch.Tensor):
+        raise TypeError(f"{name}: expected a torch.Tensor, got {type(t).__name__}")
+    if t.dtype not in dtypes:
+        raise TypeError(f"{name}: dtype {t.dtype}, expected one of {dtypes}")
+    if t.device != device:
+        raise ValueError(f"{name}: must be on {device}, not {t.device}")
+    if not strided and not t.is_contiguous():
+        raise ValueError(f"{name}: must be contiguous")
+
+
+def _cuda_device(name, t):
+    if not isinstance(t, torch.Tensor):
+        raise TypeError(f"{name}: expected a torch.Tensor, got {type(t).__name__}")
+    if t.device.type != "cuda":
+        raise ValueError(f"{name}: must be on a CUDA device, not {t.device}")
+    return t.device
+
+
+def _on(device, stream, call, what):
+    """`call(stream)` with `device` current, on `stream` (default: that device's current
+    one); raises DsaError for a status other than DSA_OK."""
+    if device.index == torch.cuda.current_device():
+        rc = call((torch.cuda.current_stream() if stream is None else stream).cuda_stream)
+    else:
+        with torch.cuda.device(device):
+            rc = call((torch.cuda.current_stream() if stream is None else stream).cuda_stream)
+    if rc != DSA_OK:
+        raise DsaError(rc, what)
+
+
+def _new(stream, make):
+    """make() with its memory (and fill) on the stream that the call runs on."""
+    if stream is None:
+        return make()
+    with torch.cuda.stream(stream):
+        return make()
+
+
+def rope_frequencies(rot_dim, base=10000.0, scaling="plain", factor=1.0, original_len=4096,
+                     beta_fast=32.0, beta_slow=1.0, device="cuda"):
+    """Table of rotary frequencies (radians a position, float64 [rot_dim / 2]) to keep
+    beside the weights.  scaling: "plain", "linear" or "yarn" (see include/dsaidx.h)."""
+    kinds = {"plain": DSA_ROPE_PLAIN, "linear": DSA_ROPE_LINEAR, "yarn": DSA_ROPE_YARN}
+    if scaling not in kinds:
+        raise ValueError(f"scaling: {scaling!r}, expected one of {tuple(kinds)}")
+    out = torch.empty(max(rot_dim, 0) // 2, dtype=torch.float64)
+    _check(lib.dsa_rope_frequencies(rot_dim, base, kinds[scaling], factor, original_len, beta_fast,
+                                    beta_slow, C.cast(out.data_ptr(), C.POINTER(C.c_double))),
+           "dsa_rope_frequencies")
+    return out.to(device)
+
+
+def _rope(x, pos, freq, offset, interleaved, mscale, out, stream, flags, what):
+    dev = _cuda_device("x", x)
+    _need("x", x, _ROWS, dev, strided=True)
+    if x.dim() != 3 or (x.stride(2) != 1 and x.shape[2] > 1):
+        raise ValueError("x: must be [tokens, heads, dim] with contiguous values")
+    n, heads, dim = x.shape
+    _need("pos", pos, _I32, dev)
+    _need("freq", freq, _F64, dev)
+    if pos.numel() != n:
+        raise ValueError(f"pos: {pos.numel()} positions for {n} tokens")
+    if out is None:
+        out = _new(stream, lambda: torch.empty((n, heads, dim), dtype=x.dtype, device=dev))
+    else:
+        _need("out", out, (x.dtype,), dev, strided=True)
+        if out.shape != x.shape or (out.stride(2) != 1 and dim > 1):
+            raise ValueError("out: must have x's shape and contiguous values")
+    if n == 0 or heads == 0:
+        return out
+    xs, os_ = x.stride(), out.stride()
+    p = DsaRopeProblem(n, heads, dim, offset, 2 * freq.numel(), _dtype_code(x), mscale, xs[0],
+                       xs[1], os_[0], os_[1], flags | (DSA_FLAG_INTERLEAVED if interleaved else 0))
+    _on(dev, stream, lambda st: lib.dsa_rope(C.byref(p), x.data_ptr(), pos.data_ptr(),
+                                             freq.data_ptr(), out.data_ptr(), st), what)
+    return out
+
+
+def rope(x, pos, freq, offset=0, interleaved=False, mscale=1.0, out=None, stream=None):
+    """Rotary positions on the 2 * len(freq) values of each head that start at `offset`.
+    x [tokens, heads, dim] bf16 or fp32 (any token and head strides), pos [tokens] int32,
+    freq as from rope_frequencies.  out=x works in place."""
+    return _rope(x, pos, freq, offset, interleaved, mscale, out, stream, 0, "rope")
+
+
+def rope_backward(grad, pos, freq, offset=0, interleaved=False, mscale=1.0, out=None, stream=None):
+    """Gradient of rope: the transpose of the same rotation applied to `grad`."""
+    return _rope(grad, pos, freq, offset, interleaved, mscale, out, stream, DSA_FLAG_INVERSE,
+                 "rope_backward")
+
+
+class PagedCache:
+    """The planes of a paged cache (dsa_cache of include/dsaidx.h): codes [pages, page,
+    dim_q] e4m3 (or uint8), scale [pages, page, dim_q / 128] fp32, raw [pages, page,
+    dim_raw] bf16; codes and scale, or raw, may be None.  The pages of a plane may be
+    strided (a layer of a larger block); the rest of it is contiguous."""
+
+    __slots__ = ("codes", "scale", "raw", "c", "device")
+
+    def __init__(self, codes=None, scale=None, raw=None):
+        if codes is None and raw is None:
+            raise ValueError("codes, raw: at least one plane is needed")
+        if (codes is None) != (scale is None):
+            raise ValueError("codes and scale come together")
+        first = raw if codes is None else codes
+        dev = self.device = _cuda_device("raw" if codes is None else "codes", first)
+        self.codes, self.scale, self.raw = codes, scale, raw
+        c = self.c = DsaCache()
+        if first.dim() != 3:
+            raise ValueError("planes: must be [pages, page, width]")
+        c.n_pages, c.page_size = first.shape[0], first.shape[1]
+        if codes is not None:
+            c.dim_q = codes.shape[2]
+            c.codes, c.codes_page_stride = self._plane("codes", codes, _CODES, c.dim_q)
+            c.scale, c.scale_page_stride = self._plane("scale", scale, _F32, c.dim_q // 128)
+        if raw is not None:
+            c.dim_raw = raw.shape[2]
+            c.raw, c.raw_page_stride = self._plane("raw", raw, (torch.bfloat16,), c.dim_raw)
+
+    def _plane(self, name, t, dtypes, width):
+        _need(name, t, dtypes, self.device, strided=True)
+        pages, page = self.c.n_pages, self.c.page_size
+        if t.dim() != 3 or tuple(t.shape) != (pages, page, width):
+            raise ValueError(f"{name}: shape {tuple(t.shape)}, expected {(pages, page, width)}")
+        ps, rs, vs = t.stride()
+        if (vs != 1 and width > 1) or (rs != width and page > 1):
+            raise ValueError(f"{name}: the rows of a page must be contiguous")
+        return t.data_ptr(), page * width if pages == 1 else ps
+
+    @staticmethod
+    def empty(n_pages, page_size, dim_q, dim_raw, device="cuda"):
+        """A cache of zeros (e4m3 codes 0, scale 1)."""
+        codes = scale = raw = None
+        if dim_q:
+            codes = torch.zeros((n_pages, page_size, dim_q), dtype=torch.uint8, device=device)
+            codes = codes.view(torch.float8_e4m3fn)
+            scale = torch.ones((n_pages, page_size, dim_q // 128), device=device)
+        if dim_raw:
+            raw = torch.zeros((n_pages, page_size, dim_raw), dtype=torch.bfloat16, device=device)
+        return PagedCache(codes, scale, raw)
+
+
+def cache_write(cache, x, slots, pow2=False, freq=None, pos=None, offset=0, interleaved=False,
+                mscale=1.0, stream=None):
+    """Write rows x [tokens, dim_q + dim_raw] (bf16 or fp32, rows may be strided) at slots
+    [tokens] int64 (page * page_size + row; -1 skips).  With freq and pos the values at
+    `offset` are rotated first.  pow2: scales that are powers of two (for paged_mla)."""
+    dev, c = cache.device, cache.c
+    _need("x", x, _ROWS, dev, strided=True)
+    _need("slots", slots, _I64, dev)
+    n = x.shape[0]
+    if x.dim() != 2 or x.shape[1] != c.dim_q + c.dim_raw or (x.stride(1) != 1 and x.shape[1] > 1):
+        raise ValueError(f"x: must be [tokens, {c.dim_q + c.dim_raw}] with contiguous rows")
+    if slots.numel() != n:
+        raise ValueError(f"slots: {slots.numel()} slots for {n} tokens")
+    turn = pos_p = freq_p = None
+    if (freq is None) != (pos is None):
+        raise ValueError("freq and pos come together")
+    if freq is not None:
+        _need("freq", freq, _F64, dev)
+        _need("pos", pos, _I32, dev)
+        if pos.numel() != n:
+            raise ValueError(f"pos: {pos.numel()} positions for {n} tokens")
+        turn = C.byref(DsaRopeProblem(offset=offset, rot_dim=2 * freq.numel(), mscale=mscale,
+                                      flags=DSA_FLAG_INTERLEAVED if interleaved else 0))
+        pos_p, freq_p = pos.data_ptr(), freq.data_ptr()
+    flags = DSA_FLAG_POW2_SCALE if pow2 else 0
+    _on(dev, stream, lambda st: lib.dsa_cache_write(
+        C.byref(c), x.data_ptr(), _dtype_code(x), x.stride(0), n, slots.data_ptr(), turn, pos_p,
+        freq_p, flags, st), "dsa_cache_write")
+
+
+def _table(cache, block_table, n_k, k_len):
+    _need("block_table", block_table, _I32, cache.device)
+    if block_table.dim() != 2:
+        raise ValueError("block_table: must be [batch, max_pages]")
+    if k_len is not None:
+        _need("k_len", k_len, _I32, cache.device)
+        if k_len.numel() != block_table.shape[0]:
+            raise ValueError(f"k_len: {k_len.numel()} lengths for {block_table.shape[0]} sequences")
+
+
+def cache_read(cache, block_table, n_k, k_len=None, dtype=torch.bfloat16, out=None, stream=None):
+    """Positions [0, n_k) of each sequence as rows [batch, n_k, dim_q + dim_raw] of bf16
+    (the kv of sparse_mla) or fp32.  Rows at or behind k_len[b] are left as they were
+    (zeros in a new tensor)."""
+    dev, c = cache.device, cache.c
+    _table(cache, block_table, n_k, k_len)
+    shape = (block_table.shape[0], n_k, c.dim_q + c.dim_raw)
+    if out is None:
+        out = _new(stream, lambda: torch.zeros(shape, dtype=dtype, device=dev))
+    _need("out", out, _ROWS, dev)
+    if tuple(out.shape) != shape:
+        raise ValueError(f"out: shape {tuple(out.shape)}, expected {shape}")
+    _on(dev, stream, lambda st: lib.dsa_cache_read(
+        C.byref(c), block_table.data_ptr(), shape[0], block_table.shape[1], n_k,
+        None if k_len is None else k_len.data_ptr(), out.data_ptr(), _dtype_code(out), st),
+        "dsa_cache_read")
+    return out
+
+
+def cache_read_codes(cache, block_table, n_k, k_len=None, out=None, stream=None):
+    """Positions [0, n_k) of each sequence as they are held: (codes [batch, n_k, dim_q],
+    scale [batch, n_k] or [batch, n_k, dim_q / 128]), with dim_q = 128 the k and k_scale of
+    dsa_index.  Rows at or behind k_len[b] are left as they were (codes 0, scale 1 in new
+    tensors)."""
+    dev, c = cache.device, cache.c
+    _table(cache, block_table, n_k, k_len)
+    batch, groups = block_table.shape[0], c.dim_q // 128
+    if out is None:
+        per_row = (batch, n_k) if groups == 1 else (batch, n_k, groups)
+        out = _new(stream, lambda: (
+            torch.zeros((batch, n_k, c.dim_q), dtype=torch.uint8, device=dev)
+            .view(torch.float8_e4m3fn), torch.ones(per_row, device=dev)))
+    codes, scale = out
+    _need("codes", codes, _CODES, dev)
+    _need("scale", scale, _F32, dev)
+    if tuple(codes.shape) != (batch, n_k, c.dim_q) or scale.numel() != batch * n_k * groups:
+        raise ValueError(f"out: shapes {tuple(codes.shape)}, {tuple(scale.shape)}")
+    _on(dev, stream, lambda st: lib.dsa_cache_read_codes(
+        C.byref(c), block_table.data_ptr(), batch, block_table.shape[1], n_k,
+        None if k_len is None else k_len.data_ptr(), codes.data_ptr(), scale.data_ptr(), st),
+        "dsa_cache_read_codes")
+    return codes, scale
 
 
 def dsa_read_status(workspace: torch.Tensor, stream=None) -> int:

@@ -1,0 +1,471 @@
+// cache.cuh — rotary positions, and the paged cache of a DSA layer: rows written
+// (quantised) into pages and read back.
+//
+// Rotary positions: the pair (x_a, x_b) number i of a token at position p becomes
+//     y_a = m (x_a cos t - x_b sin t),  y_b = m (x_b cos t + x_a sin t),  t = p f_i,
+// with a factor m (1 unless positions are scaled) and a table f of frequencies in
+// radians a position.  The transpose, which is also the gradient, turns by -t.
+// The angle of a far position has no digits left in 32 bits, so turns = p (f / 2 pi)
+// is formed in 64 bits, its whole part is dropped, and only the remaining fraction
+// goes to sincospif in 32 bits.
+//
+// The paged cache holds a row's first dim_q values as e4m3 codes in groups of 128 with
+// one fp32 scale a group, and its last dim_raw values as bf16, in three planes
+// [page][row][..] (a page's rows lie together in each plane, so a group of 128 codes is
+// one aligned 128-byte run and the bf16 part can be an operand of a TMA copy).
+//
+// All three are bound by memory: they read a row once, write it once and hold it in
+// registers between.
+#pragma once
+#include "operand.cuh"
+
+namespace dsa {
+
+// ------------------------------------------------------------- conversions --
+template <typename T>
+struct RowType;
+template <>
+struct RowType<float> {
+  static constexpr int kVec = 4;      // values in 16 bytes
+  __device__ static float get(const float* p) { return *p; }
+  __device__ static void put(float* p, float v) { *p = v; }
+  __device__ static void unpack(const uint4& u, float (&v)[4]) {
+    v[0] = __uint_as_float(u.x);
+    v[1] = __uint_as_float(u.y);
+    v[2] = __uint_as_float(u.z);
+    v[3] = __uint_as_float(u.w);
+  }
+  __device__ static uint4 pack(const float (&v)[4]) {
+    return make_uint4(__float_as_uint(v[0]), __float_as_uint(v[1]), __float_as_uint(v[2]),
+                      __float_as_uint(v[3]));
+  }
+};
+
+__device__ __forceinline__ uint32_t bf16x2(float lo, float hi) {
+  const __nv_bfloat162 h = __floats2bfloat162_rn(lo, hi);
+  uint32_t u;
+  memcpy(&u, &h, 4);
+  return u;
+}
+
+template <>
+struct RowType<__nv_bfloat16> {
+  static constexpr int kVec = 8;
+  __device__ static float get(const __nv_bfloat16* p) { return __bfloat162float(*p); }
+  __device__ static void put(__nv_bfloat16* p, float v) { *p = __float2bfloat16_rn(v); }
+  __device__ static void unpack(const uint4& u, float (&v)[8]) {
+    const uint32_t w[4] = {u.x, u.y, u.z, u.w};
+#pragma unroll
+    for (int i = 0; i < 4; ++i) {
+      v[2 * i] = __uint_as_float(w[i] << 16);
+      v[2 * i + 1] = __uint_as_float(w[i] & 0xffff0000u);
+    }
+  }
+  __device__ static uint4 pack(const float (&v)[8]) {
+    return make_uint4(bf16x2(v[0], v[1]), bf16x2(v[2], v[3]), bf16x2(v[4], v[5]),
+                      bf16x2(v[6], v[7]));
+  }
+};
+
+// cos and sin of position * freq.
+__device__ __forceinline__ float2 turn_of(int32_t position, double freq) {
+  const double turns = (double)position * (freq * 0.15915494309189533577);   // 1 / (2 pi)
+  const float part = (float)(turns - rint(turns));                           // [-1/2, 1/2]
+  float s, c;
+  sincospif(2.f * part, &s, &c);
+  return make_float2(c, s);
+}
+
+// -------------------------------------------------------- rotary positions --
+struct RopeArgs {
+  const void* x;
+  void* out;
+  const int32_t* pos;      // [n_tokens]
+  const double* freq;      // [rot / 2]
+  int64_t n_tokens;
+  int64_t x_ts, x_hs, o_ts, o_hs;   // token and head strides (elements)
+  int32_t heads, offset, rot;
+  int32_t pairs;           // pair units of a head (see below)
+  int32_t units;           // pair and copy units of a head
+  int32_t tpb;             // tokens of a block
+  int32_t span;            // units that one block of a token takes (blockIdx.y of them)
+  float mscale;
+  float sign;              // +1, or -1 for the transpose
+};
+
+constexpr int kRopeThreads = 256;
+constexpr int kRopeBatch = 4;    // units a thread holds at once
+
+// The work of a head is cut into units of one 16-byte vector: in the half layout a
+// pair unit is one vector of the first half and its partner in the second, in the
+// interleaved layout one vector holding whole pairs; the values outside the rotated
+// part are copy units (none when the call is in place).  A thread issues the loads of
+// four units before it uses any, and the block forms the cosines and sines of its
+// tokens (once for all heads) while they are in flight.  Rows that are not aligned to
+// 16 bytes take the same path one pair at a time (VEC = false).
+// Measured: see the table of the operators.
+template <typename T, bool VEC, bool INTER>
+__global__ void __launch_bounds__(kRopeThreads) rope_kernel(const RopeArgs a) {
+  using R = RowType<T>;
+  constexpr int N = VEC ? R::kVec : 1;
+  extern __shared__ float2 turns[];                  // [tpb][rot / 2]: m cos, m sin
+  const int64_t t0 = (int64_t)blockIdx.x * a.tpb;
+  const int nt = (int)(a.n_tokens - t0 < a.tpb ? a.n_tokens - t0 : a.tpb);
+  const int half = a.rot >> 1;
+  const uint32_t per_token = (uint32_t)a.heads * a.units;
+  const uint32_t first = blockIdx.y * (uint32_t)a.span;
+  uint32_t last = a.tpb > 1 ? per_token * nt : first + a.span;
+  if (a.tpb == 1 && last > per_token) last = per_token;
+  const T* x = reinterpret_cast<const T*>(a.x);
+  T* out = reinterpret_cast<T*>(a.out);
+  bool ready = false;
+  for (uint32_t base = first + threadIdx.x; base - threadIdx.x < last;
+       base += kRopeBatch * kRopeThreads) {
+    uint4 va[kRopeBatch], vb[kRopeBatch];
+    float sa[kRopeBatch], sb[kRopeBatch];
+    int64_t oa[kRopeBatch];
+    int tab[kRopeBatch];                             // place in `turns`; -1: a copy unit
+#pragma unroll
+    for (int k = 0; k < kRopeBatch; ++k) {
+      const uint32_t i = base + k * kRopeThreads;
+      if (i >= last) continue;
+      const uint32_t tl = a.tpb > 1 ? i / per_token : 0;
+      const uint32_t r = i - tl * per_token;
+      const uint32_t h = r / (uint32_t)a.units;
+      const int u = (int)(r - h * a.units);
+      int d;
+      if (u < a.pairs) {
+        const int j = INTER && VEC ? u * (N / 2) : u * N;   // first pair of the unit
+        d = a.offset + (INTER ? 2 * j : j);
+        tab[k] = (int)tl * half + j;
+      } else {
+        d = (u - a.pairs) * N;
+        if (d >= a.offset) d += a.rot;
+        tab[k] = -1;
+      }
+      const T* px = x + (t0 + tl) * a.x_ts + (int64_t)h * a.x_hs + d;
+      oa[k] = (t0 + tl) * a.o_ts + (int64_t)h * a.o_hs + d;
+      const int part = INTER ? 1 : half;             // distance of the partner
+      if constexpr (VEC) {
+        va[k] = *reinterpret_cast<const uint4*>(px);
+        if (!INTER && tab[k] >= 0) vb[k] = *reinterpret_cast<const uint4*>(px + half);
+      } else {
+        sa[k] = R::get(px);
+        if (tab[k] >= 0) sb[k] = R::get(px + part);
+      }
+    }
+    if (!ready) {
+      for (int i = threadIdx.x; i < nt * half; i += kRopeThreads) {
+        const int tl = i / half;
+        const float2 cs = turn_of(a.pos[t0 + tl], a.freq[i - tl * half]);
+        turns[i] = make_float2(cs.x * a.mscale, cs.y * a.mscale * a.sign);
+      }
+      __syncthreads();
+      ready = true;
+    }
+#pragma unroll
+    for (int k = 0; k < kRopeBatch; ++k) {
+      const uint32_t i = base + k * kRopeThreads;
+      if (i >= last) continue;
+      T* po = out + oa[k];
+      if (tab[k] < 0) {
+        if constexpr (VEC)
+          *reinterpret_cast<uint4*>(po) = va[k];
+        else
+          R::put(po, sa[k]);
+      } else if constexpr (!VEC) {
+        const float2 cs = turns[tab[k]];
+        R::put(po, sa[k] * cs.x - sb[k] * cs.y);
+        R::put(po + (INTER ? 1 : half), sb[k] * cs.x + sa[k] * cs.y);
+      } else if constexpr (INTER) {
+        float v[N];
+        R::unpack(va[k], v);
+#pragma unroll
+        for (int j = 0; j < N / 2; ++j) {
+          const float2 cs = turns[tab[k] + j];
+          const float p = v[2 * j], q = v[2 * j + 1];
+          v[2 * j] = p * cs.x - q * cs.y;
+          v[2 * j + 1] = q * cs.x + p * cs.y;
+        }
+        *reinterpret_cast<uint4*>(po) = R::pack(v);
+      } else {
+        float v[N], w[N];
+        R::unpack(va[k], v);
+        R::unpack(vb[k], w);
+#pragma unroll
+        for (int j = 0; j < N; ++j) {
+          const float2 cs = turns[tab[k] + j];
+          const float p = v[j], q = w[j];
+          v[j] = p * cs.x - q * cs.y;
+          w[j] = q * cs.x + p * cs.y;
+        }
+        *reinterpret_cast<uint4*>(po) = R::pack(v);
+        *reinterpret_cast<uint4*>(po + half) = R::pack(w);
+      }
+    }
+  }
+}
+
+// -------------------------------------------------------------- paged cache --
+struct CachePlanes {
+  uint8_t* codes;          // [page][row][dim_q]
+  float* scale;            // [page][row][dim_q / 128]
+  __nv_bfloat16* raw;      // [page][row][dim_raw]
+  int64_t codes_ps, scale_ps, raw_ps;   // page strides (elements)
+  int32_t n_pages, page_shift, dim_q, dim_raw;
+};
+
+constexpr int kCacheThreads = 256;
+constexpr int kCacheUnits = kCacheThreads / 8;   // 8 lanes take one chunk of 128 values
+
+struct CacheWriteArgs {
+  CachePlanes c;
+  const void* x;           // rows of dim_q + dim_raw values, x_ts apart
+  int64_t x_ts;
+  const int64_t* slots;    // [n_tokens] page * page_size + row; outside the cache: not written
+  int64_t n_tokens;
+  const int32_t* pos;      // rotation of [offset, offset + rot) (null: none)
+  const double* freq;
+  int32_t offset, rot, inter;
+  float mscale;
+  float sign;              // +1, or -1 for the transpose
+  int32_t pow2;            // scale: least power of two >= amax / 448 (else amax / 448)
+};
+
+// The 8 values of a row that start at d (a multiple of 8), rotated where they lie in
+// the rotated part.
+template <typename T, bool VEC>
+__device__ __forceinline__ void load8(const T* row, int d, float (&v)[8]) {
+  using R = RowType<T>;
+  if constexpr (VEC) {
+    if constexpr (R::kVec == 8) {
+      R::unpack(*reinterpret_cast<const uint4*>(row + d), v);
+    } else {
+      float lo[4], hi[4];
+      R::unpack(*reinterpret_cast<const uint4*>(row + d), lo);
+      R::unpack(*reinterpret_cast<const uint4*>(row + d + 4), hi);
+#pragma unroll
+      for (int j = 0; j < 4; ++j) {
+        v[j] = lo[j];
+        v[j + 4] = hi[j];
+      }
+    }
+  } else {
+#pragma unroll
+    for (int j = 0; j < 8; ++j) v[j] = R::get(row + d + j);
+  }
+}
+
+template <typename T, bool VEC>
+__device__ __forceinline__ void load8_turned(const CacheWriteArgs& a, const T* row, int64_t token,
+                                             int d, float (&v)[8]) {
+  load8<T, VEC>(row, d, v);
+  if (!a.pos || d < a.offset || d >= a.offset + a.rot) return;
+  const int r = d - a.offset, half = a.rot >> 1;
+  const int32_t p = a.pos[token];
+  if (a.inter) {
+#pragma unroll
+    for (int j = 0; j < 4; ++j) {
+      float2 cs = turn_of(p, a.freq[(r >> 1) + j]);
+      cs.x *= a.mscale;
+      cs.y *= a.mscale * a.sign;
+      const float x0 = v[2 * j], x1 = v[2 * j + 1];
+      v[2 * j] = x0 * cs.x - x1 * cs.y;
+      v[2 * j + 1] = x1 * cs.x + x0 * cs.y;
+    }
+  } else {
+    const bool low = r < half;
+    float w[8];
+    load8<T, VEC>(row, low ? d + half : d - half, w);
+#pragma unroll
+    for (int j = 0; j < 8; ++j) {
+      float2 cs = turn_of(p, a.freq[(low ? r : r - half) + j]);
+      cs.x *= a.mscale;
+      cs.y *= (low ? -a.mscale : a.mscale) * a.sign;
+      v[j] = v[j] * cs.x + w[j] * cs.y;
+    }
+  }
+}
+
+// 8 lanes take one chunk of 128 values of a row (two runs of 8 values a lane, 64
+// apart, so each access of the 8 lanes is one contiguous run); the group's largest
+// magnitude is a three-step exchange between them and the chunk is never reread.
+// A scale that is a power of two makes code * scale exact in bf16, so attention on the
+// tensor cores reads the quantised values without a second rounding; e4m3 being a
+// floating format, it costs at most one binade at the bottom of its range.
+template <typename T, bool VEC>
+__global__ void __launch_bounds__(kCacheThreads) cache_write_kernel(const CacheWriteArgs a) {
+  const int l = threadIdx.x & 7;
+  const int chunks = a.c.dim_q / 128 + (a.c.dim_raw + 127) / 128;
+  const int64_t unit = (int64_t)blockIdx.x * kCacheUnits + (threadIdx.x >> 3);
+  const int64_t token = unit / chunks;
+  const int c = (int)(unit - token * chunks);
+  bool live = token < a.n_tokens;
+  int64_t slot = live ? a.slots[token] : -1;
+  live = slot >= 0 && (slot >> a.c.page_shift) < a.c.n_pages;
+  const int64_t page = slot >> a.c.page_shift;
+  const int64_t row = slot & ((1 << a.c.page_shift) - 1);
+  const T* x = reinterpret_cast<const T*>(a.x) + token * a.x_ts;
+  const int q_chunks = a.c.dim_q / 128;
+  if (c < q_chunks) {
+    float v[2][8];
+    float amax = 0.f;
+    if (live) {
+#pragma unroll
+      for (int h = 0; h < 2; ++h) {
+        load8_turned<T, VEC>(a, x, token, c * 128 + h * 64 + l * 8, v[h]);
+#pragma unroll
+        for (int j = 0; j < 8; ++j) amax = fmaxf(amax, fabsf(v[h][j]));
+      }
+    }
+    const uint32_t mates = 0xffu << (threadIdx.x & 24);
+    amax = fmaxf(amax, __shfl_xor_sync(mates, amax, 1));
+    amax = fmaxf(amax, __shfl_xor_sync(mates, amax, 2));
+    amax = fmaxf(amax, __shfl_xor_sync(mates, amax, 4));
+    if (!live) return;
+    float s = 1.f;
+    if (amax > 0.f) {
+      if (a.pow2) {
+        int e;
+        const float m = frexpf(amax, &e);            // amax = m 2^e, m in [1/2, 1)
+        e = m > 0.875f ? e - 8 : e - 9;              // 448 = 0.875 2^9
+        s = ldexpf(1.f, amax > 3.0e38f ? 120 : (e < -126 ? -126 : e));
+      } else {
+        s = __fdiv_rn(amax, 448.f);
+      }
+    }
+    uint8_t* dst = a.c.codes + page * a.c.codes_ps + row * a.c.dim_q + c * 128 + l * 8;
+    const float inv = __fdiv_rn(1.f, s);             // exact where s is a power of two
+#pragma unroll
+    for (int h = 0; h < 2; ++h) {
+      uint32_t w[2] = {0u, 0u};
+#pragma unroll
+      for (int j = 0; j < 8; ++j) {
+        const float u = a.pow2 ? v[h][j] * inv : __fdiv_rn(v[h][j], s);
+        w[j >> 2] |= (uint32_t)e4m3_rn_sat(u) << (8 * (j & 3));
+      }
+      *reinterpret_cast<uint2*>(dst + h * 64) = make_uint2(w[0], w[1]);
+    }
+    if (l == 0) a.c.scale[page * a.c.scale_ps + row * q_chunks + c] = s;
+  } else if (live) {
+    __nv_bfloat16* dst = a.c.raw + page * a.c.raw_ps + row * a.c.dim_raw;
+#pragma unroll
+    for (int h = 0; h < 2; ++h) {
+      const int d = (c - q_chunks) * 128 + h * 64 + l * 8;
+      if (d >= a.c.dim_raw) continue;
+      float v[8];
+      load8_turned<T, VEC>(a, x, token, a.c.dim_q + d, v);
+      *reinterpret_cast<uint4*>(dst + d) = RowType<__nv_bfloat16>::pack(v);
+    }
+  }
+}
+
+struct CacheReadArgs {
+  CachePlanes c;
+  const int32_t* table;    // [batch][max_pages]
+  const int32_t* k_len;    // [batch] or null
+  int32_t batch, max_pages, n_k;
+  void* out;               // [batch][n_k][dim_q + dim_raw], or codes [batch][n_k][dim_q]
+  float* out_scale;        // [batch][n_k][dim_q / 128] (codes)
+};
+
+// Page of a sequence's row, or -1 for a table entry outside the cache.
+__device__ __forceinline__ int32_t page_of(const int32_t* table, int32_t key, int shift,
+                                           int32_t n_pages) {
+  const int32_t p = table[key >> shift];
+  return (uint32_t)p < (uint32_t)n_pages ? p : -1;
+}
+
+__device__ __forceinline__ void e4m3x4_values(uint32_t w, float s, float* v) {
+  const __half2 lo(__nv_cvt_fp8x2_to_halfraw2((__nv_fp8x2_storage_t)(w & 0xffffu), __NV_E4M3));
+  const __half2 hi(__nv_cvt_fp8x2_to_halfraw2((__nv_fp8x2_storage_t)(w >> 16), __NV_E4M3));
+  const float2 a = __half22float2(lo), b = __half22float2(hi);
+  v[0] = a.x * s;
+  v[1] = a.y * s;
+  v[2] = b.x * s;
+  v[3] = b.y * s;
+}
+
+template <typename T>
+__device__ __forceinline__ void store8(T* p, const float (&v)[8]) {
+  using R = RowType<T>;
+  if constexpr (R::kVec == 8) {
+    *reinterpret_cast<uint4*>(p) = R::pack(v);
+  } else {
+    const float lo[4] = {v[0], v[1], v[2], v[3]}, hi[4] = {v[4], v[5], v[6], v[7]};
+    *reinterpret_cast<uint4*>(p) = R::pack(lo);
+    *reinterpret_cast<uint4*>(p + 4) = R::pack(hi);
+  }
+}
+
+// Values of a sequence's first n_k rows (those before its length; the rest of `out`
+// stays as it was).  8 lanes take one chunk of 128 values as in the write.
+template <typename T>
+__global__ void __launch_bounds__(kCacheThreads) cache_read_kernel(const CacheReadArgs a) {
+  const int l = threadIdx.x & 7;
+  const int q_chunks = a.c.dim_q / 128;
+  const int chunks = q_chunks + (a.c.dim_raw + 127) / 128;
+  const int64_t unit = (int64_t)blockIdx.x * kCacheUnits + (threadIdx.x >> 3);
+  const int64_t r = unit / chunks;
+  const int c = (int)(unit - r * chunks);
+  const int b = (int)(r / a.n_k);
+  const int s = (int)(r - (int64_t)b * a.n_k);
+  if (b >= a.batch || (a.k_len && s >= a.k_len[b])) return;
+  const int32_t page = page_of(a.table + (int64_t)b * a.max_pages, s, a.c.page_shift, a.c.n_pages);
+  const int row = s & ((1 << a.c.page_shift) - 1);
+  T* out = reinterpret_cast<T*>(a.out) + r * (a.c.dim_q + a.c.dim_raw);
+  if (c < q_chunks) {
+    uint2 w[2] = {make_uint2(0, 0), make_uint2(0, 0)};
+    float sc = 1.f;
+    if (page >= 0) {
+      const uint8_t* src = a.c.codes + page * a.c.codes_ps + row * a.c.dim_q + c * 128 + l * 8;
+      w[0] = *reinterpret_cast<const uint2*>(src);
+      w[1] = *reinterpret_cast<const uint2*>(src + 64);
+      sc = a.c.scale[page * a.c.scale_ps + row * q_chunks + c];
+    }
+#pragma unroll
+    for (int h = 0; h < 2; ++h) {
+      float v[8];
+      e4m3x4_values(w[h].x, sc, v);
+      e4m3x4_values(w[h].y, sc, v + 4);
+      store8(out + c * 128 + h * 64 + l * 8, v);
+    }
+  } else {
+#pragma unroll
+    for (int h = 0; h < 2; ++h) {
+      const int d = (c - q_chunks) * 128 + h * 64 + l * 8;
+      if (d >= a.c.dim_raw) continue;
+      uint4 w = make_uint4(0, 0, 0, 0);
+      if (page >= 0)
+        w = *reinterpret_cast<const uint4*>(a.c.raw + page * a.c.raw_ps + row * a.c.dim_raw + d);
+      float v[8];
+      RowType<__nv_bfloat16>::unpack(w, v);
+      store8(out + a.c.dim_q + d, v);
+    }
+  }
+}
+
+// Codes and scales as they stand (the operands of the indexer's e4m3 scan).
+__global__ void __launch_bounds__(kCacheThreads) cache_read_codes_kernel(const CacheReadArgs a) {
+  const int l = threadIdx.x & 7;
+  const int chunks = a.c.dim_q / 128;
+  const int64_t unit = (int64_t)blockIdx.x * kCacheUnits + (threadIdx.x >> 3);
+  const int64_t r = unit / chunks;
+  const int c = (int)(unit - r * chunks);
+  const int b = (int)(r / a.n_k);
+  const int s = (int)(r - (int64_t)b * a.n_k);
+  if (b >= a.batch || (a.k_len && s >= a.k_len[b])) return;
+  const int32_t page = page_of(a.table + (int64_t)b * a.max_pages, s, a.c.page_shift, a.c.n_pages);
+  const int row = s & ((1 << a.c.page_shift) - 1);
+  uint4 w = make_uint4(0, 0, 0, 0);
+  float sc = 1.f;
+  if (page >= 0) {
+    w = *reinterpret_cast<const uint4*>(a.c.codes + page * a.c.codes_ps + row * a.c.dim_q +
+                                        c * 128 + l * 16);
+    sc = a.c.scale[page * a.c.scale_ps + row * chunks + c];
+  }
+  *reinterpret_cast<uint4*>(reinterpret_cast<uint8_t*>(a.out) + r * a.c.dim_q + c * 128 + l * 16) = w;
+  if (l == 0) a.out_scale[r * chunks + c] = sc;
+}
+
+}  // namespace dsa

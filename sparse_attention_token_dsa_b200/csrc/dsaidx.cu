@@ -18,6 +18,7 @@
 #include "bwd.cuh"
 #include "dosa.cuh"
 #include "finalize.cuh"
+#include "host.cuh"
 #include "mla.cuh"
 #include "prep.cuh"
 #include "resid.cuh"
@@ -186,25 +187,6 @@ size_t log_bytes(const ScanPlan& pl) {
 }
 
 // ---------------------------------------------------------- TMA encoding --
-typedef CUresult (*EncodeTiledFn)(CUtensorMap*, CUtensorMapDataType, cuuint32_t, void*,
-                                  const cuuint64_t*, const cuuint64_t*, const cuuint32_t*,
-                                  const cuuint32_t*, CUtensorMapInterleave, CUtensorMapSwizzle,
-                                  CUtensorMapL2promotion, CUtensorMapFloatOOBfill);
-
-EncodeTiledFn encode_fn() {
-  static EncodeTiledFn fn = nullptr;
-  static std::once_flag once;
-  std::call_once(once, [] {
-    void* p = nullptr;
-    cudaDriverEntryPointQueryResult q;
-    if (cudaGetDriverEntryPoint("cuTensorMapEncodeTiled", &p, cudaEnableDefault, &q) ==
-            cudaSuccess &&
-        q == cudaDriverEntryPointSuccess)
-      fn = reinterpret_cast<EncodeTiledFn>(p);
-  });
-  return fn;
-}
-
 // 2-D map over a row-major [rows, 128 elements] operand: box = 128 bytes x box_rows,
 // 128-byte swizzle (the layout the MMA descriptors expect).
 bool make_map(CUtensorMap* m, const void* base, int esz, uint64_t rows, uint32_t box_rows) {
@@ -439,7 +421,6 @@ int validate_problem(const dsa_problem* p) {
   return DSA_OK;
 }
 
-bool aligned16(const void* p) { return (reinterpret_cast<uintptr_t>(p) & 15) == 0; }
 
 // Output order of a problem: 0 any, 1 (score desc, index asc), 2 index asc.
 int out_order(const dsa_problem* p) {

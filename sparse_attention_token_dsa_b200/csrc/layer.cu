@@ -1,0 +1,299 @@
+// layer.cu — C ABI of the steps around a cached DSA layer (see include/dsaidx.h):
+// rotary positions, the paged cache and latent attention over it.  Host code here
+// only validates arguments, plans the launch and launches the kernels.
+#include <cuda.h>
+#include <cuda_runtime.h>
+#include <math.h>
+#include <stddef.h>
+#include <stdint.h>
+
+#include "../../include/dsaidx.h"
+#include "cache.cuh"
+#include "common.cuh"
+#include "host.cuh"
+
+using namespace dsa;
+
+namespace {
+
+bool aligned(const void* p, size_t n) { return (reinterpret_cast<uintptr_t>(p) & (n - 1)) == 0; }
+
+int launch_status() { return cudaGetLastError() == cudaSuccess ? DSA_OK : DSA_ERR_CUDA; }
+
+// ---------------------------------------------------------- rotary positions --
+// Whether the places t * ts + h * hs + d of a [tokens][heads][dim] array are distinct.
+bool distinct(int64_t tokens, int64_t heads, int64_t dim, int64_t ts, int64_t hs) {
+  if (ts < 0 || hs < 0) return false;
+  if (tokens == 1 && heads == 1) return true;
+  if (tokens == 1) return hs >= dim;
+  if (heads == 1) return ts >= dim;
+  const bool heads_inside = hs >= dim && ts >= (heads - 1) * hs + dim;
+  const bool tokens_inside = ts >= dim && hs >= (tokens - 1) * ts + dim;
+  return heads_inside || tokens_inside;
+}
+
+template <typename T>
+int launch_rope(RopeArgs& a, int dim, bool vec, bool inter, bool in_place, cudaStream_t st) {
+  const int n = vec ? RowType<T>::kVec : 1;
+  a.pairs = vec && inter ? a.rot / n : a.rot / 2 / n;
+  a.units = a.pairs + (in_place ? 0 : (dim - a.rot) / n);
+  // a block takes about 1024 units (four a thread): several tokens of few heads, or a
+  // part of one token's heads
+  const int64_t per_token = (int64_t)a.heads * a.units;
+  const int64_t target = kRopeThreads * kRopeBatch;
+  int64_t tpb = target / per_token;
+  tpb = tpb < 1 ? 1 : (tpb > 32 ? 32 : tpb);
+  int64_t parts = tpb > 1 ? 1 : (per_token + target - 1) / target;
+  if (parts > 65535) parts = 65535;
+  a.tpb = (int32_t)tpb;
+  a.span = (int32_t)((per_token + parts - 1) / parts);
+  const int64_t blocks = (a.n_tokens + tpb - 1) / tpb;
+  if (blocks > 0x7fffffffll) return DSA_ERR_UNSUPPORTED;
+  const dim3 grid((unsigned)blocks, (unsigned)parts);
+  const size_t smem = (size_t)tpb * (a.rot / 2) * sizeof(float2);   // <= 64 KB
+  void (*kern)(const RopeArgs) =
+      vec ? (inter ? rope_kernel<T, true, true> : rope_kernel<T, true, false>)
+          : (inter ? rope_kernel<T, false, true> : rope_kernel<T, false, false>);
+  if (smem > 48 * 1024 &&
+      cudaFuncSetAttribute(kern, cudaFuncAttributeMaxDynamicSharedMemorySize, (int)smem) !=
+          cudaSuccess)
+    return DSA_ERR_CUDA;
+  kern<<<grid, kRopeThreads, smem, st>>>(a);
+  return launch_status();
+}
+
+// -------------------------------------------------------------- paged cache --
+int page_shift(int v) {
+  int s = 0;
+  while ((1 << s) < v) ++s;
+  return s;
+}
+
+int validate_cache(const dsa_cache* c) {
+  if (!c) return DSA_ERR_INVALID;
+  if (c->n_pages < 1 || c->dim_q < 0 || c->dim_raw < 0 || c->dim_q + (int64_t)c->dim_raw < 1)
+    return DSA_ERR_INVALID;
+  if (c->page_size < 8 || c->page_size > 4096 || (c->page_size & (c->page_size - 1)) ||
+      c->dim_q % 128 || c->dim_raw % 8 || c->dim_q > 4096 || c->dim_raw > 4096)
+    return DSA_ERR_UNSUPPORTED;
+  if (c->dim_q) {
+    if (!c->codes || !c->scale) return DSA_ERR_INVALID;
+    if (!aligned16(c->codes) || !aligned(c->scale, 4) || c->codes_page_stride % 16)
+      return DSA_ERR_INVALID;
+    if (c->codes_page_stride < (int64_t)c->page_size * c->dim_q ||
+        c->scale_page_stride < (int64_t)c->page_size * (c->dim_q / 128))
+      return DSA_ERR_INVALID;
+  } else if (c->codes || c->scale) {
+    return DSA_ERR_INVALID;
+  }
+  if (c->dim_raw) {
+    if (!c->raw || !aligned16(c->raw) || c->raw_page_stride % 8 ||
+        c->raw_page_stride < (int64_t)c->page_size * c->dim_raw)
+      return DSA_ERR_INVALID;
+  } else if (c->raw) {
+    return DSA_ERR_INVALID;
+  }
+  return DSA_OK;
+}
+
+CachePlanes planes(const dsa_cache* c) {
+  CachePlanes p{};
+  p.codes = reinterpret_cast<uint8_t*>(c->codes);
+  p.scale = c->scale;
+  p.raw = reinterpret_cast<__nv_bfloat16*>(c->raw);
+  p.codes_ps = c->codes_page_stride;
+  p.scale_ps = c->scale_page_stride;
+  p.raw_ps = c->raw_page_stride;
+  p.n_pages = c->n_pages;
+  p.page_shift = page_shift(c->page_size);
+  p.dim_q = c->dim_q;
+  p.dim_raw = c->dim_raw;
+  return p;
+}
+
+int chunks_of(const dsa_cache* c) { return c->dim_q / 128 + (c->dim_raw + 127) / 128; }
+
+// Arguments shared by the two reads; *blocks: the grid (0: nothing to read).
+int read_args(const dsa_cache* c, const int32_t* table, int32_t batch, int32_t max_pages,
+              int32_t n_k, const int32_t* k_len, void* out, int chunks, CacheReadArgs* a,
+              unsigned* blocks) {
+  const int v = validate_cache(c);
+  if (v != DSA_OK) return v;
+  if (!table || !out || batch < 1 || n_k < 0 || max_pages < 0) return DSA_ERR_INVALID;
+  if (!aligned(table, 4) || !aligned(k_len, 4)) return DSA_ERR_INVALID;
+  if ((int64_t)max_pages * c->page_size < n_k || !aligned16(out)) return DSA_ERR_INVALID;
+  const int64_t n = ((int64_t)batch * n_k * chunks + kCacheUnits - 1) / kCacheUnits;
+  if (n > 0x7fffffffll) return DSA_ERR_UNSUPPORTED;
+  *blocks = (unsigned)n;
+  a->c = planes(c);
+  a->table = table;
+  a->k_len = k_len;
+  a->batch = batch;
+  a->max_pages = max_pages;
+  a->n_k = n_k;
+  a->out = out;
+  return DSA_OK;
+}
+
+}  // namespace
+
+extern "C" {
+
+int dsa_rope_frequencies(int32_t rot_dim, double base, int32_t scaling, double factor,
+                         double original_len, double beta_fast, double beta_slow, double* out) {
+  if (!out || rot_dim < 2 || !(base > 1.0) || !isfinite(base)) return DSA_ERR_INVALID;
+  if ((rot_dim & 1) || rot_dim > 512 || scaling < DSA_ROPE_PLAIN || scaling > DSA_ROPE_YARN)
+    return DSA_ERR_UNSUPPORTED;
+  if (scaling != DSA_ROPE_PLAIN && (!(factor > 0.0) || !isfinite(factor))) return DSA_ERR_INVALID;
+  double lo = 0, hi = 0;
+  if (scaling == DSA_ROPE_YARN) {
+    if (!(original_len > 0.0) || !isfinite(original_len) || !(beta_fast > 0.0) ||
+        !(beta_slow > 0.0) || !isfinite(beta_fast) || !isfinite(beta_slow))
+      return DSA_ERR_INVALID;
+    const double two_pi = 6.283185307179586477;
+    lo = floor(rot_dim * log(original_len / (two_pi * beta_fast)) / (2.0 * log(base)));
+    hi = ceil(rot_dim * log(original_len / (two_pi * beta_slow)) / (2.0 * log(base)));
+    lo = lo < 0 ? 0 : lo;
+    hi = hi > rot_dim - 1 ? rot_dim - 1 : hi;
+  }
+  for (int i = 0; i < rot_dim / 2; ++i) {
+    const double f = pow(base, -2.0 * i / rot_dim);
+    double g = scaling == DSA_ROPE_LINEAR ? 1.0 : 0.0;
+    if (scaling == DSA_ROPE_YARN) {
+      g = (i - lo) / (hi - lo > 0.001 ? hi - lo : 0.001);
+      g = g < 0 ? 0 : (g > 1 ? 1 : g);
+    }
+    out[i] = scaling == DSA_ROPE_PLAIN ? f : f * (g / factor + 1.0 - g);
+  }
+  return DSA_OK;
+}
+
+int dsa_rope(const dsa_rope_problem* p, const void* x, const int32_t* pos, const double* freq,
+             void* out, void* stream) {
+  if (!p || p->n_tokens < 0 || p->heads < 1 || p->dim < 1 || p->offset < 0 || p->rot_dim < 2)
+    return DSA_ERR_INVALID;
+  if (p->dtype != DSA_BF16 && p->dtype != DSA_F32) return DSA_ERR_UNSUPPORTED;
+  if ((p->rot_dim & 1) || p->rot_dim > 512 || p->dim > 65536 || p->heads > 65536)
+    return DSA_ERR_UNSUPPORTED;
+  if ((int64_t)p->offset + p->rot_dim > p->dim || !isfinite(p->mscale)) return DSA_ERR_INVALID;
+  if (p->n_tokens == 0) return DSA_OK;
+  if (!x || !pos || !freq || !out) return DSA_ERR_INVALID;
+  const size_t esz = p->dtype == DSA_BF16 ? 2 : 4;
+  if (!aligned(x, esz) || !aligned(out, esz) || !aligned(pos, 4) || !aligned(freq, 8))
+    return DSA_ERR_INVALID;
+  if (!distinct(p->n_tokens, p->heads, p->dim, p->out_token_stride, p->out_head_stride))
+    return DSA_ERR_INVALID;
+  const bool same = p->x_token_stride == p->out_token_stride &&
+                    p->x_head_stride == p->out_head_stride;
+  if (x == out && !same) return DSA_ERR_INVALID;
+  RopeArgs a{};
+  a.x = x;
+  a.out = out;
+  a.pos = pos;
+  a.freq = freq;
+  a.n_tokens = p->n_tokens;
+  a.x_ts = p->x_token_stride;
+  a.x_hs = p->x_head_stride;
+  a.o_ts = p->out_token_stride;
+  a.o_hs = p->out_head_stride;
+  a.heads = p->heads;
+  a.offset = p->offset;
+  a.rot = p->rot_dim;
+  a.mscale = p->mscale;
+  a.sign = p->flags & DSA_FLAG_INVERSE ? -1.f : 1.f;
+  const bool inter = (p->flags & DSA_FLAG_INTERLEAVED) != 0;
+  // 16-byte vectors where every head's row, the rotated part and (halves) its middle
+  // start on one
+  const int n = (int)(16 / esz);
+  const bool vec = aligned16(x) && aligned16(out) && p->dim % n == 0 && p->offset % n == 0 &&
+                   (inter ? p->rot_dim % n == 0 : p->rot_dim % (2 * n) == 0) &&
+                   a.x_ts % n == 0 && a.x_hs % n == 0 && a.o_ts % n == 0 && a.o_hs % n == 0;
+  cudaStream_t st = reinterpret_cast<cudaStream_t>(stream);
+  return p->dtype == DSA_BF16 ? launch_rope<__nv_bfloat16>(a, p->dim, vec, inter, x == out, st)
+                              : launch_rope<float>(a, p->dim, vec, inter, x == out, st);
+}
+
+int dsa_cache_write(const dsa_cache* c, const void* x, int32_t x_dtype, int64_t x_stride,
+                    int64_t n_tokens, const int64_t* slots, const dsa_rope_problem* rope,
+                    const int32_t* pos, const double* freq, uint32_t flags, void* stream) {
+  const int v = validate_cache(c);
+  if (v != DSA_OK) return v;
+  if (n_tokens < 0 || x_stride < 0) return DSA_ERR_INVALID;
+  if (x_dtype != DSA_BF16 && x_dtype != DSA_F32) return DSA_ERR_UNSUPPORTED;
+  if (rope) {
+    if (rope->offset < 0 || rope->rot_dim < 2 ||
+        (int64_t)rope->offset + rope->rot_dim > c->dim_q + c->dim_raw || !isfinite(rope->mscale))
+      return DSA_ERR_INVALID;
+    if (rope->offset % 8 || rope->rot_dim % 16 || rope->rot_dim > 512) return DSA_ERR_UNSUPPORTED;
+    if (n_tokens && (!pos || !freq)) return DSA_ERR_INVALID;
+  } else if (pos || freq) {
+    return DSA_ERR_INVALID;
+  }
+  if (n_tokens == 0) return DSA_OK;
+  const size_t esz = x_dtype == DSA_BF16 ? 2 : 4;
+  if (!x || !slots || !aligned(x, esz) || !aligned(slots, 8) || !aligned(pos, 4) ||
+      !aligned(freq, 8))
+    return DSA_ERR_INVALID;
+  CacheWriteArgs a{};
+  a.c = planes(c);
+  a.x = x;
+  a.x_ts = x_stride;
+  a.slots = slots;
+  a.n_tokens = n_tokens;
+  if (rope) {
+    a.pos = pos;
+    a.freq = freq;
+    a.offset = rope->offset;
+    a.rot = rope->rot_dim;
+    a.inter = (rope->flags & DSA_FLAG_INTERLEAVED) != 0;
+    a.mscale = rope->mscale;
+    a.sign = rope->flags & DSA_FLAG_INVERSE ? -1.f : 1.f;
+  }
+  a.pow2 = (flags & DSA_FLAG_POW2_SCALE) != 0;
+  const int64_t blocks = (n_tokens * chunks_of(c) + kCacheUnits - 1) / kCacheUnits;
+  if (n_tokens > (1ll << 40) || blocks > 0x7fffffffll) return DSA_ERR_UNSUPPORTED;
+  const bool vec = aligned16(x) && x_stride % (int64_t)(16 / esz) == 0;
+  cudaStream_t st = reinterpret_cast<cudaStream_t>(stream);
+  void (*kern)(const CacheWriteArgs) =
+      x_dtype == DSA_BF16
+          ? (vec ? cache_write_kernel<__nv_bfloat16, true> : cache_write_kernel<__nv_bfloat16, false>)
+          : (vec ? cache_write_kernel<float, true> : cache_write_kernel<float, false>);
+  kern<<<(unsigned)blocks, kCacheThreads, 0, st>>>(a);
+  return launch_status();
+}
+
+int dsa_cache_read(const dsa_cache* c, const int32_t* block_table, int32_t batch,
+                   int32_t max_pages, int32_t n_k, const int32_t* k_len, void* out,
+                   int32_t out_dtype, void* stream) {
+  CacheReadArgs a{};
+  unsigned blocks = 0;
+  const int v = read_args(c, block_table, batch, max_pages, n_k, k_len, out,
+                          c ? chunks_of(c) : 0, &a, &blocks);
+  if (v != DSA_OK) return v;
+  if (out_dtype != DSA_BF16 && out_dtype != DSA_F32) return DSA_ERR_UNSUPPORTED;
+  if (blocks == 0) return DSA_OK;
+  cudaStream_t st = reinterpret_cast<cudaStream_t>(stream);
+  if (out_dtype == DSA_BF16)
+    cache_read_kernel<__nv_bfloat16><<<blocks, kCacheThreads, 0, st>>>(a);
+  else
+    cache_read_kernel<float><<<blocks, kCacheThreads, 0, st>>>(a);
+  return launch_status();
+}
+
+int dsa_cache_read_codes(const dsa_cache* c, const int32_t* block_table, int32_t batch,
+                         int32_t max_pages, int32_t n_k, const int32_t* k_len, void* out,
+                         float* out_scale, void* stream) {
+  CacheReadArgs a{};
+  unsigned blocks = 0;
+  const int v = read_args(c, block_table, batch, max_pages, n_k, k_len, out,
+                          c ? c->dim_q / 128 : 0, &a, &blocks);
+  if (v != DSA_OK) return v;
+  if (!out_scale || !aligned(out_scale, 4) || c->dim_q == 0) return DSA_ERR_INVALID;
+  if (c->dim_raw) return DSA_ERR_UNSUPPORTED;
+  if (blocks == 0) return DSA_OK;
+  a.out_scale = out_scale;
+  cache_read_codes_kernel<<<blocks, kCacheThreads, 0, reinterpret_cast<cudaStream_t>(stream)>>>(a);
+  return launch_status();
+}
+
+}  // extern "C"

@@ -24,7 +24,7 @@
 // rescaled.  The result o = O / l is exact up to rounding for any m.
 // Warps 0-3: softmax and output; warp 4: TMA producer; warp 5: MMA issuer.
 #pragma once
-#include "common.cuh"
+#include "operand.cuh"
 
 namespace dsa {
 
@@ -60,37 +60,6 @@ struct MlaSmemTail {
 constexpr size_t mla_smem_bytes() {
   return 1024 + (size_t)kMlaQChunks * 16384 + (size_t)kMlaKS * 8192 + 4 * 8192 + 16384 +
          sizeof(MlaSmemTail);
-}
-
-
-// Shared-memory descriptor of an MN-major operand in 128-byte swizzled rows:
-// each 128-byte row holds 64 consecutive MN elements of one K index, 8 rows form
-// a 1024-byte atom (SBO = 1024 between K groups of 8), and MN blocks of 64
-// elements lie `lbo` bytes apart.
-__device__ __forceinline__ uint64_t make_sdesc_mn(uint32_t smem_addr, uint32_t lbo) {
-  uint64_t d = 0;
-  d |= (uint64_t)((smem_addr >> 4) & 0x3FFF);
-  d |= (uint64_t)((lbo >> 4) & 0x3FFF) << 16;
-  d |= (uint64_t)(1024 >> 4) << 32;
-  d |= (uint64_t)1 << 46;
-  d |= (uint64_t)2 << 61;
-  return d;
-}
-
-__device__ __forceinline__ void tmem_st32(uint32_t taddr, const uint32_t (&r)[32]) {
-  asm volatile(
-      "tcgen05.st.sync.aligned.32x32b.x32.b32 [%0], {%1, %2, %3, %4, %5, %6, %7, %8, %9, %10, "
-      "%11, %12, %13, %14, %15, %16, %17, %18, %19, %20, %21, %22, %23, %24, %25, %26, %27, "
-      "%28, %29, %30, %31, %32};" ::"r"(taddr),
-      "r"(r[0]), "r"(r[1]), "r"(r[2]), "r"(r[3]), "r"(r[4]), "r"(r[5]), "r"(r[6]), "r"(r[7]),
-      "r"(r[8]), "r"(r[9]), "r"(r[10]), "r"(r[11]), "r"(r[12]), "r"(r[13]), "r"(r[14]),
-      "r"(r[15]), "r"(r[16]), "r"(r[17]), "r"(r[18]), "r"(r[19]), "r"(r[20]), "r"(r[21]),
-      "r"(r[22]), "r"(r[23]), "r"(r[24]), "r"(r[25]), "r"(r[26]), "r"(r[27]), "r"(r[28]),
-      "r"(r[29]), "r"(r[30]), "r"(r[31])
-      : "memory");
-}
-__device__ __forceinline__ void tmem_st_wait() {
-  asm volatile("tcgen05.wait::st.sync.aligned;" ::: "memory");
 }
 
 __global__ void __launch_bounds__(kMlaThreads, 1)

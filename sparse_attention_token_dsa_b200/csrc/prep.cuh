@@ -7,23 +7,9 @@
 // heads of a query token), a = amax / 448 (448 = largest finite E4M3), codes by
 // round-to-nearest-even with saturation; both divisions in IEEE fp32.
 #pragma once
-#include "common.cuh"
+#include "operand.cuh"
 
 namespace dsa {
-
-__device__ __forceinline__ float load_as_f32(const void* x, int dtype, int64_t i) {
-  if (dtype == DSA_F32) return reinterpret_cast<const float*>(x)[i];
-  return __uint_as_float((uint32_t)reinterpret_cast<const uint16_t*>(x)[i] << 16);
-}
-
-__device__ __forceinline__ uint8_t e4m3_rn_sat(float v) {
-  return (uint8_t)__nv_cvt_float_to_fp8(v, __NV_SATFINITE, __NV_E4M3);
-}
-
-__device__ __forceinline__ float e4m3_value(uint8_t c) {
-  __half_raw h = __nv_cvt_fp8_to_halfraw((__nv_fp8_storage_t)c, __NV_E4M3);
-  return __half2float(__half(h));
-}
 
 // One warp per row: amax, scale, codes.
 __global__ void quantize_rows_kernel(const void* __restrict__ x, int dtype, int64_t rows,
