@@ -473,6 +473,48 @@ int dsa_cache_read_codes(const dsa_cache* c, const int32_t* block_table, int32_t
                          int32_t max_pages, int32_t n_k, const int32_t* k_len, void* out,
                          float* out_scale, void* stream);
 
+/* Latent attention over the paged cache: absorbed MLA over every cached position, for
+ * one query token a sequence (decode), a few (speculation) or a chunk of a prompt.  The
+ * cache holds rows of 576 values, either dim_q = 0, dim_raw = 576, or dim_q = 512,
+ * dim_raw = 64 (e4m3 codes; with DSA_FLAG_POW2_SCALE scales their values enter the
+ * products exactly, with others they are rounded to bf16).  Query token t of sequence b
+ * sits at position k_len[b] - q_len[b] + t and sees positions s up to its own (its own
+ * row is already cached):
+ *     x_s = scale * q_{t,h} . kv_s,   o_{t,h} = sum_s softmax(x)_s kv_s[0:512],
+ *     lse_{t,h} = log sum_s exp(x_s)      (natural log)
+ *   q   [batch, n_q, heads, 576] bf16
+ *   block_table [batch, max_pages] int32, k_len [batch] int32 (clamped to [0, max_pages *
+ *     page_size]), q_len [batch] int32 (clamped to [0, n_q]; NULL: n_q)
+ *   out [batch, n_q, heads, 512] bf16; out_lse [batch, n_q, heads] fp32 or NULL; tokens at
+ *     or behind q_len[b] are padding: their rows of both are left as they were
+ * A token that sees no position (k_len 0, or k_len < q_len for the first ones) gets out 0
+ * and lse -inf.  Rows of the cache behind k_len may hold anything; a non-finite value
+ * before it makes the outputs of its sequence's tokens unspecified, also of those it is
+ * not visible to.  A block table entry outside [0, n_pages) that covers k_len is recorded
+ * as DSA_ERR_INVALID in the status word and read as zeros.
+ * The softmax weights enter the value product in bf16 (fp32 accumulation); logits, maxima,
+ * denominators and partial outputs are fp32.  Results do not depend on the run: the split
+ * over positions follows from the lengths alone, and partials are joined in their order.
+ * Supported: dim_qk 576, dim_v 512, heads 1 .. 128, max_pages * page_size <= 2^24.
+ * workspace: dsa_paged_mla_workspace_size() bytes, 16-byte aligned (status word first). */
+typedef struct {
+  int32_t batch;
+  int32_t n_q;
+  int32_t heads;
+  int32_t dim_qk;
+  int32_t dim_v;
+  int32_t max_pages;
+  int32_t page_size;
+  float scale;
+  uint32_t flags;
+} dsa_paged_mla_problem;
+
+int dsa_paged_mla_workspace_size(const dsa_paged_mla_problem* p, size_t* bytes);
+int dsa_paged_mla(const dsa_paged_mla_problem* p, const dsa_cache* c, const void* q,
+                  const int32_t* block_table, const int32_t* k_len, const int32_t* q_len,
+                  void* out, float* out_lse, void* workspace, size_t workspace_bytes,
+                  void* stream);
+
 /* Device status word recorded in `workspace` by the last call that used it
  * (DSA_OK, DSA_ERR_TIMEOUT or DSA_ERR_NONFINITE).  Synchronises `stream`. */
 int dsa_read_status(const void* workspace, void* stream);

@@ -65,6 +65,12 @@ class DsaCache(C.Structure):
                 ("scale_page_stride", C.c_int64), ("raw_page_stride", C.c_int64)]
 
 
+class DsaPagedMlaProblem(C.Structure):
+    _fields_ = [("batch", C.c_int32), ("n_q", C.c_int32), ("heads", C.c_int32),
+                ("dim_qk", C.c_int32), ("dim_v", C.c_int32), ("max_pages", C.c_int32),
+                ("page_size", C.c_int32), ("scale", C.c_float), ("flags", C.c_uint32)]
+
+
 class DsaError(RuntimeError):
     def __init__(self, status: int, what: str):
         super().__init__(f"{what}: {status_string(status)} ({status})")
@@ -106,7 +112,10 @@ def _load():
     lib.dsa_cache_write.argtypes = [K, vp, i32, i64, i64, vp, Z, vp, vp, C.c_uint32, vp]
     lib.dsa_cache_read.argtypes = [K, vp, i32, i32, i32, vp, vp, i32, vp]
     lib.dsa_cache_read_codes.argtypes = [K, vp, i32, i32, i32, vp, vp, vp, vp]
-    for f in ("dsa_rope_frequencies", "dsa_rope", "dsa_cache_write", "dsa_cache_read",
+    A = C.POINTER(DsaPagedMlaProblem)
+    lib.dsa_paged_mla_workspace_size.argtypes = [A, C.POINTER(sz)]
+    lib.dsa_paged_mla.argtypes = [A, K, vp, vp, vp, vp, vp, vp, vp, sz, vp]
+    for f in ("dsa_paged_mla_workspace_size", "dsa_paged_mla", "dsa_rope_frequencies", "dsa_rope", "dsa_cache_write", "dsa_cache_read",
               "dsa_cache_read_codes",
               "dsa_read_status", "dsa_read_pruned", "dsa_host_staging_size", "dsa_index_host",
               "dsa_dosa_bounds",
@@ -670,6 +679,61 @@ def cache_read_codes(cache, block_table, n_k, k_len=None, out=None, stream=None)
         None if k_len is None else k_len.data_ptr(), codes.data_ptr(), scale.data_ptr(), st),
         "dsa_cache_read_codes")
     return codes, scale
+
+
+def paged_mla_workspace_size(batch, n_q, heads, max_pages, page_size) -> int:
+    """Bytes of workspace of a paged_mla call (q [batch, n_q, heads, 576])."""
+    p = DsaPagedMlaProblem(batch, n_q, heads, 576, 512, max_pages, page_size, 1.0, 0)
+    n = C.c_size_t(0)
+    _check(lib.dsa_paged_mla_workspace_size(C.byref(p), C.byref(n)), "dsa_paged_mla_workspace_size")
+    return n.value
+
+
+def paged_mla(q, cache, block_table, k_len, scale, q_len=None, flags=0, out=None, out_lse=None,
+              workspace=None, stream=None):
+    """Latent attention over every cached position.  q [batch, n_q, heads, 576] bf16, cache a
+    PagedCache of 576-wide rows (bf16, or 512 e4m3 + 64 bf16), block_table [batch, max_pages],
+    k_len [batch] cached positions (the queries' own included), q_len [batch] query tokens
+    (default n_q).  Returns (out [batch, n_q, heads, 512] bf16, lse [batch, n_q, heads] fp32);
+    rows of tokens at or behind q_len are left as they were."""
+    dev = cache.device
+    _need("q", q, (torch.bfloat16,), dev)
+    if q.dim() != 4:
+        raise ValueError("q: must be [batch, n_q, heads, 576]")
+    batch, n_q, heads, dim = q.shape
+    _table(cache, block_table, 0, k_len)
+    if k_len is None or block_table.shape[0] != batch:
+        raise ValueError(f"block_table, k_len: {block_table.shape[0]} sequences for {batch} in q")
+    if q_len is not None:
+        _need("q_len", q_len, _I32, dev)
+        if q_len.numel() != batch:
+            raise ValueError(f"q_len: {q_len.numel()} lengths for {batch} sequences")
+    p = DsaPagedMlaProblem(batch, n_q, heads, dim, 512, block_table.shape[1], cache.c.page_size,
+                           scale, flags)
+    n = C.c_size_t(0)
+    _check(lib.dsa_paged_mla_workspace_size(C.byref(p), C.byref(n)), "dsa_paged_mla")
+    if out is None:
+        out = _new(stream, lambda: torch.empty((batch, n_q, heads, 512), dtype=torch.bfloat16,
+                                               device=dev))
+    else:
+        _need("out", out, (torch.bfloat16,), dev)
+        if out.numel() != batch * n_q * heads * 512:
+            raise ValueError(f"out: shape {tuple(out.shape)}")
+    if out_lse is None:
+        out_lse = _new(stream, lambda: torch.empty((batch, n_q, heads), device=dev))
+    else:
+        _need("out_lse", out_lse, _F32, dev)
+        if out_lse.numel() != batch * n_q * heads:
+            raise ValueError(f"out_lse: shape {tuple(out_lse.shape)}")
+    if workspace is None:
+        workspace = _new(stream, lambda: torch.empty(n.value, dtype=torch.uint8, device=dev))
+    else:
+        _need("workspace", workspace, _U8, dev)
+    _on(dev, stream, lambda st: lib.dsa_paged_mla(
+        C.byref(p), C.byref(cache.c), q.data_ptr(), block_table.data_ptr(), k_len.data_ptr(),
+        None if q_len is None else q_len.data_ptr(), out.data_ptr(), out_lse.data_ptr(),
+        workspace.data_ptr(), workspace.numel(), st), "dsa_paged_mla")
+    return out, out_lse
 
 
 def dsa_read_status(workspace: torch.Tensor, stream=None) -> int:

@@ -11,6 +11,7 @@
 #include "cache.cuh"
 #include "common.cuh"
 #include "host.cuh"
+#include "paged_mla.cuh"
 
 using namespace dsa;
 
@@ -132,6 +133,65 @@ int read_args(const dsa_cache* c, const int32_t* table, int32_t batch, int32_t m
   a->max_pages = max_pages;
   a->n_k = n_k;
   a->out = out;
+  return DSA_OK;
+}
+
+// -------------------------------------------------------- latent attention --
+// 2-D map over the query rows [rows][576] bf16: box of 64 values x 64 rows, 128-byte
+// swizzle; rows past the end read as zeros.
+bool map_query(CUtensorMap* m, const void* base, uint64_t rows) {
+  EncodeTiledFn fn = encode_fn();
+  if (!fn) return false;
+  cuuint64_t dims[2] = {(cuuint64_t)kPmDqk, (cuuint64_t)rows};
+  cuuint64_t strides[1] = {(cuuint64_t)kPmDqk * 2};
+  cuuint32_t box[2] = {64, 64};
+  cuuint32_t estr[2] = {1, 1};
+  return fn(m, CU_TENSOR_MAP_DATA_TYPE_BFLOAT16, 2, const_cast<void*>(base), dims, strides, box,
+            estr, CU_TENSOR_MAP_INTERLEAVE_NONE, CU_TENSOR_MAP_SWIZZLE_128B,
+            CU_TENSOR_MAP_L2_PROMOTION_L2_256B, CU_TENSOR_MAP_FLOAT_OOB_FILL_NONE) == CUDA_SUCCESS;
+}
+
+// 3-D map over the bf16 plane [pages][page][576]: box of 64 values x box_rows x one page;
+// a page past the end reads as zeros.
+bool map_pages(CUtensorMap* m, const dsa_cache* c, uint32_t box_rows) {
+  EncodeTiledFn fn = encode_fn();
+  if (!fn) return false;
+  cuuint64_t dims[3] = {(cuuint64_t)kPmDqk, (cuuint64_t)c->page_size, (cuuint64_t)c->n_pages};
+  cuuint64_t strides[2] = {(cuuint64_t)kPmDqk * 2, (cuuint64_t)c->raw_page_stride * 2};
+  cuuint32_t box[3] = {64, box_rows, 1};
+  cuuint32_t estr[3] = {1, 1, 1};
+  return fn(m, CU_TENSOR_MAP_DATA_TYPE_BFLOAT16, 3, c->raw, dims, strides, box, estr,
+            CU_TENSOR_MAP_INTERLEAVE_NONE, CU_TENSOR_MAP_SWIZZLE_128B,
+            CU_TENSOR_MAP_L2_PROMOTION_L2_256B, CU_TENSOR_MAP_FLOAT_OOB_FILL_NONE) == CUDA_SUCCESS;
+}
+
+struct PagedMlaPlan {
+  int row_tiles, clusters;
+  int64_t pairs;
+  size_t off_plan, off_ml, off_o, bytes;
+};
+
+int plan_paged_mla(const dsa_paged_mla_problem* p, PagedMlaPlan* pl) {
+  if (!p) return DSA_ERR_INVALID;
+  if (p->batch < 1 || p->n_q < 1 || p->heads < 1 || p->max_pages < 1 || p->page_size < 1)
+    return DSA_ERR_INVALID;
+  if (p->heads > 128 || p->dim_qk != kPmDqk || p->dim_v != kPmDv || p->page_size > 4096 ||
+      (int64_t)p->max_pages * p->page_size > (1ll << 24))
+    return DSA_ERR_UNSUPPORTED;
+  const int64_t rows = (int64_t)p->n_q * p->heads;
+  const int64_t row_tiles = (rows + kPmRows - 1) / kPmRows;
+  pl->pairs = row_tiles * p->batch;
+  const int64_t key_tiles = ((int64_t)p->max_pages * p->page_size + kPmKeys - 1) / kPmKeys;
+  if (rows * p->batch > 0x7fffffffll || pl->pairs * key_tiles > 0x3fffffffll)
+    return DSA_ERR_UNSUPPORTED;
+  pl->row_tiles = (int)row_tiles;
+  const int64_t tiles = pl->pairs * key_tiles;
+  pl->clusters = tiles < kPmClusters ? (int)tiles : kPmClusters;
+  auto up = [](size_t x) { return (x + 255) / 256 * 256; };
+  pl->off_plan = kWsHeaderBytes;
+  pl->off_ml = pl->off_plan + up((size_t)(1 + pl->pairs) * sizeof(int32_t));
+  pl->off_o = pl->off_ml + up((size_t)2 * pl->clusters * kPmRows * sizeof(float2));
+  pl->bytes = pl->off_o + (size_t)2 * pl->clusters * kPmRows * kPmDv * sizeof(float);
   return DSA_OK;
 }
 
@@ -294,6 +354,77 @@ int dsa_cache_read_codes(const dsa_cache* c, const int32_t* block_table, int32_t
   a.out_scale = out_scale;
   cache_read_codes_kernel<<<blocks, kCacheThreads, 0, reinterpret_cast<cudaStream_t>(stream)>>>(a);
   return launch_status();
+}
+
+int dsa_paged_mla_workspace_size(const dsa_paged_mla_problem* p, size_t* bytes) {
+  if (!bytes) return DSA_ERR_INVALID;
+  PagedMlaPlan pl{};
+  const int v = plan_paged_mla(p, &pl);
+  if (v != DSA_OK) return v;
+  *bytes = pl.bytes;
+  return DSA_OK;
+}
+
+int dsa_paged_mla(const dsa_paged_mla_problem* p, const dsa_cache* c, const void* q,
+                  const int32_t* block_table, const int32_t* k_len, const int32_t* q_len,
+                  void* out, float* out_lse, void* workspace, size_t workspace_bytes,
+                  void* stream) {
+  PagedMlaPlan pl{};
+  int v = plan_paged_mla(p, &pl);
+  if (v != DSA_OK) return v;
+  v = validate_cache(c);
+  if (v != DSA_OK) return v;
+  if (c->page_size != p->page_size) return DSA_ERR_INVALID;
+  const bool codes = c->dim_q == kPmDv && c->dim_raw == kPmDqk - kPmDv;
+  if (!codes && !(c->dim_q == 0 && c->dim_raw == kPmDqk)) return DSA_ERR_UNSUPPORTED;
+  if (!q || !block_table || !k_len || !out) return DSA_ERR_INVALID;
+  if (!aligned16(q) || !aligned16(out) || !aligned(block_table, 4) || !aligned(k_len, 4) ||
+      !aligned(q_len, 4) || !aligned(out_lse, 4))
+    return DSA_ERR_INVALID;
+  if (!(p->scale > 0.f) || !(p->scale < 1.0e38f)) return DSA_ERR_INVALID;
+  if (!workspace || workspace_bytes < pl.bytes) return DSA_ERR_WORKSPACE;
+  if (!aligned16(workspace)) return DSA_ERR_INVALID;
+  cudaStream_t st = reinterpret_cast<cudaStream_t>(stream);
+  uint8_t* ws = reinterpret_cast<uint8_t*>(workspace);
+  if (cudaMemsetAsync(ws, 0, kWsHeaderBytes, st) != cudaSuccess) return DSA_ERR_CUDA;
+  CUtensorMap qm{}, km{}, vm{};
+  if (!map_query(&qm, q, (uint64_t)p->batch * p->n_q * p->heads)) return DSA_ERR_CUDA;
+  if (!codes) {
+    const uint32_t page = (uint32_t)c->page_size;
+    if (!map_pages(&km, c, page < 64 ? page : 64) || !map_pages(&vm, c, page < 32 ? page : 32))
+      return DSA_ERR_CUDA;
+  }
+  PagedMlaArgs a{};
+  a.c = planes(c);
+  a.table = block_table;
+  a.k_len = k_len;
+  a.q_len = q_len;
+  a.batch = p->batch;
+  a.n_q = p->n_q;
+  a.heads = p->heads;
+  a.max_pages = p->max_pages;
+  a.row_tiles = pl.row_tiles;
+  a.pairs = (int32_t)pl.pairs;
+  a.scale_log2 = p->scale * 1.4426950408889634f;
+  a.out = reinterpret_cast<uint16_t*>(out);
+  a.lse = out_lse;
+  a.status = reinterpret_cast<int32_t*>(ws);
+  a.plan = reinterpret_cast<int32_t*>(ws + pl.off_plan);
+  a.part_ml = reinterpret_cast<float2*>(ws + pl.off_ml);
+  a.part_o = reinterpret_cast<float*>(ws + pl.off_o);
+  const int smem = (int)paged_mla_smem_bytes();
+  auto kern = codes ? paged_mla_kernel<true> : paged_mla_kernel<false>;
+  if (cudaFuncSetAttribute(kern, cudaFuncAttributeMaxDynamicSharedMemorySize, smem) != cudaSuccess)
+    return DSA_ERR_CUDA;
+  kern<<<(unsigned)(2 * pl.clusters), codes ? kPmThreadsCodes : kPmThreadsRaw, smem, st>>>(qm, km,
+                                                                                         vm, a);
+  if (launch_status() != DSA_OK) return DSA_ERR_CUDA;
+  const int64_t rows = (int64_t)p->n_q * p->heads;
+  const dim3 grid((unsigned)pl.pairs, (unsigned)(rows < kPmRows ? rows : kPmRows));
+  paged_mla_join_kernel<<<grid, kPmJoinThreads, 0, st>>>(a);
+  if (launch_status() != DSA_OK) return DSA_ERR_CUDA;
+  if (p->flags & DSA_FLAG_CHECK) return dsa_read_status(workspace, stream);
+  return DSA_OK;
 }
 
 }  // extern "C"
