@@ -259,70 +259,82 @@ __global__ void __cluster_dims__(2, 1, 1)
 
   if (warp == 4) {
     // ----------------------------------------------------------------- MMA --
-    if (rank == 0 && lane == 0) {
+    // The whole warp waits, one lane issues.
+    if (rank == 0) {
       const uint32_t idesc_s = make_idesc<MmaKind::BF16>(kPmKeys);
       const uint32_t idesc_pv = make_idesc<MmaKind::BF16>(256) | (1u << 16);   // B MN-major
+      const uint64_t q_desc = make_sdesc(smem_u32(Qs)), k_desc = make_sdesc(smem_u32(Ks));
+      const uint64_t p_desc = make_sdesc(smem_u32(Ps)), v_desc = make_sdesc_mn(smem_u32(Vs), 4096);
       uint32_t sc = 0, pc = 0, qc = 0;               // S tiles, PV tiles, segments so far
       bool ok = true;
+      auto wait = [&](uint64_t* bar, uint32_t parity, int where) -> bool {
+        const bool w = mbar_wait(bar, parity, abort, a.status, where);
+        return __all_sync(0xffffffffu, w);
+      };
       auto issue_s = [&]() -> bool {
         const int b = sc & 1;
-        if (!mbar_wait_cluster(&T->s_empty[b], ((sc >> 1) & 1) ^ 1, abort, a.status, 51))
-          return false;
+        if (!wait(&T->s_empty[b], ((sc >> 1) & 1) ^ 1, 51)) return false;
         tc_fence_after();
         const uint32_t d = tmem + 256 + b * 64;
         for (int c = 0; c < kPmKSlots; ++c) {
-          if (!mbar_wait_cluster(&T->k_ready[c], sc & 1, abort, a.status, 52)) return false;
+          if (!wait(&T->k_ready[c], sc & 1, 52)) return false;
           tc_fence_after();
+          if (elect_one()) {
 #pragma unroll
-          for (int kk = 0; kk < 4; ++kk)
-            pair_mma_bf16(d, make_sdesc(smem_u32(Qs + c * kPmKBytes) + kk * 32),
-                          make_sdesc(smem_u32(Ks + c * kPmKBytes) + kk * 32), idesc_s,
-                          (c | kk) != 0);
-          pair_commit(&T->k_empty[c]);
+            for (int kk = 0; kk < 4; ++kk)           // 16 values
+              pair_mma_bf16(d, q_desc + ((c * kPmKBytes + kk * 32) >> 4),
+                            k_desc + ((c * kPmKBytes + kk * 32) >> 4), idesc_s, (c | kk) != 0);
+            pair_commit(&T->k_empty[c]);
+          }
+          __syncwarp();
         }
-        pair_commit(&T->s_full[b]);
+        if (elect_one()) pair_commit(&T->s_full[b]);
+        __syncwarp();
         ++sc;
         return true;
       };
       while (ok && pm_next(a, walk, s)) {
-        ok = mbar_wait_cluster(&T->q_ready, qc & 1, abort, a.status, 53);
-        ok = ok && issue_s();
+        ok = wait(&T->q_ready, qc & 1, 53) && issue_s();
         for (int i = 0; i < s.n && ok; ++i) {
           if (i + 1 < s.n) {
             ok = issue_s();
-          } else {
+          } else if (elect_one()) {
             pair_commit(&T->q_empty);
           }
-          if (ok && i == 0) ok = mbar_wait_cluster(&T->o_empty, (qc & 1) ^ 1, abort, a.status, 54);
-          ok = ok && mbar_wait_cluster(&T->p_full, pc & 1, abort, a.status, 55);
+          __syncwarp();
+          if (ok && i == 0) ok = wait(&T->o_empty, (qc & 1) ^ 1, 54);
+          ok = ok && wait(&T->p_full, pc & 1, 55);
           if (!ok) break;
           tc_fence_after();
           for (int v = 0; v < kPmVSlots && ok; ++v) {
-            ok = mbar_wait_cluster(&T->v_ready[v], pc & 1, abort, a.status, 56);
+            ok = wait(&T->v_ready[v], pc & 1, 56);
             if (!ok) break;
             tc_fence_after();
+            if (elect_one()) {
 #pragma unroll
-            for (int kk = 0; kk < 2; ++kk) {
-              const int k16 = v * 2 + kk;            // 16 positions
-              const uint64_t ad =
-                  make_sdesc(smem_u32(Ps + (k16 >> 2) * kPmKBytes) + (k16 & 3) * 32);
+              for (int kk = 0; kk < 2; ++kk) {       // 16 positions
+                const int k16 = v * 2 + kk;
+                const uint64_t ad =
+                    p_desc + (((k16 >> 2) * kPmKBytes + (k16 & 3) * 32) >> 4);
 #pragma unroll
-              for (int h = 0; h < 2; ++h)            // 128 values of each CTA
-                pair_mma_bf16(tmem + h * 128, ad,
-                              make_sdesc_mn(smem_u32(Vs + v * kPmVBytes) + h * 8192 + kk * 2048,
-                                            4096),
-                              idesc_pv, (i | k16) != 0);
+                for (int h = 0; h < 2; ++h)          // 128 values of each CTA
+                  pair_mma_bf16(tmem + h * 128, ad,
+                                v_desc + ((v * kPmVBytes + h * 8192 + kk * 2048) >> 4), idesc_pv,
+                                (i | k16) != 0);
+              }
+              pair_commit(&T->v_empty[v]);
+              if (v == kPmVSlots - 1) pair_commit(&T->pv_done);
             }
-            pair_commit(&T->v_empty[v]);
+            __syncwarp();
           }
-          pair_commit(&T->pv_done);
           ++pc;
         }
         ++qc;
       }
       if (!ok) {
         // abort path: the MMAs already issued must end before TMEM is freed
-        pair_commit(&T->drain);
+        if (elect_one()) pair_commit(&T->drain);
+        __syncwarp();
         mbar_wait_drain(&T->drain, 0);
       }
     }

@@ -21,40 +21,15 @@ __device__ __forceinline__ uint32_t in_cta(const void* p, uint32_t rank) {
   asm volatile("mapa.shared::cluster.u32 %0, %1, %2;" : "=r"(a) : "r"(smem_u32(p)), "r"(rank));
   return a;
 }
-// Arrive on a barrier of the cluster; what this thread has written or observed before
-// is visible to the thread that waits for it.
+// Arrive on a barrier of the cluster.  Relaxed: a release over the cluster costs about a
+// thousand clocks a call (measured: 13 us a tile of the attention kernel against 2), and
+// nothing here needs it.  What the arrival announces is either no memory at all (a slot
+// read by the tensor core, TMEM read back) or shared memory of the arriving thread's own
+// CTA that the async proxy reads: written by TMA and observed on a barrier, or by this
+// warp before a proxy fence, which orders it with the async proxy itself.
 __device__ __forceinline__ void mbar_arrive_cluster(uint32_t bar) {
-  asm volatile("mbarrier.arrive.release.cluster.shared::cluster.b64 _, [%0];" ::"r"(bar)
+  asm volatile("mbarrier.arrive.relaxed.cluster.shared::cluster.b64 _, [%0];" ::"r"(bar)
                : "memory");
-}
-__device__ __forceinline__ bool mbar_try_wait_cluster(uint64_t* bar, uint32_t parity) {
-  uint32_t ok;
-  asm volatile(
-      "{\n\t.reg .pred p;\n\t"
-      "mbarrier.try_wait.parity.acquire.cluster.shared::cta.b64 p, [%1], %2, %3;\n\t"
-      "selp.u32 %0, 1, 0, p;\n\t}"
-      : "=r"(ok)
-      : "r"(smem_u32(bar)), "r"(parity), "r"(20000u)
-      : "memory");
-  return ok != 0;
-}
-// As mbar_wait, for a barrier that threads of either CTA arrive on.
-__device__ __forceinline__ bool mbar_wait_cluster(uint64_t* bar, uint32_t parity,
-                                                  volatile int* abort, int32_t* status, int where,
-                                                  long long budget = kWaitCycles) {
-  if (mbar_try_wait_cluster(bar, parity)) return true;
-  const long long t0 = clock64();
-  for (uint32_t it = 1;; ++it) {
-    if (mbar_try_wait_cluster(bar, parity)) return true;
-    if ((it & 15) == 0) {
-      if (*abort) return false;
-      if (clock64() - t0 > budget) {
-        *abort = 1;
-        set_status(status, DSA_ERR_TIMEOUT, where);
-        return false;
-      }
-    }
-  }
 }
 
 // ------------------------------------------------------------ cta_group::2 --
@@ -77,6 +52,16 @@ __device__ __forceinline__ void pair_commit(uint64_t* bar) {
       " [%0], %1;" ::"r"(smem_u32(bar)),
       "h"((uint16_t)3)
       : "memory");
+}
+// One lane of a converged warp.  Matrix instructions stand under this and not under a
+// test of the lane's number: their operands then stay in uniform registers (43 against 77
+// clocks from one MMA to the next, N = 128, and 250 with the slot waits between).
+__device__ __forceinline__ bool elect_one() {
+  uint32_t e;
+  asm volatile(
+      "{\n\t.reg .pred p;\n\telect.sync _|p, 0xffffffff;\n\tselp.u32 %0, 1, 0, p;\n\t}"
+      : "=r"(e));
+  return e != 0;
 }
 // bf16 MMA of the pair: M = 128 rows, 64 from each CTA's A tile; N columns, half from
 // each CTA's B tile; the descriptors name the same places in both CTAs.  CTA c's TMEM
