@@ -428,7 +428,7 @@ int dsa_rope(const dsa_rope_problem* p, const void* x, const int32_t* pos, const
  * so a page may lie inside a larger block (other layers beside it).  An indexer key
  * cache has dim_q = 128, dim_raw = 0; a latent cache dim_q = 512, dim_raw = 64, or
  * dim_q = 0, dim_raw = 576 unquantised.  dim_q a multiple of 128, dim_raw of 8, both at
- * most 4096; page_size a power of two in [8, 4096]; codes and raw on 16-byte boundaries with page
+ * most 4096; page_size a power of two in [16, 4096]; codes and raw on 16-byte boundaries with page
  * strides that keep them there.  A plane whose width is 0 is NULL.
  * A block table [batch, max_pages] int32 (device) names the page that holds positions
  * j * page_size .. of a sequence.  Only the entries that cover k_len are read; one

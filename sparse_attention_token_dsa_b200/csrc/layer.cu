@@ -74,7 +74,7 @@ int validate_cache(const dsa_cache* c) {
   if (!c) return DSA_ERR_INVALID;
   if (c->n_pages < 1 || c->dim_q < 0 || c->dim_raw < 0 || c->dim_q + (int64_t)c->dim_raw < 1)
     return DSA_ERR_INVALID;
-  if (c->page_size < 8 || c->page_size > 4096 || (c->page_size & (c->page_size - 1)) ||
+  if (c->page_size < 16 || c->page_size > 4096 || (c->page_size & (c->page_size - 1)) ||
       c->dim_q % 128 || c->dim_raw % 8 || c->dim_q > 4096 || c->dim_raw > 4096)
     return DSA_ERR_UNSUPPORTED;
   if (c->dim_q) {
@@ -151,16 +151,18 @@ bool map_query(CUtensorMap* m, const void* base, uint64_t rows) {
             CU_TENSOR_MAP_L2_PROMOTION_L2_256B, CU_TENSOR_MAP_FLOAT_OOB_FILL_NONE) == CUDA_SUCCESS;
 }
 
-// 3-D map over the bf16 plane [pages][page][576]: box of 64 values x box_rows x one page;
-// a page past the end reads as zeros.
-bool map_pages(CUtensorMap* m, const dsa_cache* c, uint32_t box_rows) {
+// 4-D map over the bf16 plane [pages][page][9 chunks of 64 values]: box of 64 values x
+// box_rows x box_chunks x one page, so a copy lands as whole chunks one after another; a
+// page past the end reads as zeros.
+bool map_pages(CUtensorMap* m, const dsa_cache* c, uint32_t box_rows, uint32_t box_chunks) {
   EncodeTiledFn fn = encode_fn();
   if (!fn) return false;
-  cuuint64_t dims[3] = {(cuuint64_t)kPmDqk, (cuuint64_t)c->page_size, (cuuint64_t)c->n_pages};
-  cuuint64_t strides[2] = {(cuuint64_t)kPmDqk * 2, (cuuint64_t)c->raw_page_stride * 2};
-  cuuint32_t box[3] = {64, box_rows, 1};
-  cuuint32_t estr[3] = {1, 1, 1};
-  return fn(m, CU_TENSOR_MAP_DATA_TYPE_BFLOAT16, 3, c->raw, dims, strides, box, estr,
+  cuuint64_t dims[4] = {64, (cuuint64_t)c->page_size, (cuuint64_t)(kPmDqk / 64),
+                        (cuuint64_t)c->n_pages};
+  cuuint64_t strides[3] = {(cuuint64_t)kPmDqk * 2, 128, (cuuint64_t)c->raw_page_stride * 2};
+  cuuint32_t box[4] = {64, box_rows, box_chunks, 1};
+  cuuint32_t estr[4] = {1, 1, 1, 1};
+  return fn(m, CU_TENSOR_MAP_DATA_TYPE_BFLOAT16, 4, c->raw, dims, strides, box, estr,
             CU_TENSOR_MAP_INTERLEAVE_NONE, CU_TENSOR_MAP_SWIZZLE_128B,
             CU_TENSOR_MAP_L2_PROMOTION_L2_256B, CU_TENSOR_MAP_FLOAT_OOB_FILL_NONE) == CUDA_SUCCESS;
 }
@@ -390,8 +392,10 @@ int dsa_paged_mla(const dsa_paged_mla_problem* p, const dsa_cache* c, const void
   CUtensorMap qm{}, km{}, vm{};
   if (!map_query(&qm, q, (uint64_t)p->batch * p->n_q * p->heads)) return DSA_ERR_CUDA;
   if (!codes) {
+    // one copy a slot where a page holds its rows, else one a page and chunk
     const uint32_t page = (uint32_t)c->page_size;
-    if (!map_pages(&km, c, page < 64 ? page : 64) || !map_pages(&vm, c, page < 32 ? page : 32))
+    if (!map_pages(&km, c, page < 64 ? page : 64, page < 64 ? 1 : 3) ||
+        !map_pages(&vm, c, page < 32 ? page : 32, page < 32 ? 1 : 4))
       return DSA_ERR_CUDA;
   }
   PagedMlaArgs a{};

@@ -17,7 +17,7 @@
 //     S = Q K^T   N = 128 positions, of which the CTA brings 64 (all 576 values)
 //     O += P V    N = 2 x 256 values, of which the CTA brings 256 (of all 128 positions)
 // A single CTA would have to hold 128 x 512 outputs, all of TMEM, with no place for S.
-// A tile of 128 positions runs through rings of operand slots: 9 of 64 positions x 64
+// A tile of 128 positions runs through rings of operand slots: 3 of 64 positions x 192
 // values (K) and 4 of 32 positions x 256 values (V, read in place as an MN-major operand).
 //
 // Work split.  The tiles of all (sequence, row tile) pairs form one line, cut into equal
@@ -40,17 +40,18 @@ constexpr int kPmDqk = 576;
 constexpr int kPmDv = 512;
 constexpr int kPmRows = 128;            // rows of a tile (64 a CTA)
 constexpr int kPmKeys = 128;            // positions of a tile
-constexpr int kPmKSlots = 9;            // K chunks of 64 values: one tile
+constexpr int kPmKSlots = 3;            // K runs of 3 chunks of 64 values: one tile
 constexpr int kPmVSlots = 4;            // V slices of 32 positions: one tile
-constexpr int kPmKBytes = 64 * 128;
+constexpr int kPmChunk = 64 * 128;      // 64 positions (or rows) x 64 values
+constexpr int kPmKBytes = 3 * kPmChunk;
 constexpr int kPmVBytes = 4 * 32 * 128;
 constexpr int kPmQBytes = 9 * 64 * 128;
 constexpr int kPmPBytes = 2 * 64 * 128;
 constexpr int kPmClusters = 74;         // one CTA an SM
 constexpr float kPmLazy = 8.f;          // log2 headroom before the maximum is raised
-constexpr int kPmLoaders = 8;           // warps that convert e4m3 rows
-constexpr int kPmThreadsRaw = 32 * 7;   // softmax 4, MMA, Q and relay, TMA
-constexpr int kPmThreadsCodes = 32 * (6 + kPmLoaders);
+constexpr int kPmLoaders = 4;           // warps that convert e4m3 rows, for K and for V
+constexpr int kPmThreadsRaw = 32 * 10;  // softmax 4, S, PV, K, V, relays of K and V
+constexpr int kPmThreadsCodes = 32 * (6 + 2 * kPmLoaders);   // softmax 4, S, PV, K 4, V 4
 constexpr int kPmJoinThreads = 128;
 
 struct PagedMlaArgs {
@@ -71,11 +72,10 @@ struct PagedMlaArgs {
 };
 
 struct PagedMlaTail {
-  uint64_t q_full, q_empty, q_ready, o_empty, p_full, pv_done, drain;
+  uint64_t q_full, q_empty, q_ready, o_empty, p_full, pv_done, drain[2];
   uint64_t k_full[kPmKSlots], k_ready[kPmKSlots], k_empty[kPmKSlots];
   uint64_t v_full[kPmVSlots], v_ready[kPmVSlots], v_empty[kPmVSlots];
   uint64_t s_full[2], s_empty[2];
-  uint64_t mates[2];       // the two warps that hold the same 32 rows
   float peer[2][128];      // maxima (and at the end denominators) of a row's two threads
   int32_t start_pair, start_off, count, share;
   uint32_t tmem_base;
@@ -150,6 +150,45 @@ __device__ __forceinline__ float ex2(float x) {
   return y;
 }
 
+// Two fp32 values side by side.
+__device__ __forceinline__ uint64_t pack2u(uint32_t lo, uint32_t hi) {
+  uint64_t r;
+  asm("mov.b64 %0, {%1, %2};" : "=l"(r) : "r"(lo), "r"(hi));
+  return r;
+}
+__device__ __forceinline__ uint64_t pack2(float lo, float hi) {
+  return pack2u(__float_as_uint(lo), __float_as_uint(hi));
+}
+__device__ __forceinline__ float lo2(uint64_t v) { return __uint_as_float((uint32_t)v); }
+__device__ __forceinline__ float hi2(uint64_t v) { return __uint_as_float((uint32_t)(v >> 32)); }
+__device__ __forceinline__ uint64_t fma2(uint64_t x, uint64_t y, uint64_t z) {
+  uint64_t r;
+  asm("fma.rn.f32x2 %0, %1, %2, %3;" : "=l"(r) : "l"(x), "l"(y), "l"(z));
+  return r;
+}
+__device__ __forceinline__ uint64_t add2(uint64_t x, uint64_t y) {
+  uint64_t r;
+  asm("add.rn.f32x2 %0, %1, %2;" : "=l"(r) : "l"(x), "l"(y));
+  return r;
+}
+
+// 32 lanes x 8 columns.
+__device__ __forceinline__ void tmem_ld8(uint32_t taddr, uint32_t (&r)[8]) {
+  asm volatile(
+      "tcgen05.ld.sync.aligned.32x32b.x8.b32 {%0, %1, %2, %3, %4, %5, %6, %7}, [%8];\n\t"
+      "tcgen05.wait::ld.sync.aligned;"
+      : "=r"(r[0]), "=r"(r[1]), "=r"(r[2]), "=r"(r[3]), "=r"(r[4]), "=r"(r[5]), "=r"(r[6]),
+        "=r"(r[7])
+      : "r"(taddr)
+      : "memory");
+}
+__device__ __forceinline__ void tmem_st8(uint32_t taddr, const uint32_t (&r)[8]) {
+  asm volatile(
+      "tcgen05.st.sync.aligned.32x32b.x8.b32 [%0], {%1, %2, %3, %4, %5, %6, %7, %8};" ::"r"(taddr),
+      "r"(r[0]), "r"(r[1]), "r"(r[2]), "r"(r[3]), "r"(r[4]), "r"(r[5]), "r"(r[6]), "r"(r[7])
+      : "memory");
+}
+
 // 16 e4m3 codes times a scale as bf16 (exact where the scale is a power of two).
 __device__ __forceinline__ void codes_to_bf16(const uint4& w, float s, uint4& lo, uint4& hi) {
   float v[16];
@@ -160,6 +199,22 @@ __device__ __forceinline__ void codes_to_bf16(const uint4& w, float s, uint4& lo
   lo = make_uint4(bf16x2(v[0], v[1]), bf16x2(v[2], v[3]), bf16x2(v[4], v[5]), bf16x2(v[6], v[7]));
   hi = make_uint4(bf16x2(v[8], v[9]), bf16x2(v[10], v[11]), bf16x2(v[12], v[13]),
                   bf16x2(v[14], v[15]));
+}
+
+__device__ __forceinline__ void tma_load_4d(void* dst, const CUtensorMap* map, uint64_t* bar,
+                                            int32_t x, int32_t y, int32_t z, int32_t w) {
+  asm volatile(
+      "cp.async.bulk.tensor.4d.shared::cluster.global.mbarrier::complete_tx::bytes"
+      " [%0], [%1, {%3, %4, %5, %6}], [%2];" ::"r"(smem_u32(dst)),
+      "l"(reinterpret_cast<uint64_t>(map)), "r"(smem_u32(bar)), "r"(x), "r"(y), "r"(z), "r"(w)
+      : "memory");
+}
+
+// Abort path: let a slot's last copies land.  `n` tiles were begun; the slot's last fill
+// belongs to the n-th or, where the loader gave up before it, to the one before, which
+// the wait's limit then covers.
+__device__ __forceinline__ void drain_slot(uint64_t* full, uint32_t n) {
+  mbar_wait_drain(full, (n & 1) ^ 1, kWaitCycles / 64);
 }
 
 template <bool CODES>
@@ -188,7 +243,6 @@ __global__ void __cluster_dims__(2, 1, 1)
     mbar_init(&T->o_empty, 8);
     mbar_init(&T->p_full, 8);
     mbar_init(&T->pv_done, 1);
-    mbar_init(&T->drain, 1);
     for (int i = 0; i < kPmKSlots; ++i) {
       mbar_init(&T->k_full[i], 1);
       mbar_init(&T->k_ready[i], kReady);
@@ -202,7 +256,7 @@ __global__ void __cluster_dims__(2, 1, 1)
     for (int i = 0; i < 2; ++i) {
       mbar_init(&T->s_full[i], 1);
       mbar_init(&T->s_empty[i], 8);
-      mbar_init(&T->mates[i], 2);
+      mbar_init(&T->drain[i], 1);
     }
     T->abort = 0;
     fence_barrier_init();
@@ -257,125 +311,226 @@ __global__ void __cluster_dims__(2, 1, 1)
   PmWalk walk{T->start_pair, T->start_off, T->count, 2 * cl};
   PmSegment s;
 
+  auto wait = [&](uint64_t* bar, uint32_t parity, int where) -> bool {
+    return mbar_wait(bar, parity, abort, a.status, where);
+  };
+  // The result of `wait`, asked for earlier: a slot's barrier is looked at before the
+  // matrix instructions of the slot before it are issued.
+  auto wait_seen = [&](bool seen, uint64_t* bar, uint32_t parity, int where) -> bool {
+    return seen || mbar_wait(bar, parity, abort, a.status, where);
+  };
+
+  // The roles of warps 4 and up (but for the conversion of codes) run in one lane.
   if (warp == 4) {
-    // ----------------------------------------------------------------- MMA --
-    // The whole warp waits, one lane issues.
-    if (rank == 0) {
-      const uint32_t idesc_s = make_idesc<MmaKind::BF16>(kPmKeys);
-      const uint32_t idesc_pv = make_idesc<MmaKind::BF16>(256) | (1u << 16);   // B MN-major
+    // ------------------------------------------------------- Q, and S = Q K^T --
+    // Each CTA loads its 64 rows of q; CTA 0's warp issues the products of both.  S and
+    // O += P V have a warp each, so neither waits for the other's operands.
+    if (elect_one()) {
+      const uint32_t idesc = make_idesc<MmaKind::BF16>(kPmKeys);
       const uint64_t q_desc = make_sdesc(smem_u32(Qs)), k_desc = make_sdesc(smem_u32(Ks));
-      const uint64_t p_desc = make_sdesc(smem_u32(Ps)), v_desc = make_sdesc_mn(smem_u32(Vs), 4096);
-      uint32_t sc = 0, pc = 0, qc = 0;               // S tiles, PV tiles, segments so far
+      const uint32_t q_ready = in_cta(&T->q_ready, 0);
+      uint32_t sc = 0, qc = 0;                       // tiles, segments so far
       bool ok = true;
-      auto wait = [&](uint64_t* bar, uint32_t parity, int where) -> bool {
-        const bool w = mbar_wait(bar, parity, abort, a.status, where);
-        return __all_sync(0xffffffffu, w);
-      };
-      auto issue_s = [&]() -> bool {
-        const int b = sc & 1;
-        if (!wait(&T->s_empty[b], ((sc >> 1) & 1) ^ 1, 51)) return false;
-        tc_fence_after();
-        const uint32_t d = tmem + 256 + b * 64;
-        for (int c = 0; c < kPmKSlots; ++c) {
-          if (!wait(&T->k_ready[c], sc & 1, 52)) return false;
-          tc_fence_after();
-          if (elect_one()) {
-#pragma unroll
-            for (int kk = 0; kk < 4; ++kk)           // 16 values
-              pair_mma_bf16(d, q_desc + ((c * kPmKBytes + kk * 32) >> 4),
-                            k_desc + ((c * kPmKBytes + kk * 32) >> 4), idesc_s, (c | kk) != 0);
-            pair_commit(&T->k_empty[c]);
-          }
-          __syncwarp();
-        }
-        if (elect_one()) pair_commit(&T->s_full[b]);
-        __syncwarp();
-        ++sc;
-        return true;
-      };
       while (ok && pm_next(a, walk, s)) {
-        ok = wait(&T->q_ready, qc & 1, 53) && issue_s();
-        for (int i = 0; i < s.n && ok; ++i) {
-          if (i + 1 < s.n) {
-            ok = issue_s();
-          } else if (elect_one()) {
-            pair_commit(&T->q_empty);
-          }
-          __syncwarp();
-          if (ok && i == 0) ok = wait(&T->o_empty, (qc & 1) ^ 1, 54);
-          ok = ok && wait(&T->p_full, pc & 1, 55);
-          if (!ok) break;
-          tc_fence_after();
-          for (int v = 0; v < kPmVSlots && ok; ++v) {
-            ok = wait(&T->v_ready[v], pc & 1, 56);
+        ok = wait(&T->q_empty, (qc & 1) ^ 1, 57);
+        if (!ok) break;
+        mbar_arrive_expect_tx(&T->q_full, kPmQBytes);
+        const int row = s.pair.b * a.n_q * a.heads + s.pair.row0 + 64 * rank;
+        for (int c = 0; c < 9; ++c)
+          tma_load_2d(Qs + c * kPmChunk, &qmap, &T->q_full, c * 64, row);
+        ok = wait(&T->q_full, qc & 1, 58);
+        if (!ok) mbar_wait_drain(&T->q_full, qc & 1);
+        else mbar_arrive_cluster(q_ready);
+        if (rank == 0) {
+          ok = ok && wait(&T->q_ready, qc & 1, 53);
+          for (int i = 0; i < s.n && ok; ++i, ++sc) {
+            const int b = sc & 1;
+            bool seen = mbar_try_wait(&T->k_ready[0], sc & 1);
+            ok = wait(&T->s_empty[b], ((sc >> 1) & 1) ^ 1, 51);
             if (!ok) break;
             tc_fence_after();
-            if (elect_one()) {
+            const uint32_t d = tmem + 256 + b * 64;
 #pragma unroll
-              for (int kk = 0; kk < 2; ++kk) {       // 16 positions
-                const int k16 = v * 2 + kk;
-                const uint64_t ad =
-                    p_desc + (((k16 >> 2) * kPmKBytes + (k16 & 3) * 32) >> 4);
+            for (int k = 0; k < kPmKSlots; ++k) {
+              ok = ok && wait_seen(seen, &T->k_ready[k], sc & 1, 52);
+              if (!ok) break;
+              if (k + 1 < kPmKSlots) seen = mbar_try_wait(&T->k_ready[k + 1], sc & 1);
 #pragma unroll
-                for (int h = 0; h < 2; ++h)          // 128 values of each CTA
-                  pair_mma_bf16(tmem + h * 128, ad,
-                                v_desc + ((v * kPmVBytes + h * 8192 + kk * 2048) >> 4), idesc_pv,
-                                (i | k16) != 0);
-              }
-              pair_commit(&T->v_empty[v]);
-              if (v == kPmVSlots - 1) pair_commit(&T->pv_done);
+              for (int c = 3 * k; c < 3 * k + 3; ++c)
+#pragma unroll
+                for (int kk = 0; kk < 4; ++kk)       // 16 values
+                  pair_mma_bf16(d, q_desc + ((c * kPmChunk + kk * 32) >> 4),
+                                k_desc + ((c * kPmChunk + kk * 32) >> 4), idesc, (c | kk) != 0);
+              pair_commit(&T->k_empty[k]);
             }
-            __syncwarp();
+            if (!ok) break;
+            pair_commit(&T->s_full[b]);
+            if (i == s.n - 1) pair_commit(&T->q_empty);
           }
-          ++pc;
+        }
+        ++qc;
+      }
+      // the last arrival from the MMAs has come before the CTA may end
+      if (ok && qc) wait(&T->q_empty, (qc & 1) ^ 1, 70);
+      if (!ok && rank == 0) {
+        // abort path: the MMAs already issued must end before TMEM is freed
+        pair_commit(&T->drain[0]);
+        mbar_wait_drain(&T->drain[0], 0);
+      }
+    }
+  } else if (warp == 5) {
+    // ---------------------------------------------------------------- O += P V --
+    if (rank == 0 && elect_one()) {
+      const uint32_t idesc = make_idesc<MmaKind::BF16>(256) | (1u << 16);   // B MN-major
+      const uint64_t p_desc = make_sdesc(smem_u32(Ps)), v_desc = make_sdesc_mn(smem_u32(Vs), 4096);
+      uint32_t pc = 0, qc = 0;
+      bool ok = true;
+      while (ok && pm_next(a, walk, s)) {
+        ok = wait(&T->o_empty, (qc & 1) ^ 1, 54);
+        for (int i = 0; i < s.n && ok; ++i, ++pc) {
+          ok = wait(&T->p_full, pc & 1, 55);
+          if (!ok) break;
+          bool seen = mbar_try_wait(&T->v_ready[0], pc & 1);
+          tc_fence_after();
+#pragma unroll
+          for (int v = 0; v < kPmVSlots; ++v) {
+            ok = ok && wait_seen(seen, &T->v_ready[v], pc & 1, 56);
+            if (!ok) break;
+            if (v + 1 < kPmVSlots) seen = mbar_try_wait(&T->v_ready[v + 1], pc & 1);
+#pragma unroll
+            for (int kk = 0; kk < 2; ++kk) {         // 16 positions
+              const int k16 = v * 2 + kk;
+              const uint64_t ad = p_desc + (((k16 >> 2) * kPmChunk + (k16 & 3) * 32) >> 4);
+#pragma unroll
+              for (int h = 0; h < 2; ++h)            // 128 values of each CTA
+                pair_mma_bf16(tmem + h * 128, ad,
+                              v_desc + ((v * kPmVBytes + h * 8192 + kk * 2048) >> 4), idesc,
+                              (i | k16) != 0);
+            }
+            pair_commit(&T->v_empty[v]);
+          }
+          if (ok) pair_commit(&T->pv_done);
         }
         ++qc;
       }
       if (!ok) {
-        // abort path: the MMAs already issued must end before TMEM is freed
-        if (elect_one()) pair_commit(&T->drain);
-        __syncwarp();
-        mbar_wait_drain(&T->drain, 0);
+        pair_commit(&T->drain[1]);
+        mbar_wait_drain(&T->drain[1], 0);
       }
     }
-  } else if (warp == 5) {
-    // ------------------------------------------------- Q, and relay to the MMA --
-    // Loads this CTA's 64 rows of q, and tells the MMA thread (in CTA 0) of each
-    // operand slot that TMA has filled here, after zeroing V rows behind k_len.
-    const uint32_t q_ready = in_cta(&T->q_ready, 0);
-    uint32_t kc = 0, vc = 0, qc = 0;
+  } else if (warp >= 6) {
+    // --------------------------------------------------------------- loaders --
+    // K and V have loaders of their own: a V slot comes free half a tile later than the K
+    // slots beside it, and one loader for both would hold the K copies back.
+    uint32_t n = 0;                                  // tiles so far
     bool ok = true;
-    while (ok && pm_next(a, walk, s)) {
-      if (lane == 0) {
-        ok = mbar_wait(&T->q_empty, (qc & 1) ^ 1, abort, a.status, 57);
-        if (ok) {
-          mbar_arrive_expect_tx(&T->q_full, kPmQBytes);
-          const int row = s.pair.b * a.n_q * a.heads + s.pair.row0 + 64 * rank;
-          for (int c = 0; c < 9; ++c)
-            tma_load_2d(Qs + c * kPmKBytes, &qmap, &T->q_full, c * 64, row);
-          ok = mbar_wait(&T->q_full, qc & 1, abort, a.status, 58);
-          if (ok) mbar_arrive_cluster(q_ready);
-          else mbar_wait_drain(&T->q_full, qc & 1);
-        }
-      }
-      ok = __shfl_sync(0xffffffffu, ok, 0);
-      ++qc;
-      if constexpr (!CODES) {
-        for (int i = -1; i < s.n && ok; ++i) {
-          if (i + 1 < s.n) {
-            for (int c = 0; c < kPmKSlots && ok; ++c) {
-              ok = mbar_wait(&T->k_full[c], kc & 1, abort, a.status, 59);
-              ok = __all_sync(0xffffffffu, ok);
-              if (ok && lane == 0) mbar_arrive_cluster(in_cta(&T->k_ready[c], 0));
+    const int shift = a.c.page_shift, mask = (1 << shift) - 1;
+    const int32_t* table = nullptr;                  // of the sequence
+    if constexpr (!CODES) {
+      // page of a position; past the end (and where the table is wrong) one that TMA
+      // reads as zeros
+      auto page_at = [&](int key) -> int {
+        if (key >= s.pair.kl) return a.c.n_pages;
+        const int p = page_of(table, key, shift, a.c.n_pages);
+        if (p < 0) set_status(a.status, DSA_ERR_INVALID, 61);
+        return p < 0 ? a.c.n_pages : p;
+      };
+      if (warp == 6 && elect_one()) {
+        const int rows = min(1 << shift, 64);        // of a copy
+        const int first = 64 * rank;
+        int z[4], next[4];                           // pages of a tile's copies
+        auto pages = [&](int tile, int (&to)[4]) {
+#pragma unroll
+          for (int j = 0; j < 4; ++j)
+            if (j * rows < 64) to[j] = page_at(tile * kPmKeys + first + j * rows);
+        };
+        while (ok && pm_next(a, walk, s)) {
+          table = a.table + (int64_t)s.pair.b * a.max_pages;
+          pages(s.t0, next);
+          for (int i = s.t0; i < s.t0 + s.n && ok; ++i, ++n) {
+#pragma unroll
+            for (int j = 0; j < 4; ++j) z[j] = next[j];
+            if (i + 1 < s.t0 + s.n) pages(i + 1, next);
+            const int row = (i * kPmKeys + first) & mask;
+            for (int k = 0; k < kPmKSlots; ++k) {
+              ok = wait(&T->k_empty[k], (n & 1) ^ 1, 62);
+              if (!ok) break;
+              mbar_arrive_expect_tx(&T->k_full[k], kPmKBytes);
+              if (rows == 64) {
+                tma_load_4d(Ks + k * kPmKBytes, &kmap, &T->k_full[k], 0, row, 3 * k, z[0]);
+              } else {                               // chunk by chunk, pages below one another
+                for (int c = 0; c < 3; ++c)
+#pragma unroll
+                  for (int j = 0; j < 4; ++j)
+                    if (j * rows < 64)
+                      tma_load_4d(Ks + k * kPmKBytes + c * kPmChunk + j * rows * 128, &kmap,
+                                  &T->k_full[k], 0, 0, 3 * k + c, z[j]);
+              }
             }
-            ++kc;
           }
-          if (i >= 0) {
-            for (int v = 0; v < kPmVSlots && ok; ++v) {
-              ok = mbar_wait(&T->v_full[v], vc & 1, abort, a.status, 60);
+        }
+        // the last copies have landed (also on the abort path) and the last arrivals from
+        // the MMAs have come before the CTA may end
+        for (int k = 0; k < kPmKSlots && n; ++k)
+          if (ok) wait(&T->k_empty[k], (n & 1) ^ 1, 64);
+          else drain_slot(&T->k_full[k], n);
+      } else if (warp == 7 && elect_one()) {
+        const int rows = min(1 << shift, 32);
+        int z[8], next[8];
+        auto pages = [&](int tile, int (&to)[8]) {
+#pragma unroll
+          for (int j = 0; j < 8; ++j)
+            if (j * rows < kPmKeys) to[j] = page_at(tile * kPmKeys + j * rows);
+        };
+        while (ok && pm_next(a, walk, s)) {
+          table = a.table + (int64_t)s.pair.b * a.max_pages;
+          pages(s.t0, next);
+          for (int i = s.t0; i < s.t0 + s.n && ok; ++i, ++n) {
+#pragma unroll
+            for (int j = 0; j < 8; ++j) z[j] = next[j];
+            if (i + 1 < s.t0 + s.n) pages(i + 1, next);
+#pragma unroll
+            for (int v = 0; v < kPmVSlots; ++v) {
+              ok = ok && wait(&T->v_empty[v], (n & 1) ^ 1, 63);
+              if (!ok) break;
+              mbar_arrive_expect_tx(&T->v_full[v], kPmVBytes);
+              if (rows == 32) {
+                tma_load_4d(Vs + v * kPmVBytes, &vmap, &T->v_full[v], 0,
+                            (i * kPmKeys + v * 32) & mask, rank * 4, z[v]);
+              } else {
+#pragma unroll
+                for (int j = 0; j < 2; ++j)
+                  for (int blk = 0; blk < 4; ++blk)
+                    tma_load_4d(Vs + v * kPmVBytes + blk * 4096 + j * 2048, &vmap, &T->v_full[v],
+                                0, 0, rank * 4 + blk, z[2 * v + j]);
+              }
+            }
+          }
+        }
+        for (int v = 0; v < kPmVSlots && n; ++v)
+          if (ok) wait(&T->v_empty[v], (n & 1) ^ 1, 65);
+          else drain_slot(&T->v_full[v], n);
+      } else if (warp == 8 && elect_one()) {
+        // K slots to the matrix warp (in CTA 0).  The slots' own barriers stay in the CTA
+        // that issued the copies, so either CTA can wait for its own before it ends.
+        const uint32_t k_ready = in_cta(&T->k_ready[0], 0);
+        while (ok && pm_next(a, walk, s))
+          for (int i = 0; i < s.n && ok; ++i, ++n)
+            for (int k = 0; k < kPmKSlots && ok; ++k) {
+              ok = wait(&T->k_full[k], n & 1, 59);
+              if (ok) mbar_arrive_cluster(k_ready + k * 8);
+            }
+      } else if (warp == 9) {
+        // V slots to the matrix warp, after zeroing the rows behind k_len
+        const uint32_t v_ready = in_cta(&T->v_ready[0], 0);
+        while (ok && pm_next(a, walk, s)) {
+          for (int i = s.t0; i < s.t0 + s.n && ok; ++i, ++n) {
+            for (int v = 0; v < kPmVSlots; ++v) {
+              ok = wait(&T->v_full[v], n & 1, 60);
               ok = __all_sync(0xffffffffu, ok);
-              const int live = s.pair.kl - ((s.t0 + i) * kPmKeys + v * 32);
-              if (ok && live < 32) {
+              if (!ok) break;
+              const int live = s.pair.kl - (i * kPmKeys + v * 32);
+              if (live < 32) {
                 const int from = max(live, 0);
                 for (int u = lane; u < (32 - from) * 32; u += 32) {
                   const int r = from + (u >> 5), blk = (u >> 3) & 3, k = u & 7;
@@ -385,314 +540,259 @@ __global__ void __cluster_dims__(2, 1, 1)
                 fence_proxy_async_smem();
                 __syncwarp();
               }
-              if (ok && lane == 0) mbar_arrive_cluster(in_cta(&T->v_ready[v], 0));
+              if (lane == 0) mbar_arrive_cluster(v_ready + v * 8);
             }
-            ++vc;
           }
         }
-      }
-    }
-    // the last arrival from the MMAs has come before the CTA may end
-    if (ok && lane == 0 && qc) mbar_wait(&T->q_empty, (qc & 1) ^ 1, abort, a.status, 70);
-  } else if (warp >= 6) {
-    // --------------------------------------------------------------- loaders --
-    uint32_t kc = 0, vc = 0;                         // tiles of K and V so far
-    bool ok = true;
-    const int shift = a.c.page_shift;
-    if constexpr (!CODES) {
-      // one warp: the boxes of each slot, spread over its lanes
-      const int kb = min(1 << shift, 64), vb = min(1 << shift, 32);   // rows of a box
-      auto pages = [&](int tile) -> int {            // lane j: page of the tile's j-th run
-        const int key = tile * kPmKeys + (lane << shift);
-        int z = a.c.n_pages;                         // past the end: reads as zeros
-        if ((lane << shift) < kPmKeys && key < s.pair.kl) {
-          const int p = page_of(a.table + (int64_t)s.pair.b * a.max_pages, key, shift, a.c.n_pages);
-          if (p >= 0) z = p;
-          else set_status(a.status, DSA_ERR_INVALID, 61);
-        }
-        return z;
-      };
-      const int mask = (1 << shift) - 1;
-      auto load_k = [&](int tile) {
-        const int z0 = pages(tile);
-        const int o = 64 * rank + lane * kb;         // lane j < 64 / kb: box j
-        const int z = __shfl_sync(0xffffffffu, z0, (o >> shift) & 31);
-        const int row = (tile * kPmKeys + o) & mask;
-        for (int c = 0; c < kPmKSlots && ok; ++c) {
-          if (lane == 0) {
-            ok = mbar_wait(&T->k_empty[c], (kc & 1) ^ 1, abort, a.status, 62);
-            if (ok) mbar_arrive_expect_tx(&T->k_full[c], kPmKBytes);
-          }
-          ok = __shfl_sync(0xffffffffu, ok, 0);
-          if (ok && lane * kb < 64)
-            tma_load_3d(Ks + c * kPmKBytes + lane * kb * 128, &kmap, &T->k_full[c], c * 64, row, z);
-        }
-        ++kc;
-      };
-      auto load_v = [&](int tile) {
-        const int z0 = pages(tile);
-        const int per = 32 / vb;                     // boxes of a block
-        const int blk = lane / per, j = lane - blk * per;
-        for (int v = 0; v < kPmVSlots && ok; ++v) {
-          const int o = v * 32 + j * vb;
-          const int z = __shfl_sync(0xffffffffu, z0, (o >> shift) & 31);
-          if (lane == 0) {
-            ok = mbar_wait(&T->v_empty[v], (vc & 1) ^ 1, abort, a.status, 63);
-            if (ok) mbar_arrive_expect_tx(&T->v_full[v], kPmVBytes);
-          }
-          ok = __shfl_sync(0xffffffffu, ok, 0);
-          if (ok && blk < 4)
-            tma_load_3d(Vs + v * kPmVBytes + blk * 4096 + j * vb * 128, &vmap, &T->v_full[v],
-                        rank * 256 + blk * 64, (tile * kPmKeys + o) & mask, z);
-        }
-        ++vc;
-      };
-      while (ok && pm_next(a, walk, s)) {
-        load_k(s.t0);
-        for (int i = 0; i < s.n && ok; ++i) {
-          if (i + 1 < s.n) load_k(s.t0 + i + 1);
-          if (ok) load_v(s.t0 + i);
-        }
-      }
-      if (lane == 0) {
-        // the last copies have landed (also on the abort path), and the last arrivals
-        // from the MMAs have come, before the CTA may end
-        for (int c = 0; c < kPmKSlots && kc; ++c)
-          if (ok) mbar_wait(&T->k_empty[c], (kc & 1) ^ 1, abort, a.status, 64);
-          else mbar_wait_drain(&T->k_full[c], (kc & 1) ^ 1, kWaitCycles / 64);
-        for (int v = 0; v < kPmVSlots && vc; ++v)
-          if (ok) mbar_wait(&T->v_empty[v], (vc & 1) ^ 1, abort, a.status, 65);
-          else mbar_wait_drain(&T->v_full[v], (vc & 1) ^ 1, kWaitCycles / 64);
       }
     } else {
-      // eight warps: 16 codes a thread and load, converted on the way to the slots
-      const int c = threadIdx.x - 192;
-      const int krow = c >> 2, ku = c & 3;           // K chunk: row, run of 16 values
-      const int vrow = c >> 3, vu = c & 7;           // V slice: row, runs vu and vu + 8
-      uint4 kreg[8], rreg[2], vreg[8];
-      float ksc[4], vsc[8];
-      auto load_k = [&](int tile) {
-        const int key = tile * kPmKeys + 64 * rank + krow;
-        int page = -1;
-        if (key < s.pair.kl) {
-          page = page_of(a.table + (int64_t)s.pair.b * a.max_pages, key, shift, a.c.n_pages);
-          if (page < 0) set_status(a.status, DSA_ERR_INVALID, 61);
-        }
-        const int row = key & ((1 << shift) - 1);
-        const uint8_t* codes = a.c.codes + page * a.c.codes_ps + row * kPmDv + ku * 16;
-        const float* sc = a.c.scale + page * a.c.scale_ps + row * 4;
-        const __nv_bfloat16* raw = a.c.raw + page * a.c.raw_ps + row * 64 + ku * 16;
-#pragma unroll
-        for (int i = 0; i < 8; ++i)
-          kreg[i] = page >= 0 ? *reinterpret_cast<const uint4*>(codes + i * 64) : make_uint4(0, 0, 0, 0);
-#pragma unroll
-        for (int i = 0; i < 2; ++i)
-          rreg[i] = page >= 0 ? *reinterpret_cast<const uint4*>(raw + i * 8) : make_uint4(0, 0, 0, 0);
-#pragma unroll
-        for (int i = 0; i < 4; ++i) ksc[i] = page >= 0 ? sc[i] : 0.f;
+      // 16 codes a thread and load, converted on the way to the slots; a tile's loads are
+      // issued before the slots of the tile before it are waited for
+      auto page_at = [&](int key) -> int {
+        if (key >= s.pair.kl) return -1;             // reads as zeros
+        const int p = page_of(table, key, shift, a.c.n_pages);
+        if (p < 0) set_status(a.status, DSA_ERR_INVALID, 61);
+        return p;
       };
-      auto load_v = [&](int tile) {
-#pragma unroll
-        for (int v = 0; v < 4; ++v) {
-          const int key = tile * kPmKeys + v * 32 + vrow;
-          int page = -1;
-          if (key < s.pair.kl)
-            page = page_of(a.table + (int64_t)s.pair.b * a.max_pages, key, shift, a.c.n_pages);
-          const int row = key & ((1 << shift) - 1);
-          const uint8_t* codes = a.c.codes + page * a.c.codes_ps + row * kPmDv + rank * 256 + vu * 16;
-          const float* sc = a.c.scale + page * a.c.scale_ps + row * 4 + rank * 2;
-#pragma unroll
-          for (int h = 0; h < 2; ++h) {
-            vreg[2 * v + h] = page >= 0 ? *reinterpret_cast<const uint4*>(codes + h * 128)
-                                        : make_uint4(0, 0, 0, 0);
-            vsc[2 * v + h] = page >= 0 ? sc[h] : 0.f;
-          }
-        }
-      };
-      auto ready = [&](uint64_t* bar) {
+      auto ready = [&](uint32_t bar) {
         fence_proxy_async_smem();
         __syncwarp();
-        if (lane == 0) mbar_arrive_cluster(in_cta(bar, 0));
+        if (lane == 0) mbar_arrive_cluster(bar);
       };
-      auto fill_k = [&]() {
+      const uint4 zero = make_uint4(0, 0, 0, 0);
+      if (warp < 6 + kPmLoaders) {
+        // K: two threads a row, two runs of 16 values of each chunk
+        const int c = threadIdx.x - 192, krow = c >> 1, ku = (c & 1) * 2;
+        const uint32_t k_ready = in_cta(&T->k_ready[0], 0);
+        uint4 code[8][2], tail[4];
+        float scale[4];
+        auto load = [&](int tile) {
+          const int key = tile * kPmKeys + 64 * rank + krow;
+          const int page = page_at(key), row = key & mask;
+          const uint4* codes = reinterpret_cast<const uint4*>(a.c.codes + page * a.c.codes_ps +
+                                                              row * kPmDv) + ku;
+          const uint4* raw = reinterpret_cast<const uint4*>(a.c.raw + page * a.c.raw_ps + row * 64) +
+                             2 * ku;
+          const float* sc = a.c.scale + page * a.c.scale_ps + row * 4;
 #pragma unroll
-        for (int i = 0; i < kPmKSlots; ++i) {
-          if (ok) ok = mbar_wait(&T->k_empty[i], (kc & 1) ^ 1, abort, a.status, 62);
-          ok = __all_sync(0xffffffffu, ok);
-          if (!ok) break;
-          uint4 lo, hi;
-          if (i < 8) {
-            codes_to_bf16(kreg[i & 7], ksc[(i & 7) >> 1], lo, hi);
-          } else {
-            lo = rreg[0];
-            hi = rreg[1];
+          for (int i = 0; i < 8; ++i)
+#pragma unroll
+            for (int h = 0; h < 2; ++h) code[i][h] = page >= 0 ? codes[i * 4 + h] : zero;
+#pragma unroll
+          for (int i = 0; i < 4; ++i) {
+            tail[i] = page >= 0 ? raw[i] : zero;
+            scale[i] = page >= 0 ? sc[i] : 0.f;
           }
-          uint8_t* dst = Ks + i * kPmKBytes + krow * 128;
-          *reinterpret_cast<uint4*>(dst + (((2 * ku) ^ (krow & 7)) << 4)) = lo;
-          *reinterpret_cast<uint4*>(dst + (((2 * ku + 1) ^ (krow & 7)) << 4)) = hi;
-          ready(&T->k_ready[i]);
-        }
-        ++kc;
-      };
-      auto fill_v = [&]() {
+        };
+        while (ok && pm_next(a, walk, s)) {
+          table = a.table + (int64_t)s.pair.b * a.max_pages;
+          load(s.t0);
+          for (int i = 0; i < s.n && ok; ++i, ++n) {
 #pragma unroll
-        for (int v = 0; v < kPmVSlots; ++v) {
-          if (ok) ok = mbar_wait(&T->v_empty[v], (vc & 1) ^ 1, abort, a.status, 63);
-          ok = __all_sync(0xffffffffu, ok);
-          if (!ok) break;
+            for (int k = 0; k < kPmKSlots; ++k) {
+              ok = ok && wait(&T->k_empty[k], (n & 1) ^ 1, 62);
+              ok = __all_sync(0xffffffffu, ok);
+              if (!ok) break;
 #pragma unroll
-          for (int h = 0; h < 2; ++h) {
-            const int u = vu + 8 * h;                // 16 values of the CTA's 256
-            uint4 lo, hi;
-            codes_to_bf16(vreg[2 * v + h], vsc[2 * v + h], lo, hi);
-            uint8_t* dst = Vs + v * kPmVBytes + (u >> 2) * 4096 + vrow * 128;
-            const int k = 2 * (u & 3);
-            *reinterpret_cast<uint4*>(dst + ((k ^ (vrow & 7)) << 4)) = lo;
-            *reinterpret_cast<uint4*>(dst + (((k + 1) ^ (vrow & 7)) << 4)) = hi;
+              for (int j = 3 * k; j < 3 * k + 3; ++j) {
+                uint8_t* dst = Ks + j * kPmChunk + krow * 128;
+#pragma unroll
+                for (int h = 0; h < 2; ++h) {
+                  uint4 lo, hi;
+                  if (j < 8) {
+                    codes_to_bf16(code[j & 7][h], scale[(j & 7) >> 1], lo, hi);
+                  } else {
+                    lo = tail[2 * h];
+                    hi = tail[2 * h + 1];
+                  }
+                  const int u = 2 * (ku + h);
+                  *reinterpret_cast<uint4*>(dst + ((u ^ (krow & 7)) << 4)) = lo;
+                  *reinterpret_cast<uint4*>(dst + (((u + 1) ^ (krow & 7)) << 4)) = hi;
+                }
+              }
+              ready(k_ready + k * 8);
+            }
+            if (i + 1 < s.n) load(s.t0 + i + 1);
           }
-          ready(&T->v_ready[v]);
         }
-        ++vc;
-      };
-      while (ok && pm_next(a, walk, s)) {
-        load_k(s.t0);
-        for (int i = -1; i < s.n && ok; ++i) {
-          if (i >= 0) load_v(s.t0 + i);
-          if (i + 1 < s.n) fill_k();
-          if (i + 2 < s.n) load_k(s.t0 + i + 2);
-          if (i >= 0 && ok) fill_v();
+        if (ok && c == 0)
+          for (int k = 0; k < kPmKSlots && n; ++k)
+            mbar_wait(&T->k_empty[k], (n & 1) ^ 1, abort, a.status, 64);
+      } else {
+        // V: four threads a row, four runs of 16 of this CTA's 256 values
+        const int c = threadIdx.x - 192 - 32 * kPmLoaders, vrow = c >> 2, vu = c & 3;
+        const uint32_t v_ready = in_cta(&T->v_ready[0], 0);
+        uint4 code[4][4];
+        float scale[4][2];
+        auto load = [&](int tile) {
+#pragma unroll
+          for (int v = 0; v < kPmVSlots; ++v) {
+            const int key = tile * kPmKeys + v * 32 + vrow;
+            const int page = page_at(key), row = key & mask;
+            const uint4* codes = reinterpret_cast<const uint4*>(
+                                     a.c.codes + page * a.c.codes_ps + row * kPmDv + rank * 256) + vu;
+            const float* sc = a.c.scale + page * a.c.scale_ps + row * 4 + rank * 2;
+#pragma unroll
+            for (int h = 0; h < 4; ++h) code[v][h] = page >= 0 ? codes[4 * h] : zero;
+#pragma unroll
+            for (int h = 0; h < 2; ++h) scale[v][h] = page >= 0 ? sc[h] : 0.f;
+          }
+        };
+        while (ok && pm_next(a, walk, s)) {
+          table = a.table + (int64_t)s.pair.b * a.max_pages;
+          load(s.t0);
+          for (int i = 0; i < s.n && ok; ++i, ++n) {
+#pragma unroll
+            for (int v = 0; v < kPmVSlots; ++v) {
+              ok = ok && wait(&T->v_empty[v], (n & 1) ^ 1, 63);
+              ok = __all_sync(0xffffffffu, ok);
+              if (!ok) break;
+#pragma unroll
+              for (int h = 0; h < 4; ++h) {          // block of 64 values
+                uint4 lo, hi;
+                codes_to_bf16(code[v][h], scale[v][h >> 1], lo, hi);
+                uint8_t* dst = Vs + v * kPmVBytes + h * 4096 + vrow * 128;
+                *reinterpret_cast<uint4*>(dst + (((2 * vu) ^ (vrow & 7)) << 4)) = lo;
+                *reinterpret_cast<uint4*>(dst + (((2 * vu + 1) ^ (vrow & 7)) << 4)) = hi;
+              }
+              ready(v_ready + v * 8);
+            }
+            if (i + 1 < s.n) load(s.t0 + i + 1);
+          }
         }
-      }
-      if (ok && threadIdx.x == 192) {
-        for (int i = 0; i < kPmKSlots && kc; ++i)
-          mbar_wait(&T->k_empty[i], (kc & 1) ^ 1, abort, a.status, 64);
-        for (int v = 0; v < kPmVSlots && vc; ++v)
-          mbar_wait(&T->v_empty[v], (vc & 1) ^ 1, abort, a.status, 65);
+        if (ok && c == 0)
+          for (int v = 0; v < kPmVSlots && n; ++v)
+            mbar_wait(&T->v_empty[v], (n & 1) ^ 1, abort, a.status, 65);
       }
     }
   } else {
     // --------------------------------------------------- softmax and output --
     // Thread t of 128 = TMEM lane t: row t & 63 of this CTA, positions (or values) of
-    // half t >> 6.  Warps w and w + 2 hold the two halves of the same rows.
+    // half t >> 6.  Warps w and w + 2 hold the two halves of the same rows and exchange
+    // their maxima over a named barrier; a warp whose wait has run out goes on to meet its
+    // mate there (with nothing else to wait for), so neither is left behind.
+    // This is the longest chain of a tile, and it is short code on purpose: the roles of a
+    // CTA share its instruction cache, and unrolled masks and rescales made every role
+    // wait for instructions (42 % of all stalls; 4900 clocks a tile).
     const int t = threadIdx.x, half = t >> 6, row = t & 63;
     const uint32_t lane_off = (uint32_t)(warp * 32) << 16;
     const float inf = __int_as_float(0x7f800000);
     const uint32_t p_full = in_cta(&T->p_full, 0), o_empty = in_cta(&T->o_empty, 0);
-    const uint32_t s_empty[2] = {in_cta(&T->s_empty[0], 0), in_cta(&T->s_empty[1], 0)};
-    uint32_t sc = 0, xc = 0;                         // tiles, exchanges so far
+    const uint32_t s_empty = in_cta(&T->s_empty[0], 0);
+    uint32_t sc = 0;                                 // tiles so far
     bool ok = true;
-    // v of this thread and its mate (bounded, as every wait: the mate may have given up)
-    auto exchange = [&](float v) -> float {
-      T->peer[xc & 1][t] = v;
-      __syncwarp();
-      if (lane == 0) mbar_arrive(&T->mates[warp & 1]);
-      ok = mbar_wait(&T->mates[warp & 1], xc & 1, abort, a.status, 69);
-      ok = __all_sync(0xffffffffu, ok);
-      return T->peer[xc++ & 1][t ^ 64];
+    auto exchange = [&](float v, int at) -> float {
+      T->peer[at][t] = v;
+      named_bar_sync(1 + (warp & 1), 64);
+      return T->peer[at][t ^ 64];
     };
-    while (ok && pm_next(a, walk, s)) {
+    auto wait_all = [&](uint64_t* bar, uint32_t parity, int where) {
+      if (ok) ok = mbar_wait(bar, parity, abort, a.status, where);
+      ok = __all_sync(0xffffffffu, ok);
+    };
+    while (pm_next(a, walk, s)) {
       const int r = s.pair.row0 + rank * 64 + row;   // row of the sequence
       const bool mine = rank * 64 + row < s.pair.rows;
-      // positions this row sees: [0, lim)
-      const int lim = mine ? max(0, s.pair.kl - s.pair.ql + r / a.heads + 1) : 0;
+      // positions this row sees: [0, lim); rows past the last are not looked at again
+      const int lim = mine ? s.pair.kl - s.pair.ql + r / a.heads + 1 : 0x7fffffff;
       float m_run = -inf, l_run = 0.f;
+#pragma unroll 1
       for (int i = 0; i < s.n; ++i, ++sc) {
-        ok = mbar_wait(&T->s_full[sc & 1], (sc >> 1) & 1, abort, a.status, 66);
-        ok = __all_sync(0xffffffffu, ok);
-        if (!ok) break;
+        wait_all(&T->s_full[sc & 1], (sc >> 1) & 1, 66);
         tc_fence_after();
-        float x[64];
-        {
-          uint32_t sv[2][32];
-          const uint32_t at = tmem + lane_off + 256 + (sc & 1) * 64;
-          tmem_ld32(at, sv[0]);
-          tmem_ld32(at + 32, sv[1]);
-          tmem_ld_wait(sv[0]);
-          tmem_ld_wait(sv[1]);
+        const uint32_t at = tmem + lane_off + 256 + (sc & 1) * 64;
+        const int seen = lim - ((s.t0 + i) * kPmKeys + half * 64);   // of these 64
+        if (!__all_sync(0xffffffffu, seen >= 64)) {
+#pragma unroll 1
+          for (int c = 0; c < 64; c += 8) {
+            uint32_t v[8];
+            tmem_ld8(at + c, v);
 #pragma unroll
-          for (int j = 0; j < 64; ++j) x[j] = __uint_as_float(sv[j >> 5][j & 31]);
+            for (int j = 0; j < 8; ++j)
+              if (c + j >= seen) v[j] = 0xff800000u;
+            tmem_st8(at + c, v);
+          }
+          tmem_st_wait();
         }
+        uint32_t x[2][32];
+        tmem_ld32(at, x[0]);
+        tmem_ld32(at + 32, x[1]);
+        tmem_ld_wait(x[0]);
+        tmem_ld_wait(x[1]);
         tc_fence_before();
         __syncwarp();
-        if (lane == 0) mbar_arrive_cluster(s_empty[sc & 1]);
-        const int seen = lim - ((s.t0 + i) * kPmKeys + half * 64);   // of these 64
-        float mt = -inf;
-        if (__all_sync(0xffffffffu, seen >= 64)) {
+        if (lane == 0) mbar_arrive_cluster(s_empty + (sc & 1) * 8);
+        float top[4] = {-inf, -inf, -inf, -inf};
 #pragma unroll
-          for (int j = 0; j < 64; ++j) mt = fmaxf(mt, x[j] * a.scale_log2);
-        } else {
-#pragma unroll
-          for (int j = 0; j < 64; ++j) {
-            if (j >= seen) x[j] = -inf;
-            else mt = fmaxf(mt, x[j] * a.scale_log2);
-          }
-        }
-        mt = fmaxf(mt, exchange(mt));
-        if (!ok) break;
-        // P and O are free once the previous PV is complete
-        if (i > 0) {
-          ok = mbar_wait(&T->pv_done, (sc - 1) & 1, abort, a.status, 67);
-          ok = __all_sync(0xffffffffu, ok);
-          if (!ok) break;
-          tc_fence_after();
-        }
+        for (int j = 0; j < 64; ++j)
+          top[j & 3] = fmaxf(top[j & 3], __uint_as_float(x[j >> 5][j & 31]));
+        float mt = fmaxf(fmaxf(top[0], top[1]), fmaxf(top[2], top[3]));
+        mt = fmaxf(mt, exchange(mt, sc & 1)) * a.scale_log2;
         float f = 1.f;
-        if (mt > m_run + kPmLazy || (m_run == -inf && mt > -inf)) {
+        if (mt > m_run + kPmLazy) {
           if (m_run > -inf) {
             f = ex2(m_run - mt);
             l_run *= f;
           }
           m_run = mt;
         }
-        if (i > 0 && __any_sync(0xffffffffu, f != 1.f)) {
-          for (int c0 = 0; c0 < 256; c0 += 32) {
-            uint32_t ov[32];
-            tmem_ld32(tmem + lane_off + c0, ov);
-            tmem_ld_wait(ov);
-#pragma unroll
-            for (int j = 0; j < 32; ++j) ov[j] = __float_as_uint(__uint_as_float(ov[j]) * f);
-            tmem_st32(tmem + lane_off + c0, ov);
-          }
-          tmem_st_wait();
-        }
         // positions the row does not see weigh 0, also while its maximum is still -inf
-        const float m_sub = m_run == -inf ? 0.f : m_run;
-        uint8_t* prow = Ps + half * kPmKBytes + row * 128;
+        const float m_sub = m_run == -inf ? 0.f : -m_run;
+        const uint64_t scale2 = pack2(a.scale_log2, a.scale_log2), m2 = pack2(m_sub, m_sub);
+        uint64_t l2 = 0;
+        uint32_t w[32];
 #pragma unroll
-        for (int c = 0; c < 8; ++c) {
-          uint32_t w4[4];
-#pragma unroll
-          for (int u = 0; u < 4; ++u) {
-            const int j = c * 8 + u * 2;
-            const float p0 = ex2(fmaf(x[j], a.scale_log2, -m_sub));
-            const float p1 = ex2(fmaf(x[j + 1], a.scale_log2, -m_sub));
-            l_run += p0 + p1;
-            w4[u] = bf16x2(p0, p1);
-          }
-          *reinterpret_cast<uint4*>(prow + ((c ^ (row & 7)) << 4)) =
-              make_uint4(w4[0], w4[1], w4[2], w4[3]);
+        for (int j = 0; j < 32; ++j) {
+          const uint64_t e = fma2(pack2u(x[j >> 4][2 * (j & 15)], x[j >> 4][2 * (j & 15) + 1]),
+                                  scale2, m2);
+          const float p0 = ex2(lo2(e)), p1 = ex2(hi2(e));
+          l2 = add2(l2, pack2(p0, p1));
+          w[j] = bf16x2(p0, p1);
         }
+        l_run += lo2(l2) + hi2(l2);
+        // P and O are free once the previous PV is complete
+        if (i > 0) {
+          wait_all(&T->pv_done, (sc - 1) & 1, 67);
+          tc_fence_after();
+          if (__any_sync(0xffffffffu, f != 1.f)) {
+#pragma unroll 1
+            for (int c0 = 0; c0 < 256; c0 += 32) {
+              uint32_t ov[32];
+              tmem_ld32(tmem + lane_off + c0, ov);
+              tmem_ld_wait(ov);
+#pragma unroll
+              for (int j = 0; j < 32; ++j) ov[j] = __float_as_uint(__uint_as_float(ov[j]) * f);
+              tmem_st32(tmem + lane_off + c0, ov);
+            }
+            tmem_st_wait();
+          }
+        }
+        uint8_t* prow = Ps + half * kPmChunk + row * 128;
+#pragma unroll
+        for (int c = 0; c < 8; ++c)
+          *reinterpret_cast<uint4*>(prow + ((c ^ (row & 7)) << 4)) =
+              make_uint4(w[4 * c], w[4 * c + 1], w[4 * c + 2], w[4 * c + 3]);
         fence_proxy_async_smem();
         tc_fence_before();
         __syncwarp();
         if (lane == 0) mbar_arrive_cluster(p_full);
       }
-      if (!ok) break;
-      ok = mbar_wait(&T->pv_done, (sc - 1) & 1, abort, a.status, 68);
-      ok = __all_sync(0xffffffffu, ok);
-      if (!ok) break;
+      wait_all(&T->pv_done, (sc - 1) & 1, 68);
       tc_fence_after();
-      l_run += exchange(l_run);
-      if (!ok) break;
+      l_run += exchange(l_run, sc & 1);
+      named_bar_sync(1 + (warp & 1), 64);            // the next tile writes the same place
+      if (!ok) continue;
       const int64_t grow = (int64_t)s.pair.b * a.n_q * a.heads + r;
       const int64_t prow = (int64_t)s.slot * kPmRows + rank * 64 + row;
       if (mine && half == 0) {
         if (!s.whole) a.part_ml[prow] = make_float2(m_run, l_run);
         else if (a.lse)
           a.lse[grow] = l_run == 0.f ? -inf : (m_run + log2f(l_run)) * 0.6931471805599453f;
-        if (rank == 0 && row == 0 && s.t0 == 0) a.plan[1 + s.p] = cl * T->share + (T->count - walk.left - s.n);
+        if (rank == 0 && row == 0 && s.t0 == 0)
+          a.plan[1 + s.p] = cl * T->share + (T->count - walk.left - s.n);
       }
       const float inv = l_run == 0.f ? 0.f : 1.f / l_run;
+#pragma unroll 1
       for (int c0 = 0; c0 < 256; c0 += 32) {
         uint32_t ov[32];
         tmem_ld32(tmem + lane_off + c0, ov);

@@ -266,7 +266,7 @@ def test_write_of_values_at_the_ends(B, pow2):
     x[3, 7] = float("inf")
     x[4] = 1.0
     x[5, 0] = 2.0 ** -140
-    cache = B.PagedCache.empty(1, 8, 128, 0)
+    cache = B.PagedCache.empty(1, 16, 128, 0)
     B.cache_write(cache, x.cuda(), torch.arange(6, device="cuda"), pow2=pow2)
     y = B.cache_read(cache, torch.zeros(1, 1, dtype=torch.int32, device="cuda"), 6,
                      dtype=torch.float32)[0].cpu()

@@ -123,7 +123,7 @@ class Problem:
 CASES = [
     # k_lens, q_lens, n_q, heads, page: lengths of zero, one, around a tile and a page
     ([1], None, 1, 1, 64), ([0], None, 1, 16, 64), ([127, 128, 129, 0, 1], None, 1, 16, 64),
-    ([64, 63, 65, 300], None, 1, 128, 16), ([1000], None, 1, 128, 64), ([5000], None, 1, 128, 8),
+    ([64, 63, 65, 300], None, 1, 128, 16), ([1000], None, 1, 128, 64), ([5000], None, 1, 128, 16),
     ([700, 31], None, 1, 64, 32), ([900, 2], None, 1, 20, 128), ([900, 333], None, 1, 65, 256),
     ([4096, 17], None, 1, 7, 4096),
     # a few tokens, some of them before the first cached position

@@ -115,7 +115,7 @@ def cache(B, **kw):
 
 BAD_CACHES = [
     (dict(n_pages=0), -1), (dict(dim_q=-128), -1), (dict(dim_raw=-8), -1),
-    (dict(dim_q=0, dim_raw=0, codes=None, scale=None, raw=None), -1), (dict(page_size=4), -2),
+    (dict(dim_q=0, dim_raw=0, codes=None, scale=None, raw=None), -1), (dict(page_size=8), -2),
     (dict(page_size=48), -2), (dict(page_size=8192), -2), (dict(page_size=0), -2),
     (dict(dim_q=100), -2), (dict(dim_raw=60), -2), (dict(dim_q=8192), -2), (dict(codes=None), -1),
     (dict(scale=None), -1), (dict(raw=None), -1), (dict(codes=FAKE + 8), -1),
