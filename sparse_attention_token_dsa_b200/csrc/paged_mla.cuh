@@ -120,8 +120,11 @@ struct PmSegment {
   bool whole;
 };
 
-// The next run of tiles of one pair in a cluster's share.
-__device__ __forceinline__ bool pm_next(const PagedMlaArgs& a, PmWalk& w, PmSegment& s) {
+// The next run of tiles of one pair in a cluster's share (out of line: every role calls it,
+// and only between its loops).
+__device__ __noinline__ bool pm_next_far(const PagedMlaArgs& a, PmWalk* walk, PmSegment* seg) {
+  PmWalk w = *walk;
+  PmSegment s;
   if (w.left <= 0) return false;
   while (w.p < a.pairs) {
     s.pair = pm_pair(a, w.p);
@@ -141,7 +144,21 @@ __device__ __forceinline__ bool pm_next(const PagedMlaArgs& a, PmWalk& w, PmSegm
     w.off = 0;
     ++w.p;
   }
+  *walk = w;
+  *seg = s;
   return true;
+}
+
+// The same with the segment in a variable whose address nobody has.
+__device__ __forceinline__ bool pm_next(const PagedMlaArgs& a, PmWalk& w, PmSegment& s) {
+  PmWalk w1 = w;
+  PmSegment s1;
+  const bool more = pm_next_far(a, &w1, &s1);
+  if (more) {
+    w = w1;
+    s = s1;
+  }
+  return more;
 }
 
 __device__ __forceinline__ float ex2(float x) {
@@ -312,12 +329,12 @@ __global__ void __cluster_dims__(2, 1, 1)
   PmSegment s;
 
   auto wait = [&](uint64_t* bar, uint32_t parity, int where) -> bool {
-    return mbar_wait(bar, parity, abort, a.status, where);
+    return mbar_wait_far(bar, parity, abort, a.status, where);
   };
   // The result of `wait`, asked for earlier: a slot's barrier is looked at before the
   // matrix instructions of the slot before it are issued.
   auto wait_seen = [&](bool seen, uint64_t* bar, uint32_t parity, int where) -> bool {
-    return seen || mbar_wait(bar, parity, abort, a.status, where);
+    return seen || mbar_poll(bar, parity, abort, a.status, where);
   };
 
   // The roles of warps 4 and up (but for the conversion of codes) run in one lane.
@@ -350,17 +367,18 @@ __global__ void __cluster_dims__(2, 1, 1)
             if (!ok) break;
             tc_fence_after();
             const uint32_t d = tmem + 256 + b * 64;
-#pragma unroll
+#pragma unroll 1
             for (int k = 0; k < kPmKSlots; ++k) {
               ok = ok && wait_seen(seen, &T->k_ready[k], sc & 1, 52);
               if (!ok) break;
               if (k + 1 < kPmKSlots) seen = mbar_try_wait(&T->k_ready[k + 1], sc & 1);
 #pragma unroll
-              for (int c = 3 * k; c < 3 * k + 3; ++c)
+              for (int c = 0; c < 3; ++c)
 #pragma unroll
-                for (int kk = 0; kk < 4; ++kk)       // 16 values
-                  pair_mma_bf16(d, q_desc + ((c * kPmChunk + kk * 32) >> 4),
-                                k_desc + ((c * kPmChunk + kk * 32) >> 4), idesc, (c | kk) != 0);
+                for (int kk = 0; kk < 4; ++kk) {     // 16 values
+                  const uint32_t at = (k * kPmKBytes + c * kPmChunk + kk * 32) >> 4;
+                  pair_mma_bf16(d, q_desc + at, k_desc + at, idesc, (k | c | kk) != 0);
+                }
               pair_commit(&T->k_empty[k]);
             }
             if (!ok) break;
@@ -392,7 +410,7 @@ __global__ void __cluster_dims__(2, 1, 1)
           if (!ok) break;
           bool seen = mbar_try_wait(&T->v_ready[0], pc & 1);
           tc_fence_after();
-#pragma unroll
+#pragma unroll 1
           for (int v = 0; v < kPmVSlots; ++v) {
             ok = ok && wait_seen(seen, &T->v_ready[v], pc & 1, 56);
             if (!ok) break;
@@ -437,34 +455,29 @@ __global__ void __cluster_dims__(2, 1, 1)
       };
       if (warp == 6 && elect_one()) {
         const int rows = min(1 << shift, 64);        // of a copy
-        const int first = 64 * rank;
-        int z[4], next[4];                           // pages of a tile's copies
-        auto pages = [&](int tile, int (&to)[4]) {
-#pragma unroll
-          for (int j = 0; j < 4; ++j)
-            if (j * rows < 64) to[j] = page_at(tile * kPmKeys + first + j * rows);
-        };
         while (ok && pm_next(a, walk, s)) {
           table = a.table + (int64_t)s.pair.b * a.max_pages;
-          pages(s.t0, next);
+#pragma unroll 1
           for (int i = s.t0; i < s.t0 + s.n && ok; ++i, ++n) {
-#pragma unroll
-            for (int j = 0; j < 4; ++j) z[j] = next[j];
-            if (i + 1 < s.t0 + s.n) pages(i + 1, next);
-            const int row = (i * kPmKeys + first) & mask;
+            const int key = i * kPmKeys + 64 * rank;
+            const int page = page_at(key);
+#pragma unroll 1
             for (int k = 0; k < kPmKSlots; ++k) {
               ok = wait(&T->k_empty[k], (n & 1) ^ 1, 62);
               if (!ok) break;
               mbar_arrive_expect_tx(&T->k_full[k], kPmKBytes);
+              uint8_t* dst = Ks + k * kPmKBytes;
               if (rows == 64) {
-                tma_load_4d(Ks + k * kPmKBytes, &kmap, &T->k_full[k], 0, row, 3 * k, z[0]);
+                tma_load_4d(dst, &kmap, &T->k_full[k], 0, key & mask, 3 * k, page);
               } else {                               // chunk by chunk, pages below one another
-                for (int c = 0; c < 3; ++c)
-#pragma unroll
-                  for (int j = 0; j < 4; ++j)
-                    if (j * rows < 64)
-                      tma_load_4d(Ks + k * kPmKBytes + c * kPmChunk + j * rows * 128, &kmap,
-                                  &T->k_full[k], 0, 0, 3 * k + c, z[j]);
+#pragma unroll 1
+                for (int j = 0; j < 64; j += rows) {
+                  const int z = page_at(key + j);
+#pragma unroll 1
+                  for (int c = 0; c < 3; ++c)
+                    tma_load_4d(dst + c * kPmChunk + j * 128, &kmap, &T->k_full[k], 0, 0,
+                                3 * k + c, z);
+                }
               }
             }
           }
@@ -476,33 +489,29 @@ __global__ void __cluster_dims__(2, 1, 1)
           else drain_slot(&T->k_full[k], n);
       } else if (warp == 7 && elect_one()) {
         const int rows = min(1 << shift, 32);
-        int z[8], next[8];
-        auto pages = [&](int tile, int (&to)[8]) {
-#pragma unroll
-          for (int j = 0; j < 8; ++j)
-            if (j * rows < kPmKeys) to[j] = page_at(tile * kPmKeys + j * rows);
-        };
         while (ok && pm_next(a, walk, s)) {
           table = a.table + (int64_t)s.pair.b * a.max_pages;
-          pages(s.t0, next);
+#pragma unroll 1
           for (int i = s.t0; i < s.t0 + s.n && ok; ++i, ++n) {
-#pragma unroll
-            for (int j = 0; j < 8; ++j) z[j] = next[j];
-            if (i + 1 < s.t0 + s.n) pages(i + 1, next);
-#pragma unroll
+#pragma unroll 1
             for (int v = 0; v < kPmVSlots; ++v) {
-              ok = ok && wait(&T->v_empty[v], (n & 1) ^ 1, 63);
+              const int key = i * kPmKeys + v * 32;
+              const int page = page_at(key);
+              ok = wait(&T->v_empty[v], (n & 1) ^ 1, 63);
               if (!ok) break;
               mbar_arrive_expect_tx(&T->v_full[v], kPmVBytes);
+              uint8_t* dst = Vs + v * kPmVBytes;
               if (rows == 32) {
-                tma_load_4d(Vs + v * kPmVBytes, &vmap, &T->v_full[v], 0,
-                            (i * kPmKeys + v * 32) & mask, rank * 4, z[v]);
+                tma_load_4d(dst, &vmap, &T->v_full[v], 0, key & mask, rank * 4, page);
               } else {
-#pragma unroll
-                for (int j = 0; j < 2; ++j)
-                  for (int blk = 0; blk < 4; ++blk)
-                    tma_load_4d(Vs + v * kPmVBytes + blk * 4096 + j * 2048, &vmap, &T->v_full[v],
-                                0, 0, rank * 4 + blk, z[2 * v + j]);
+#pragma unroll 1
+                for (int j = 0; j < 32; j += rows) {
+                  const int z = page_at(key + j);
+#pragma unroll 1
+                  for (int c = 0; c < 4; ++c)
+                    tma_load_4d(dst + c * 4096 + j * 128, &vmap, &T->v_full[v], 0, 0, rank * 4 + c,
+                                z);
+                }
               }
             }
           }
@@ -687,7 +696,7 @@ __global__ void __cluster_dims__(2, 1, 1)
       return T->peer[at][t ^ 64];
     };
     auto wait_all = [&](uint64_t* bar, uint32_t parity, int where) {
-      if (ok) ok = mbar_wait(bar, parity, abort, a.status, where);
+      if (ok) ok = mbar_wait_far(bar, parity, abort, a.status, where);
       ok = __all_sync(0xffffffffu, ok);
     };
     while (pm_next(a, walk, s)) {

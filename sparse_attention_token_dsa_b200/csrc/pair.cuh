@@ -32,6 +32,17 @@ __device__ __forceinline__ void mbar_arrive_cluster(uint32_t bar) {
                : "memory");
 }
 
+// As mbar_wait, with the polling out of line: a kernel with a role for every warp has
+// dozens of waits, and inlined polls pushed its loops out of the instruction cache.
+__device__ __noinline__ bool mbar_poll(uint64_t* bar, uint32_t parity, volatile int* abort,
+                                       int32_t* status, int where) {
+  return mbar_wait(bar, parity, abort, status, where);
+}
+__device__ __forceinline__ bool mbar_wait_far(uint64_t* bar, uint32_t parity, volatile int* abort,
+                                              int32_t* status, int where) {
+  return mbar_try_wait(bar, parity) || mbar_poll(bar, parity, abort, status, where);
+}
+
 // ------------------------------------------------------------ cta_group::2 --
 __device__ __forceinline__ void pair_tmem_alloc(uint32_t* dst_smem, uint32_t ncols) {
   asm volatile("tcgen05.alloc.cta_group::2.sync.aligned.shared::cta.b32 [%0], %1;" ::"r"(
