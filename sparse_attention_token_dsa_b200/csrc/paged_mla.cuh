@@ -206,16 +206,48 @@ __device__ __forceinline__ void tmem_st8(uint32_t taddr, const uint32_t (&r)[8])
       : "memory");
 }
 
-// 16 e4m3 codes times a scale as bf16 (exact where the scale is a power of two).
-__device__ __forceinline__ void codes_to_bf16(const uint4& w, float s, uint4& lo, uint4& hi) {
+// 16 e4m3 codes times a scale as bf16.  A code's exponent and mantissa, moved to where
+// bf16 has its own, are the value times 2^-120 (also for e4m3's subnormal codes, which
+// become bf16's), so one packed product with 2^120 scale gives two values, exactly, where
+// the scale is a power of two of at most 2^7: five instructions for two codes and none of
+// them a conversion (those run at a quarter of the rate).
+__device__ __forceinline__ uint32_t two_codes(uint32_t w, uint32_t sel, uint32_t mul) {
+  const uint32_t t = __byte_perm(w, 0, sel);         // a code in the upper byte of each half
+  const uint32_t v = ((t >> 4) & 0x07f007f0u) | (t & 0x80008000u);
+  uint32_t r;
+  asm("mul.rn.bf16x2 %0, %1, %2;" : "=r"(r) : "r"(v), "r"(mul));
+  return r;
+}
+__device__ __forceinline__ void codes_to_bf16(const uint4& w, uint32_t mul, uint4& lo, uint4& hi) {
+  lo = make_uint4(two_codes(w.x, 0x1404, mul), two_codes(w.x, 0x3424, mul),
+                  two_codes(w.y, 0x1404, mul), two_codes(w.y, 0x3424, mul));
+  hi = make_uint4(two_codes(w.z, 0x1404, mul), two_codes(w.z, 0x3424, mul),
+                  two_codes(w.w, 0x1404, mul), two_codes(w.w, 0x3424, mul));
+}
+// 2^120 scale in both halves; 0 where the short way does not hold.
+__device__ __forceinline__ uint32_t code_factor(float scale) {
+  const uint32_t u = __float_as_uint(scale);
+  if ((u & 0x807fffffu) != 0u || u < 0x00800000u || scale > 128.f) return 0u;
+  const uint32_t h = (u >> 16) + (120u << 7);
+  return h | (h << 16);
+}
+// Any scale: in fp32, rounded to bf16 once.
+__device__ __noinline__ void codes_to_bf16_any(const uint4* w, float scale, uint4* lo, uint4* hi) {
   float v[16];
-  e4m3x4_values(w.x, s, v);
-  e4m3x4_values(w.y, s, v + 4);
-  e4m3x4_values(w.z, s, v + 8);
-  e4m3x4_values(w.w, s, v + 12);
-  lo = make_uint4(bf16x2(v[0], v[1]), bf16x2(v[2], v[3]), bf16x2(v[4], v[5]), bf16x2(v[6], v[7]));
-  hi = make_uint4(bf16x2(v[8], v[9]), bf16x2(v[10], v[11]), bf16x2(v[12], v[13]),
-                  bf16x2(v[14], v[15]));
+  e4m3x4_values(w->x, scale, v);
+  e4m3x4_values(w->y, scale, v + 4);
+  e4m3x4_values(w->z, scale, v + 8);
+  e4m3x4_values(w->w, scale, v + 12);
+  *lo = make_uint4(bf16x2(v[0], v[1]), bf16x2(v[2], v[3]), bf16x2(v[4], v[5]), bf16x2(v[6], v[7]));
+  *hi = make_uint4(bf16x2(v[8], v[9]), bf16x2(v[10], v[11]), bf16x2(v[12], v[13]),
+                   bf16x2(v[14], v[15]));
+}
+__device__ __forceinline__ void codes_to_bf16_far(const uint4& w, float scale, uint4& lo, uint4& hi) {
+  const uint4 w1 = w;
+  uint4 a, b;
+  codes_to_bf16_any(&w1, scale, &a, &b);
+  lo = a;
+  hi = b;
 }
 
 __device__ __forceinline__ void tma_load_4d(void* dst, const CUtensorMap* map, uint64_t* bar,
@@ -555,8 +587,8 @@ __global__ void __cluster_dims__(2, 1, 1)
         }
       }
     } else {
-      // 16 codes a thread and load, converted on the way to the slots; a tile's loads are
-      // issued before the slots of the tile before it are waited for
+      // 16 codes a thread and load, converted on the way to the slots; a slot's loads are
+      // issued before the slot ahead of it is converted
       auto page_at = [&](int key) -> int {
         if (key >= s.pair.kl) return -1;             // reads as zeros
         const int p = page_of(table, key, shift, a.c.n_pages);
@@ -570,108 +602,157 @@ __global__ void __cluster_dims__(2, 1, 1)
       };
       const uint4 zero = make_uint4(0, 0, 0, 0);
       if (warp < 6 + kPmLoaders) {
-        // K: two threads a row, two runs of 16 values of each chunk
+        // K: two threads a row, two runs of 16 values of each of a slot's three chunks; the
+        // last chunk of the last slot is the bf16 part
         const int c = threadIdx.x - 192, krow = c >> 1, ku = (c & 1) * 2;
         const uint32_t k_ready = in_cta(&T->k_ready[0], 0);
-        uint4 code[8][2], tail[4];
-        float scale[4];
-        auto load = [&](int tile) {
-          const int key = tile * kPmKeys + 64 * rank + krow;
-          const int page = page_at(key), row = key & mask;
+        int page = -1, row = 0;
+        uint4 next[6], now[6], tail[4];
+        float scale[4], next_scale[4] = {0.f, 0.f, 0.f, 0.f};
+        auto fetch = [&](int tile, int k) {
+          if (k == 0) {
+            const int key = tile * kPmKeys + 64 * rank + krow;
+            page = page_at(key);
+            row = key & mask;
+            const float* sc = a.c.scale + page * a.c.scale_ps + row * 4;
+#pragma unroll
+            for (int i = 0; i < 4; ++i) next_scale[i] = page >= 0 ? sc[i] : 1.f;
+          }
           const uint4* codes = reinterpret_cast<const uint4*>(a.c.codes + page * a.c.codes_ps +
-                                                              row * kPmDv) + ku;
-          const uint4* raw = reinterpret_cast<const uint4*>(a.c.raw + page * a.c.raw_ps + row * 64) +
-                             2 * ku;
-          const float* sc = a.c.scale + page * a.c.scale_ps + row * 4;
+                                                              row * kPmDv) + 12 * k + ku;
 #pragma unroll
-          for (int i = 0; i < 8; ++i)
+          for (int j = 0; j < 3; ++j)
 #pragma unroll
-            for (int h = 0; h < 2; ++h) code[i][h] = page >= 0 ? codes[i * 4 + h] : zero;
+            for (int h = 0; h < 2; ++h)
+              next[2 * j + h] = page >= 0 && (k < 2 || j < 2) ? codes[4 * j + h] : zero;
+          if (k == 2) {
+            const uint4* raw = reinterpret_cast<const uint4*>(a.c.raw + page * a.c.raw_ps +
+                                                              row * 64) + 2 * ku;
 #pragma unroll
-          for (int i = 0; i < 4; ++i) {
-            tail[i] = page >= 0 ? raw[i] : zero;
-            scale[i] = page >= 0 ? sc[i] : 0.f;
+            for (int i = 0; i < 4; ++i) tail[i] = page >= 0 ? raw[i] : zero;
           }
         };
         while (ok && pm_next(a, walk, s)) {
           table = a.table + (int64_t)s.pair.b * a.max_pages;
-          load(s.t0);
+          fetch(s.t0, 0);
+#pragma unroll 1
           for (int i = 0; i < s.n && ok; ++i, ++n) {
 #pragma unroll
+            for (int j = 0; j < 4; ++j) scale[j] = next_scale[j];
+#pragma unroll 1
             for (int k = 0; k < kPmKSlots; ++k) {
+#pragma unroll
+              for (int j = 0; j < 6; ++j) now[j] = next[j];
+              // a slot's chunks 3k .. 3k + 2 lie in groups (3k) / 2 .. (3k + 2) / 2
+              const float s0 = k == 0 ? scale[0] : (k == 1 ? scale[1] : scale[3]);
+              const float s1 = k == 0 ? scale[0] : (k == 1 ? scale[2] : scale[3]);
+              const float s2 = k == 0 ? scale[1] : scale[2];
+              const uint4 t0 = tail[0], t1 = tail[1], t2 = tail[2], t3 = tail[3];
+              if (k + 1 < kPmKSlots) fetch(s.t0 + i, k + 1);
+              else if (i + 1 < s.n) fetch(s.t0 + i + 1, 0);
               ok = ok && wait(&T->k_empty[k], (n & 1) ^ 1, 62);
               ok = __all_sync(0xffffffffu, ok);
               if (!ok) break;
+              const uint32_t f[3] = {code_factor(s0), code_factor(s1), code_factor(s2)};
+              const bool fast = __all_sync(0xffffffffu, f[0] && f[1] && f[2]);
+              uint8_t* dst = Ks + k * kPmKBytes + krow * 128;
+              auto put = [&](int j, int h, const uint4& lo, const uint4& hi) {
+                const int u = 2 * (ku + h);
+                *reinterpret_cast<uint4*>(dst + j * kPmChunk + ((u ^ (krow & 7)) << 4)) = lo;
+                *reinterpret_cast<uint4*>(dst + j * kPmChunk + (((u + 1) ^ (krow & 7)) << 4)) = hi;
+              };
+              if (fast) {
 #pragma unroll
-              for (int j = 3 * k; j < 3 * k + 3; ++j) {
-                uint8_t* dst = Ks + j * kPmChunk + krow * 128;
+                for (int j = 0; j < 3; ++j)
 #pragma unroll
-                for (int h = 0; h < 2; ++h) {
-                  uint4 lo, hi;
-                  if (j < 8) {
-                    codes_to_bf16(code[j & 7][h], scale[(j & 7) >> 1], lo, hi);
-                  } else {
-                    lo = tail[2 * h];
-                    hi = tail[2 * h + 1];
+                  for (int h = 0; h < 2; ++h) {
+                    uint4 lo, hi;
+                    codes_to_bf16(now[2 * j + h], f[j], lo, hi);
+                    put(j, h, lo, hi);
                   }
-                  const int u = 2 * (ku + h);
-                  *reinterpret_cast<uint4*>(dst + ((u ^ (krow & 7)) << 4)) = lo;
-                  *reinterpret_cast<uint4*>(dst + (((u + 1) ^ (krow & 7)) << 4)) = hi;
-                }
+              } else {
+                const float sj[3] = {s0, s1, s2};
+#pragma unroll
+                for (int j = 0; j < 3; ++j)
+#pragma unroll
+                  for (int h = 0; h < 2; ++h) {
+                    uint4 lo, hi;
+                    codes_to_bf16_far(now[2 * j + h], sj[j], lo, hi);
+                    put(j, h, lo, hi);
+                  }
+              }
+              if (k == 2) {
+                put(2, 0, t0, t1);
+                put(2, 1, t2, t3);
               }
               ready(k_ready + k * 8);
             }
-            if (i + 1 < s.n) load(s.t0 + i + 1);
           }
         }
         if (ok && c == 0)
           for (int k = 0; k < kPmKSlots && n; ++k)
-            mbar_wait(&T->k_empty[k], (n & 1) ^ 1, abort, a.status, 64);
+            wait(&T->k_empty[k], (n & 1) ^ 1, 64);
       } else {
         // V: four threads a row, four runs of 16 of this CTA's 256 values
         const int c = threadIdx.x - 192 - 32 * kPmLoaders, vrow = c >> 2, vu = c & 3;
         const uint32_t v_ready = in_cta(&T->v_ready[0], 0);
-        uint4 code[4][4];
-        float scale[4][2];
-        auto load = [&](int tile) {
+        uint4 next[4], now[4];
+        float next_scale[2];
+        auto fetch = [&](int tile, int v) {
+          const int key = tile * kPmKeys + v * 32 + vrow;
+          const int page = page_at(key), row = key & mask;
+          const uint4* codes = reinterpret_cast<const uint4*>(
+                                   a.c.codes + page * a.c.codes_ps + row * kPmDv + rank * 256) + vu;
+          const float* sc = a.c.scale + page * a.c.scale_ps + row * 4 + rank * 2;
 #pragma unroll
-          for (int v = 0; v < kPmVSlots; ++v) {
-            const int key = tile * kPmKeys + v * 32 + vrow;
-            const int page = page_at(key), row = key & mask;
-            const uint4* codes = reinterpret_cast<const uint4*>(
-                                     a.c.codes + page * a.c.codes_ps + row * kPmDv + rank * 256) + vu;
-            const float* sc = a.c.scale + page * a.c.scale_ps + row * 4 + rank * 2;
+          for (int h = 0; h < 4; ++h) next[h] = page >= 0 ? codes[4 * h] : zero;
 #pragma unroll
-            for (int h = 0; h < 4; ++h) code[v][h] = page >= 0 ? codes[4 * h] : zero;
-#pragma unroll
-            for (int h = 0; h < 2; ++h) scale[v][h] = page >= 0 ? sc[h] : 0.f;
-          }
+          for (int h = 0; h < 2; ++h) next_scale[h] = page >= 0 ? sc[h] : 1.f;
         };
         while (ok && pm_next(a, walk, s)) {
           table = a.table + (int64_t)s.pair.b * a.max_pages;
-          load(s.t0);
+          fetch(s.t0, 0);
+#pragma unroll 1
           for (int i = 0; i < s.n && ok; ++i, ++n) {
-#pragma unroll
+#pragma unroll 1
             for (int v = 0; v < kPmVSlots; ++v) {
+#pragma unroll
+              for (int h = 0; h < 4; ++h) now[h] = next[h];
+              const float sc[2] = {next_scale[0], next_scale[1]};
+              if (v + 1 < kPmVSlots) fetch(s.t0 + i, v + 1);
+              else if (i + 1 < s.n) fetch(s.t0 + i + 1, 0);
               ok = ok && wait(&T->v_empty[v], (n & 1) ^ 1, 63);
               ok = __all_sync(0xffffffffu, ok);
               if (!ok) break;
+              const uint32_t f[2] = {code_factor(sc[0]), code_factor(sc[1])};
+              const bool fast = __all_sync(0xffffffffu, f[0] && f[1]);
+              uint8_t* dst = Vs + v * kPmVBytes + vrow * 128;
+              auto put = [&](int h, const uint4& lo, const uint4& hi) {   // block of 64 values
+                *reinterpret_cast<uint4*>(dst + h * 4096 + (((2 * vu) ^ (vrow & 7)) << 4)) = lo;
+                *reinterpret_cast<uint4*>(dst + h * 4096 + (((2 * vu + 1) ^ (vrow & 7)) << 4)) = hi;
+              };
+              if (fast) {
 #pragma unroll
-              for (int h = 0; h < 4; ++h) {          // block of 64 values
-                uint4 lo, hi;
-                codes_to_bf16(code[v][h], scale[v][h >> 1], lo, hi);
-                uint8_t* dst = Vs + v * kPmVBytes + h * 4096 + vrow * 128;
-                *reinterpret_cast<uint4*>(dst + (((2 * vu) ^ (vrow & 7)) << 4)) = lo;
-                *reinterpret_cast<uint4*>(dst + (((2 * vu + 1) ^ (vrow & 7)) << 4)) = hi;
+                for (int h = 0; h < 4; ++h) {
+                  uint4 lo, hi;
+                  codes_to_bf16(now[h], f[h >> 1], lo, hi);
+                  put(h, lo, hi);
+                }
+              } else {
+#pragma unroll
+                for (int h = 0; h < 4; ++h) {
+                  uint4 lo, hi;
+                  codes_to_bf16_far(now[h], sc[h >> 1], lo, hi);
+                  put(h, lo, hi);
+                }
               }
               ready(v_ready + v * 8);
             }
-            if (i + 1 < s.n) load(s.t0 + i + 1);
           }
         }
         if (ok && c == 0)
           for (int v = 0; v < kPmVSlots && n; ++v)
-            mbar_wait(&T->v_empty[v], (n & 1) ^ 1, abort, a.status, 65);
+            wait(&T->v_empty[v], (n & 1) ^ 1, 65);
       }
     }
   } else {

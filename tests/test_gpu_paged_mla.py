@@ -194,6 +194,25 @@ def test_closed_forms(B):
     assert bool(((lse[1].double() - torch.log(torch.tensor(96.0).double())).abs() <= 1e-5).all())
 
 
+@pytest.mark.parametrize("power", [-126, -20, 0, 7, 8, 40])
+def test_every_code_and_scale_exactly(B, power):
+    """One position whose row holds every finite e4m3 code, subnormals among them, with
+    scales from the smallest to large ones: the output is its value, bit for bit (at 2^-126
+    the nearest bf16 to it: bf16 ends at 2^-133, the smallest code's value is 2^-135)."""
+    bits = torch.arange(256, dtype=torch.uint8)
+    bits[0x7f], bits[0xff] = 0x7e, 0xfe
+    codes = torch.zeros(1, 16, 512, dtype=torch.uint8)
+    codes[0, 0] = torch.cat((bits, bits.flip(0)))
+    codes = codes.cuda().view(torch.float8_e4m3fn)
+    scale = torch.full((1, 16, 4), 2.0 ** power, device="cuda")
+    cache = B.PagedCache(codes, scale, torch.zeros(1, 16, 64, dtype=torch.bfloat16, device="cuda"))
+    q = torch.zeros(1, 1, 16, 576, dtype=torch.bfloat16, device="cuda")
+    out, lse = B.paged_mla(q, cache, torch.zeros(1, 1, dtype=torch.int32, device="cuda"),
+                           torch.ones(1, dtype=torch.int32, device="cuda"), 1.0)
+    want = (codes[0, 0].float() * 2.0 ** power).bfloat16().float()
+    assert torch.equal(out[0, 0].float(), want.expand(16, 512)) and bool((lse == 0).all())
+
+
 def test_no_lse_and_clamped_lengths(B):
     """out_lse is optional at the C entry; lengths outside their range are clamped."""
     p = Problem(B, 11, [128, 100], None, 2, 16, 64, "bf16")
