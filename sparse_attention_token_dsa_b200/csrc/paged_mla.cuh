@@ -40,18 +40,25 @@ constexpr int kPmDqk = 576;
 constexpr int kPmDv = 512;
 constexpr int kPmRows = 128;            // rows of a tile (64 a CTA)
 constexpr int kPmKeys = 128;            // positions of a tile
-constexpr int kPmKSlots = 3;            // K runs of 3 chunks of 64 values: one tile
-constexpr int kPmVSlots = 4;            // V slices of 32 positions: one tile
-constexpr int kPmChunk = 64 * 128;      // 64 positions (or rows) x 64 values
-constexpr int kPmKBytes = 3 * kPmChunk;
-constexpr int kPmVBytes = 4 * 32 * 128;
+constexpr int kPmChunk = 64 * 128;      // 64 positions (or rows) x 64 values in bf16
+constexpr int kPmSlice = 4 * 32 * 128;  // 32 positions x 256 values
+// Rings of operand slots: bf16 rows are copied into them, a tile's worth; e4m3 rows are
+// copied as they are (a tile of codes of K and one of V) and converted into shorter rings.
+template <bool CODES>
+struct PmRing {
+  static constexpr int kKSlots = CODES ? 5 : 3;      // of K
+  static constexpr int kChunks = CODES ? 1 : 3;      // in a slot of K
+  static constexpr int kVSlots = CODES ? 2 : 4;      // slices of V
+  static constexpr int kKBytes = kChunks * kPmChunk;
+  static constexpr int kCodes = CODES ? 4 * 8192 : 0;   // of K, and of V
+};
 constexpr int kPmQBytes = 9 * 64 * 128;
 constexpr int kPmPBytes = 2 * 64 * 128;
 constexpr int kPmClusters = 74;         // one CTA an SM
 constexpr float kPmLazy = 8.f;          // log2 headroom before the maximum is raised
 constexpr int kPmLoaders = 4;           // warps that convert e4m3 rows, for K and for V
 constexpr int kPmThreadsRaw = 32 * 10;  // softmax 4, S, PV, K, V, relays of K and V
-constexpr int kPmThreadsCodes = 32 * (6 + 2 * kPmLoaders);   // softmax 4, S, PV, K 4, V 4
+constexpr int kPmThreadsCodes = 32 * (8 + 2 * kPmLoaders);   // 8 as above, converting K 4, V 4
 constexpr int kPmJoinThreads = 128;
 
 struct PagedMlaArgs {
@@ -73,8 +80,9 @@ struct PagedMlaArgs {
 
 struct PagedMlaTail {
   uint64_t q_full, q_empty, q_ready, o_empty, p_full, pv_done, drain[2];
-  uint64_t k_full[kPmKSlots], k_ready[kPmKSlots], k_empty[kPmKSlots];
-  uint64_t v_full[kPmVSlots], v_ready[kPmVSlots], v_empty[kPmVSlots];
+  uint64_t k_full[5], k_ready[5], k_empty[5];
+  uint64_t v_full[4], v_ready[4], v_empty[4];
+  uint64_t codes_full[2][4], codes_empty[2][4];      // of K, of V
   uint64_t s_full[2], s_empty[2];
   float peer[2][128];      // maxima (and at the end denominators) of a row's two threads
   int32_t start_pair, start_off, count, share;
@@ -83,10 +91,14 @@ struct PagedMlaTail {
 };
 
 constexpr size_t paged_mla_smem_bytes() {
-  return 1024 + kPmQBytes + kPmKSlots * kPmKBytes + kPmVSlots * kPmVBytes + kPmPBytes +
-         sizeof(PagedMlaTail);
+  return 1024 + kPmQBytes + PmRing<false>::kKSlots * PmRing<false>::kKBytes +
+         PmRing<false>::kVSlots * kPmSlice + kPmPBytes + sizeof(PagedMlaTail);
 }
 static_assert(paged_mla_smem_bytes() <= 227 * 1024, "shared memory of one CTA");
+static_assert(PmRing<true>::kKSlots * PmRing<true>::kKBytes + PmRing<true>::kVSlots * kPmSlice +
+                      2 * PmRing<true>::kCodes ==
+                  PmRing<false>::kKSlots * PmRing<false>::kKBytes + PmRing<false>::kVSlots * kPmSlice,
+              "both forms fill the same space");
 
 // ------------------------------------------------------------------- work --
 struct PmPair {
@@ -233,6 +245,10 @@ __device__ __forceinline__ uint32_t code_factor(float scale) {
 }
 // Any scale: in fp32, rounded to bf16 once.
 __device__ __noinline__ void codes_to_bf16_any(const uint4* w, float scale, uint4* lo, uint4* hi) {
+  if (scale == 0.f) {                                // a row past the end: also NaN codes
+    *lo = *hi = make_uint4(0, 0, 0, 0);
+    return;
+  }
   float v[16];
   e4m3x4_values(w->x, scale, v);
   e4m3x4_values(w->y, scale, v + 4);
@@ -271,19 +287,22 @@ __global__ void __cluster_dims__(2, 1, 1)
     __launch_bounds__(CODES ? kPmThreadsCodes : kPmThreadsRaw, 1)
     paged_mla_kernel(const __grid_constant__ CUtensorMap qmap,
                      const __grid_constant__ CUtensorMap kmap,
-                     const __grid_constant__ CUtensorMap vmap, const PagedMlaArgs a) {
+                     const __grid_constant__ CUtensorMap vmap,
+                     const __grid_constant__ CUtensorMap rmap, const PagedMlaArgs a) {
   extern __shared__ __align__(1024) uint8_t smem_raw[];
   uint8_t* smem = smem_raw + ((1024u - (smem_u32(smem_raw) & 1023u)) & 1023u);
   uint8_t* Qs = smem;                                // [9][64 rows x 128 B]
-  uint8_t* Ks = Qs + kPmQBytes;                      // [9][64 positions x 128 B]
-  uint8_t* Vs = Ks + kPmKSlots * kPmKBytes;          // [4][4 blocks][32 positions x 128 B]
-  uint8_t* Ps = Vs + kPmVSlots * kPmVBytes;          // [2][64 rows x 128 B]
-  PagedMlaTail* T = reinterpret_cast<PagedMlaTail*>(Ps + kPmPBytes);
+  using Ring = PmRing<CODES>;
+  uint8_t* Ks = Qs + kPmQBytes;                      // [slots][chunks][64 positions x 128 B]
+  uint8_t* Vs = Ks + Ring::kKSlots * Ring::kKBytes;  // [slots][4 blocks][32 positions x 128 B]
+  uint8_t* Ps = Vs + Ring::kVSlots * kPmSlice;       // [2][64 rows x 128 B]
+  uint8_t* Kc = Ps + kPmPBytes;                      // [4 groups][64 positions x 128 codes]
+  uint8_t* Vc = Kc + Ring::kCodes;                   // [4 slices][2 groups][32 positions x 128]
+  PagedMlaTail* T = reinterpret_cast<PagedMlaTail*>(Vc + Ring::kCodes);
 
   const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
   const int rank = (int)cluster_rank();
   const int cl = blockIdx.x >> 1, clusters = gridDim.x >> 1;
-  constexpr uint32_t kReady = CODES ? 2 * kPmLoaders : 2;
 
   if (threadIdx.x == 0) {
     mbar_init(&T->q_full, 1);
@@ -292,15 +311,19 @@ __global__ void __cluster_dims__(2, 1, 1)
     mbar_init(&T->o_empty, 8);
     mbar_init(&T->p_full, 8);
     mbar_init(&T->pv_done, 1);
-    for (int i = 0; i < kPmKSlots; ++i) {
+    for (int i = 0; i < 5; ++i) {
       mbar_init(&T->k_full[i], 1);
-      mbar_init(&T->k_ready[i], kReady);
+      mbar_init(&T->k_ready[i], 2);
       mbar_init(&T->k_empty[i], 1);
     }
-    for (int i = 0; i < kPmVSlots; ++i) {
+    for (int i = 0; i < 4; ++i) {
       mbar_init(&T->v_full[i], 1);
-      mbar_init(&T->v_ready[i], kReady);
+      mbar_init(&T->v_ready[i], CODES ? 2 * kPmLoaders : 2);
       mbar_init(&T->v_empty[i], 1);
+      mbar_init(&T->codes_full[0][i], 1);
+      mbar_init(&T->codes_full[1][i], 1);
+      mbar_init(&T->codes_empty[0][i], 2);
+      mbar_init(&T->codes_empty[1][i], kPmLoaders);
     }
     for (int i = 0; i < 2; ++i) {
       mbar_init(&T->s_full[i], 1);
@@ -310,10 +333,9 @@ __global__ void __cluster_dims__(2, 1, 1)
     T->abort = 0;
     fence_barrier_init();
     prefetch_tmap(&qmap);
-    if (!CODES) {
-      prefetch_tmap(&kmap);
-      prefetch_tmap(&vmap);
-    }
+    prefetch_tmap(&kmap);
+    prefetch_tmap(&vmap);
+    if (CODES) prefetch_tmap(&rmap);
   }
   if (warp == 4) pair_tmem_alloc(&T->tmem_base, 512);
   if (warp == 5) {
@@ -379,6 +401,7 @@ __global__ void __cluster_dims__(2, 1, 1)
       const uint64_t q_desc = make_sdesc(smem_u32(Qs)), k_desc = make_sdesc(smem_u32(Ks));
       const uint32_t q_ready = in_cta(&T->q_ready, 0);
       uint32_t sc = 0, qc = 0;                       // tiles, segments so far
+      int slot = 0, parity = 0;                      // of the next K slot
       bool ok = true;
       while (ok && pm_next(a, walk, s)) {
         ok = wait(&T->q_empty, (qc & 1) ^ 1, 57);
@@ -394,24 +417,29 @@ __global__ void __cluster_dims__(2, 1, 1)
           ok = ok && wait(&T->q_ready, qc & 1, 53);
           for (int i = 0; i < s.n && ok; ++i, ++sc) {
             const int b = sc & 1;
-            bool seen = mbar_try_wait(&T->k_ready[0], sc & 1);
+            bool seen = mbar_try_wait(&T->k_ready[slot], parity);
             ok = wait(&T->s_empty[b], ((sc >> 1) & 1) ^ 1, 51);
             if (!ok) break;
             tc_fence_after();
             const uint32_t d = tmem + 256 + b * 64;
 #pragma unroll 1
-            for (int k = 0; k < kPmKSlots; ++k) {
-              ok = ok && wait_seen(seen, &T->k_ready[k], sc & 1, 52);
+            for (int k = 0; k < 9; k += Ring::kChunks) {
+              ok = ok && wait_seen(seen, &T->k_ready[slot], parity, 52);
               if (!ok) break;
-              if (k + 1 < kPmKSlots) seen = mbar_try_wait(&T->k_ready[k + 1], sc & 1);
+              const int cur = slot;
+              if (++slot == Ring::kKSlots) {
+                slot = 0;
+                parity ^= 1;
+              }
+              seen = mbar_try_wait(&T->k_ready[slot], parity);
 #pragma unroll
-              for (int c = 0; c < 3; ++c)
+              for (int c = 0; c < Ring::kChunks; ++c)
 #pragma unroll
-                for (int kk = 0; kk < 4; ++kk) {     // 16 values
-                  const uint32_t at = (k * kPmKBytes + c * kPmChunk + kk * 32) >> 4;
-                  pair_mma_bf16(d, q_desc + at, k_desc + at, idesc, (k | c | kk) != 0);
-                }
-              pair_commit(&T->k_empty[k]);
+                for (int kk = 0; kk < 4; ++kk)       // 16 values
+                  pair_mma_bf16(d, q_desc + (((k + c) * kPmChunk + kk * 32) >> 4),
+                                k_desc + ((cur * Ring::kKBytes + c * kPmChunk + kk * 32) >> 4),
+                                idesc, (k | c | kk) != 0);
+              pair_commit(&T->k_empty[cur]);
             }
             if (!ok) break;
             pair_commit(&T->s_full[b]);
@@ -434,19 +462,25 @@ __global__ void __cluster_dims__(2, 1, 1)
       const uint32_t idesc = make_idesc<MmaKind::BF16>(256) | (1u << 16);   // B MN-major
       const uint64_t p_desc = make_sdesc(smem_u32(Ps)), v_desc = make_sdesc_mn(smem_u32(Vs), 4096);
       uint32_t pc = 0, qc = 0;
+      int slot = 0, parity = 0;                      // of the next V slot
       bool ok = true;
       while (ok && pm_next(a, walk, s)) {
         ok = wait(&T->o_empty, (qc & 1) ^ 1, 54);
         for (int i = 0; i < s.n && ok; ++i, ++pc) {
           ok = wait(&T->p_full, pc & 1, 55);
           if (!ok) break;
-          bool seen = mbar_try_wait(&T->v_ready[0], pc & 1);
+          bool seen = mbar_try_wait(&T->v_ready[slot], parity);
           tc_fence_after();
 #pragma unroll 1
-          for (int v = 0; v < kPmVSlots; ++v) {
-            ok = ok && wait_seen(seen, &T->v_ready[v], pc & 1, 56);
+          for (int v = 0; v < 4; ++v) {
+            ok = ok && wait_seen(seen, &T->v_ready[slot], parity, 56);
             if (!ok) break;
-            if (v + 1 < kPmVSlots) seen = mbar_try_wait(&T->v_ready[v + 1], pc & 1);
+            const int cur = slot;
+            if (++slot == Ring::kVSlots) {
+              slot = 0;
+              parity ^= 1;
+            }
+            seen = mbar_try_wait(&T->v_ready[slot], parity);
 #pragma unroll
             for (int kk = 0; kk < 2; ++kk) {         // 16 positions
               const int k16 = v * 2 + kk;
@@ -454,10 +488,10 @@ __global__ void __cluster_dims__(2, 1, 1)
 #pragma unroll
               for (int h = 0; h < 2; ++h)            // 128 values of each CTA
                 pair_mma_bf16(tmem + h * 128, ad,
-                              v_desc + ((v * kPmVBytes + h * 8192 + kk * 2048) >> 4), idesc,
+                              v_desc + ((cur * kPmSlice + h * 8192 + kk * 2048) >> 4), idesc,
                               (i | k16) != 0);
             }
-            pair_commit(&T->v_empty[v]);
+            pair_commit(&T->v_empty[cur]);
           }
           if (ok) pair_commit(&T->pv_done);
         }
@@ -476,15 +510,15 @@ __global__ void __cluster_dims__(2, 1, 1)
     bool ok = true;
     const int shift = a.c.page_shift, mask = (1 << shift) - 1;
     const int32_t* table = nullptr;                  // of the sequence
+    // page of a position; past the end (and where the table is wrong) one that TMA reads
+    // as zeros
+    auto page_at = [&](int key) -> int {
+      if (key >= s.pair.kl) return a.c.n_pages;
+      const int p = page_of(table, key, shift, a.c.n_pages);
+      if (p < 0) set_status(a.status, DSA_ERR_INVALID, 61);
+      return p < 0 ? a.c.n_pages : p;
+    };
     if constexpr (!CODES) {
-      // page of a position; past the end (and where the table is wrong) one that TMA
-      // reads as zeros
-      auto page_at = [&](int key) -> int {
-        if (key >= s.pair.kl) return a.c.n_pages;
-        const int p = page_of(table, key, shift, a.c.n_pages);
-        if (p < 0) set_status(a.status, DSA_ERR_INVALID, 61);
-        return p < 0 ? a.c.n_pages : p;
-      };
       if (warp == 6 && elect_one()) {
         const int rows = min(1 << shift, 64);        // of a copy
         while (ok && pm_next(a, walk, s)) {
@@ -494,11 +528,11 @@ __global__ void __cluster_dims__(2, 1, 1)
             const int key = i * kPmKeys + 64 * rank;
             const int page = page_at(key);
 #pragma unroll 1
-            for (int k = 0; k < kPmKSlots; ++k) {
+            for (int k = 0; k < Ring::kKSlots; ++k) {
               ok = wait(&T->k_empty[k], (n & 1) ^ 1, 62);
               if (!ok) break;
-              mbar_arrive_expect_tx(&T->k_full[k], kPmKBytes);
-              uint8_t* dst = Ks + k * kPmKBytes;
+              mbar_arrive_expect_tx(&T->k_full[k], Ring::kKBytes);
+              uint8_t* dst = Ks + k * Ring::kKBytes;
               if (rows == 64) {
                 tma_load_4d(dst, &kmap, &T->k_full[k], 0, key & mask, 3 * k, page);
               } else {                               // chunk by chunk, pages below one another
@@ -516,7 +550,7 @@ __global__ void __cluster_dims__(2, 1, 1)
         }
         // the last copies have landed (also on the abort path) and the last arrivals from
         // the MMAs have come before the CTA may end
-        for (int k = 0; k < kPmKSlots && n; ++k)
+        for (int k = 0; k < Ring::kKSlots && n; ++k)
           if (ok) wait(&T->k_empty[k], (n & 1) ^ 1, 64);
           else drain_slot(&T->k_full[k], n);
       } else if (warp == 7 && elect_one()) {
@@ -526,13 +560,13 @@ __global__ void __cluster_dims__(2, 1, 1)
 #pragma unroll 1
           for (int i = s.t0; i < s.t0 + s.n && ok; ++i, ++n) {
 #pragma unroll 1
-            for (int v = 0; v < kPmVSlots; ++v) {
+            for (int v = 0; v < Ring::kVSlots; ++v) {
               const int key = i * kPmKeys + v * 32;
               const int page = page_at(key);
               ok = wait(&T->v_empty[v], (n & 1) ^ 1, 63);
               if (!ok) break;
-              mbar_arrive_expect_tx(&T->v_full[v], kPmVBytes);
-              uint8_t* dst = Vs + v * kPmVBytes;
+              mbar_arrive_expect_tx(&T->v_full[v], kPmSlice);
+              uint8_t* dst = Vs + v * kPmSlice;
               if (rows == 32) {
                 tma_load_4d(dst, &vmap, &T->v_full[v], 0, key & mask, rank * 4, page);
               } else {
@@ -548,7 +582,7 @@ __global__ void __cluster_dims__(2, 1, 1)
             }
           }
         }
-        for (int v = 0; v < kPmVSlots && n; ++v)
+        for (int v = 0; v < Ring::kVSlots && n; ++v)
           if (ok) wait(&T->v_empty[v], (n & 1) ^ 1, 65);
           else drain_slot(&T->v_full[v], n);
       } else if (warp == 8 && elect_one()) {
@@ -557,7 +591,7 @@ __global__ void __cluster_dims__(2, 1, 1)
         const uint32_t k_ready = in_cta(&T->k_ready[0], 0);
         while (ok && pm_next(a, walk, s))
           for (int i = 0; i < s.n && ok; ++i, ++n)
-            for (int k = 0; k < kPmKSlots && ok; ++k) {
+            for (int k = 0; k < Ring::kKSlots && ok; ++k) {
               ok = wait(&T->k_full[k], n & 1, 59);
               if (ok) mbar_arrive_cluster(k_ready + k * 8);
             }
@@ -566,7 +600,7 @@ __global__ void __cluster_dims__(2, 1, 1)
         const uint32_t v_ready = in_cta(&T->v_ready[0], 0);
         while (ok && pm_next(a, walk, s)) {
           for (int i = s.t0; i < s.t0 + s.n && ok; ++i, ++n) {
-            for (int v = 0; v < kPmVSlots; ++v) {
+            for (int v = 0; v < Ring::kVSlots; ++v) {
               ok = wait(&T->v_full[v], n & 1, 60);
               ok = __all_sync(0xffffffffu, ok);
               if (!ok) break;
@@ -575,7 +609,7 @@ __global__ void __cluster_dims__(2, 1, 1)
                 const int from = max(live, 0);
                 for (int u = lane; u < (32 - from) * 32; u += 32) {
                   const int r = from + (u >> 5), blk = (u >> 3) & 3, k = u & 7;
-                  *reinterpret_cast<uint4*>(Vs + v * kPmVBytes + blk * 4096 + r * 128 + k * 16) =
+                  *reinterpret_cast<uint4*>(Vs + v * kPmSlice + blk * 4096 + r * 128 + k * 16) =
                       make_uint4(0, 0, 0, 0);
                 }
                 fence_proxy_async_smem();
@@ -586,173 +620,249 @@ __global__ void __cluster_dims__(2, 1, 1)
           }
         }
       }
+    } else if (warp == 6) {
+      // e4m3: codes of K, in 4 groups of 128 of 64 positions
+      if (elect_one()) {
+        const int rows = min(1 << shift, 64);        // of a copy
+        while (ok && pm_next(a, walk, s)) {
+          table = a.table + (int64_t)s.pair.b * a.max_pages;
+#pragma unroll 1
+          for (int i = s.t0; i < s.t0 + s.n && ok; ++i, ++n) {
+            const int key = i * kPmKeys + 64 * rank;
+#pragma unroll 1
+            for (int g = 0; g < 4; ++g) {
+              ok = wait(&T->codes_empty[0][g], (n & 1) ^ 1, 62);
+              if (!ok) break;
+              mbar_arrive_expect_tx(&T->codes_full[0][g], 8192);
+#pragma unroll 1
+              for (int j = 0; j < 64; j += rows)
+                tma_load_3d(Kc + g * 8192 + j * 128, &kmap, &T->codes_full[0][g], g * 128,
+                            (key + j) & mask, page_at(key + j));
+            }
+          }
+        }
+        for (int g = 0; g < 4 && n; ++g)
+          if (ok) wait(&T->codes_empty[0][g], (n & 1) ^ 1, 64);
+          else drain_slot(&T->codes_full[0][g], n);
+      }
+    } else if (warp == 7) {
+      // the bf16 chunk of K, straight into its slot, and the codes of V, in slices of 32
+      // positions
+      if (elect_one()) {
+        const int rows = min(1 << shift, 32);
+        while (ok && pm_next(a, walk, s)) {
+          table = a.table + (int64_t)s.pair.b * a.max_pages;
+#pragma unroll 1
+          for (int i = s.t0; i < s.t0 + s.n && ok; ++i, ++n) {
+            const uint32_t u = n * 9 + 8, slot = u % Ring::kKSlots, use = u / Ring::kKSlots;
+            // Uses of a slot lie 5 chunks apart and these 9: the parity below tells the last
+            // use from the one before only once the tile before has been read.
+            if (n) ok = wait(&T->s_full[(n - 1) & 1], ((n - 1) >> 1) & 1, 61);
+            ok = ok && wait(&T->k_empty[slot], (use & 1) ^ 1, 62);
+            if (!ok) break;
+            mbar_arrive_expect_tx(&T->k_full[0], kPmChunk);
+#pragma unroll 1
+            for (int j = 0; j < 64; j += rows) {
+              const int key = i * kPmKeys + 64 * rank + j;
+              tma_load_3d(Ks + slot * kPmChunk + j * 128, &rmap, &T->k_full[0], 0, key & mask,
+                          page_at(key));
+            }
+#pragma unroll 1
+            for (int v = 0; v < 4; ++v) {
+              ok = wait(&T->codes_empty[1][v], (n & 1) ^ 1, 63);
+              if (!ok) break;
+              mbar_arrive_expect_tx(&T->codes_full[1][v], 8192);
+#pragma unroll 1
+              for (int j = 0; j < 32; j += rows) {
+                const int key = i * kPmKeys + v * 32 + j;
+                const int page = page_at(key);
+                tma_load_3d(Vc + v * 8192 + j * 128, &vmap, &T->codes_full[1][v], rank * 256,
+                            key & mask, page);
+                tma_load_3d(Vc + v * 8192 + 4096 + j * 128, &vmap, &T->codes_full[1][v],
+                            rank * 256 + 128, key & mask, page);
+              }
+            }
+          }
+        }
+        if (!ok) drain_slot(&T->k_full[0], n);
+        for (int v = 0; v < 4 && n; ++v)
+          if (ok) wait(&T->codes_empty[1][v], (n & 1) ^ 1, 65);
+          else drain_slot(&T->codes_full[1][v], n);
+      }
     } else {
-      // 16 codes a thread and load, converted on the way to the slots; a slot's loads are
-      // issued before the slot ahead of it is converted
-      auto page_at = [&](int key) -> int {
-        if (key >= s.pair.kl) return -1;             // reads as zeros
-        const int p = page_of(table, key, shift, a.c.n_pages);
-        if (p < 0) set_status(a.status, DSA_ERR_INVALID, 61);
-        return p;
+      // Conversion of codes into slots.  Scales are loaded a tile ahead and their rows'
+      // pages looked up a tile before that.
+      const float* const scale0 = a.c.scale;
+      auto scales = [&](int page, int key) {         // of a row
+        const int64_t p = page < a.c.n_pages ? page : 0;
+        return scale0 + p * a.c.scale_ps + (int64_t)(key & mask) * 4;
       };
       auto ready = [&](uint32_t bar) {
         fence_proxy_async_smem();
         __syncwarp();
         if (lane == 0) mbar_arrive_cluster(bar);
       };
-      const uint4 zero = make_uint4(0, 0, 0, 0);
-      if (warp < 6 + kPmLoaders) {
-        // K: two threads a row, two runs of 16 values of each of a slot's three chunks; the
-        // last chunk of the last slot is the bf16 part
-        const int c = threadIdx.x - 192, krow = c >> 1, ku = (c & 1) * 2;
+      // 16 values: two 16-byte units of a swizzled row
+      auto put = [&](uint8_t* row_at, int row, int unit, bool exact, const uint4& w, uint32_t f,
+                     float scale) {
+        uint4 lo, hi;
+        if (exact) codes_to_bf16(w, f, lo, hi);
+        else codes_to_bf16_far(w, scale, lo, hi);
+        *reinterpret_cast<uint4*>(row_at + ((unit ^ (row & 7)) << 4)) = lo;
+        *reinterpret_cast<uint4*>(row_at + (((unit + 1) ^ (row & 7)) << 4)) = hi;
+      };
+      if (warp < 8 + kPmLoaders) {
+        // K: a warp takes every fourth chunk, a lane two of its rows
+        const int w = warp - 8;
         const uint32_t k_ready = in_cta(&T->k_ready[0], 0);
-        int page = -1, row = 0;
-        uint4 next[6], now[6], tail[4];
-        float scale[4], next_scale[4] = {0.f, 0.f, 0.f, 0.f};
-        auto fetch = [&](int tile, int k) {
-          if (k == 0) {
-            const int key = tile * kPmKeys + 64 * rank + krow;
-            page = page_at(key);
-            row = key & mask;
-            const float* sc = a.c.scale + page * a.c.scale_ps + row * 4;
+        int page[2];
+        float next[2][2];                            // [row][chunk w, w + 4]
+        uint32_t live = 0;                           // bit: the row of `next` is one
+        auto look = [&](int tile) {
 #pragma unroll
-            for (int i = 0; i < 4; ++i) next_scale[i] = page >= 0 ? sc[i] : 1.f;
-          }
-          const uint4* codes = reinterpret_cast<const uint4*>(a.c.codes + page * a.c.codes_ps +
-                                                              row * kPmDv) + 12 * k + ku;
+          for (int h = 0; h < 2; ++h) page[h] = page_at(tile * kPmKeys + 64 * rank + h * 32 + lane);
+        };
+        auto load = [&](int tile) {
+          live = 0;
 #pragma unroll
-          for (int j = 0; j < 3; ++j)
-#pragma unroll
-            for (int h = 0; h < 2; ++h)
-              next[2 * j + h] = page >= 0 && (k < 2 || j < 2) ? codes[4 * j + h] : zero;
-          if (k == 2) {
-            const uint4* raw = reinterpret_cast<const uint4*>(a.c.raw + page * a.c.raw_ps +
-                                                              row * 64) + 2 * ku;
-#pragma unroll
-            for (int i = 0; i < 4; ++i) tail[i] = page >= 0 ? raw[i] : zero;
+          for (int h = 0; h < 2; ++h) {
+            const float* sc = scales(page[h], tile * kPmKeys + 64 * rank + h * 32 + lane);
+            next[h][0] = sc[w >> 1];
+            next[h][1] = sc[(w >> 1) + 2];
+            live |= (page[h] < a.c.n_pages ? 1u : 0u) << h;
           }
         };
         while (ok && pm_next(a, walk, s)) {
           table = a.table + (int64_t)s.pair.b * a.max_pages;
-          fetch(s.t0, 0);
+          look(s.t0);
+          load(s.t0);
+          if (s.n > 1) look(s.t0 + 1);
 #pragma unroll 1
           for (int i = 0; i < s.n && ok; ++i, ++n) {
+            float now[2][2];
+            const uint32_t on = live;
 #pragma unroll
-            for (int j = 0; j < 4; ++j) scale[j] = next_scale[j];
+            for (int h = 0; h < 2; ++h) {
+              now[h][0] = on >> h & 1 ? next[h][0] : 0.f;
+              now[h][1] = on >> h & 1 ? next[h][1] : 0.f;
+            }
+            if (i + 1 < s.n) load(s.t0 + i + 1);
+            if (i + 2 < s.n) look(s.t0 + i + 2);
 #pragma unroll 1
-            for (int k = 0; k < kPmKSlots; ++k) {
-#pragma unroll
-              for (int j = 0; j < 6; ++j) now[j] = next[j];
-              // a slot's chunks 3k .. 3k + 2 lie in groups (3k) / 2 .. (3k + 2) / 2
-              const float s0 = k == 0 ? scale[0] : (k == 1 ? scale[1] : scale[3]);
-              const float s1 = k == 0 ? scale[0] : (k == 1 ? scale[2] : scale[3]);
-              const float s2 = k == 0 ? scale[1] : scale[2];
-              const uint4 t0 = tail[0], t1 = tail[1], t2 = tail[2], t3 = tail[3];
-              if (k + 1 < kPmKSlots) fetch(s.t0 + i, k + 1);
-              else if (i + 1 < s.n) fetch(s.t0 + i + 1, 0);
-              ok = ok && wait(&T->k_empty[k], (n & 1) ^ 1, 62);
+            for (int j = 0; j < 2; ++j) {
+              const int c = w + 4 * j, g = c >> 1;
+              const float s0 = j ? now[0][1] : now[0][0], s1 = j ? now[1][1] : now[1][0];
+              const uint32_t f0 = code_factor(s0), f1 = code_factor(s1);
+              const bool exact =
+                  __all_sync(0xffffffffu, (f0 != 0 || !(on & 1)) && (f1 != 0 || !(on & 2)));
+              ok = ok && wait(&T->codes_full[0][g], n & 1, 59);
               ok = __all_sync(0xffffffffu, ok);
               if (!ok) break;
-              const uint32_t f[3] = {code_factor(s0), code_factor(s1), code_factor(s2)};
-              const bool fast = __all_sync(0xffffffffu, f[0] && f[1] && f[2]);
-              uint8_t* dst = Ks + k * kPmKBytes + krow * 128;
-              auto put = [&](int j, int h, const uint4& lo, const uint4& hi) {
-                const int u = 2 * (ku + h);
-                *reinterpret_cast<uint4*>(dst + j * kPmChunk + ((u ^ (krow & 7)) << 4)) = lo;
-                *reinterpret_cast<uint4*>(dst + j * kPmChunk + (((u + 1) ^ (krow & 7)) << 4)) = hi;
-              };
-              if (fast) {
+              uint4 code[8];
 #pragma unroll
-                for (int j = 0; j < 3; ++j)
+              for (int h = 0; h < 2; ++h)
 #pragma unroll
-                  for (int h = 0; h < 2; ++h) {
-                    uint4 lo, hi;
-                    codes_to_bf16(now[2 * j + h], f[j], lo, hi);
-                    put(j, h, lo, hi);
-                  }
-              } else {
-                const float sj[3] = {s0, s1, s2};
+                for (int u = 0; u < 4; ++u) {
+                  const int row = h * 32 + lane;
+                  code[4 * h + u] = *reinterpret_cast<const uint4*>(
+                      Kc + g * 8192 + row * 128 + ((((c & 1) * 4 + u) ^ (row & 7)) << 4));
+                }
+              const uint32_t use = n * 9 + c, slot = use % Ring::kKSlots;
+              ok = wait(&T->k_empty[slot], ((use / Ring::kKSlots) & 1) ^ 1, 62);
+              ok = __all_sync(0xffffffffu, ok);
+              if (!ok) break;
 #pragma unroll
-                for (int j = 0; j < 3; ++j)
+              for (int h = 0; h < 2; ++h)
 #pragma unroll
-                  for (int h = 0; h < 2; ++h) {
-                    uint4 lo, hi;
-                    codes_to_bf16_far(now[2 * j + h], sj[j], lo, hi);
-                    put(j, h, lo, hi);
-                  }
-              }
-              if (k == 2) {
-                put(2, 0, t0, t1);
-                put(2, 1, t2, t3);
-              }
-              ready(k_ready + k * 8);
+                for (int u = 0; u < 4; ++u)
+                  put(Ks + slot * kPmChunk + (h * 32 + lane) * 128, lane, 2 * u, exact,
+                      code[4 * h + u], h ? f1 : f0, h ? s1 : s0);
+              ready(k_ready + slot * 8);
+              if (lane == 0) mbar_arrive(&T->codes_empty[0][g]);
+            }
+            if (w == 0 && ok) {                      // the tile's bf16 chunk has landed
+              ok = wait(&T->k_full[0], n & 1, 60);
+              ok = __all_sync(0xffffffffu, ok);
+              if (ok && lane == 0) mbar_arrive_cluster(k_ready + ((n * 9 + 8) % Ring::kKSlots) * 8);
             }
           }
         }
-        if (ok && c == 0)
-          for (int k = 0; k < kPmKSlots && n; ++k)
-            wait(&T->k_empty[k], (n & 1) ^ 1, 64);
+        // the last arrivals from the MMAs have come before the CTA may end
+        if (ok && w == 0 && lane == 0)
+          for (uint32_t i = 0; i < Ring::kKSlots && n; ++i) {
+            const uint32_t uses = (9 * n + Ring::kKSlots - 1 - i) / Ring::kKSlots;
+            wait(&T->k_empty[i], (uses & 1) ^ 1, 64);
+          }
       } else {
-        // V: four threads a row, four runs of 16 of this CTA's 256 values
-        const int c = threadIdx.x - 192 - 32 * kPmLoaders, vrow = c >> 2, vu = c & 3;
+        // V: the four warps share a slice, four lanes a row
+        const int w = warp - 8 - kPmLoaders, vrow = w * 8 + (lane >> 2), vu = lane & 3;
         const uint32_t v_ready = in_cta(&T->v_ready[0], 0);
-        uint4 next[4], now[4];
-        float next_scale[2];
-        auto fetch = [&](int tile, int v) {
-          const int key = tile * kPmKeys + v * 32 + vrow;
-          const int page = page_at(key), row = key & mask;
-          const uint4* codes = reinterpret_cast<const uint4*>(
-                                   a.c.codes + page * a.c.codes_ps + row * kPmDv + rank * 256) + vu;
-          const float* sc = a.c.scale + page * a.c.scale_ps + row * 4 + rank * 2;
+        int page[4];
+        float next[4][2];
+        uint32_t live = 0;                           // bit v: the row of next[v] is one
+        auto look = [&](int tile) {
 #pragma unroll
-          for (int h = 0; h < 4; ++h) next[h] = page >= 0 ? codes[4 * h] : zero;
+          for (int v = 0; v < 4; ++v) page[v] = page_at(tile * kPmKeys + v * 32 + vrow);
+        };
+        auto load = [&](int tile) {
+          live = 0;
 #pragma unroll
-          for (int h = 0; h < 2; ++h) next_scale[h] = page >= 0 ? sc[h] : 1.f;
+          for (int v = 0; v < 4; ++v) {
+            const float* sc = scales(page[v], tile * kPmKeys + v * 32 + vrow) + rank * 2;
+            next[v][0] = sc[0];
+            next[v][1] = sc[1];
+            live |= (page[v] < a.c.n_pages ? 1u : 0u) << v;
+          }
         };
         while (ok && pm_next(a, walk, s)) {
           table = a.table + (int64_t)s.pair.b * a.max_pages;
-          fetch(s.t0, 0);
+          look(s.t0);
+          load(s.t0);
+          if (s.n > 1) look(s.t0 + 1);
 #pragma unroll 1
           for (int i = 0; i < s.n && ok; ++i, ++n) {
-#pragma unroll 1
-            for (int v = 0; v < kPmVSlots; ++v) {
+            float now[4][2];
+            const uint32_t on = live;
 #pragma unroll
-              for (int h = 0; h < 4; ++h) now[h] = next[h];
-              const float sc[2] = {next_scale[0], next_scale[1]};
-              if (v + 1 < kPmVSlots) fetch(s.t0 + i, v + 1);
-              else if (i + 1 < s.n) fetch(s.t0 + i + 1, 0);
-              ok = ok && wait(&T->v_empty[v], (n & 1) ^ 1, 63);
+            for (int v = 0; v < 4; ++v) {
+              now[v][0] = on >> v & 1 ? next[v][0] : 0.f;
+              now[v][1] = on >> v & 1 ? next[v][1] : 0.f;
+            }
+            if (i + 1 < s.n) load(s.t0 + i + 1);
+            if (i + 2 < s.n) look(s.t0 + i + 2);
+#pragma unroll 1
+            for (int v = 0; v < 4; ++v) {
+              const float s0 = v & 2 ? (v & 1 ? now[3][0] : now[2][0]) : (v & 1 ? now[1][0] : now[0][0]);
+              const float s1 = v & 2 ? (v & 1 ? now[3][1] : now[2][1]) : (v & 1 ? now[1][1] : now[0][1]);
+              const uint32_t f0 = code_factor(s0), f1 = code_factor(s1);
+              const bool exact = __all_sync(0xffffffffu, (f0 && f1) || !(on >> v & 1));
+              ok = ok && wait(&T->codes_full[1][v], n & 1, 60);
               ok = __all_sync(0xffffffffu, ok);
               if (!ok) break;
-              const uint32_t f[2] = {code_factor(sc[0]), code_factor(sc[1])};
-              const bool fast = __all_sync(0xffffffffu, f[0] && f[1]);
-              uint8_t* dst = Vs + v * kPmVBytes + vrow * 128;
-              auto put = [&](int h, const uint4& lo, const uint4& hi) {   // block of 64 values
-                *reinterpret_cast<uint4*>(dst + h * 4096 + (((2 * vu) ^ (vrow & 7)) << 4)) = lo;
-                *reinterpret_cast<uint4*>(dst + h * 4096 + (((2 * vu + 1) ^ (vrow & 7)) << 4)) = hi;
-              };
-              if (fast) {
+              uint4 code[4];
 #pragma unroll
-                for (int h = 0; h < 4; ++h) {
-                  uint4 lo, hi;
-                  codes_to_bf16(now[h], f[h >> 1], lo, hi);
-                  put(h, lo, hi);
-                }
-              } else {
+              for (int h = 0; h < 4; ++h)
+                code[h] = *reinterpret_cast<const uint4*>(
+                    Vc + v * 8192 + (h >> 1) * 4096 + vrow * 128 +
+                    (((vu + 4 * (h & 1)) ^ (vrow & 7)) << 4));
+              const uint32_t use = n * 4 + v, slot = use % Ring::kVSlots;
+              ok = wait(&T->v_empty[slot], ((use / Ring::kVSlots) & 1) ^ 1, 63);
+              ok = __all_sync(0xffffffffu, ok);
+              if (!ok) break;
 #pragma unroll
-                for (int h = 0; h < 4; ++h) {
-                  uint4 lo, hi;
-                  codes_to_bf16_far(now[h], sc[h >> 1], lo, hi);
-                  put(h, lo, hi);
-                }
-              }
-              ready(v_ready + v * 8);
+              for (int h = 0; h < 4; ++h)            // block of 64 values
+                put(Vs + slot * kPmSlice + h * 4096 + vrow * 128, vrow, 2 * vu, exact, code[h],
+                    h < 2 ? f0 : f1, h < 2 ? s0 : s1);
+              ready(v_ready + slot * 8);
+              if (lane == 0) mbar_arrive(&T->codes_empty[1][v]);
             }
           }
         }
-        if (ok && c == 0)
-          for (int v = 0; v < kPmVSlots && n; ++v)
-            wait(&T->v_empty[v], (n & 1) ^ 1, 65);
+        if (ok && w == 0 && lane == 0)
+          for (uint32_t i = 0; i < Ring::kVSlots && n; ++i) {
+            const uint32_t uses = (4 * n + Ring::kVSlots - 1 - i) / Ring::kVSlots;
+            wait(&T->v_empty[i], (uses & 1) ^ 1, 65);
+          }
       }
     }
   } else {
