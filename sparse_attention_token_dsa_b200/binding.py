@@ -455,6 +455,7 @@ _CODES = (torch.uint8, torch.float8_e4m3fn)
 
 
 def _need(name, t, dtypes, device, strided=False):
+    """Checks of one tensor, in the order in which they are cheapest to pass."""
     if not isinstance(t, torch.Tensor):
         raise TypeError(f"{name}: expected a torch.Tensor, got {type(t).__name__}")
     if t.dtype not in dtypes:
@@ -468,19 +469,28 @@ def _need(name, t, dtypes, device, strided=False):
 def _cuda_device(name, t):
     if not isinstance(t, torch.Tensor):
         raise TypeError(f"{name}: expected a torch.Tensor, got {type(t).__name__}")
-    if t.device.type != "cuda":
+    if not t.is_cuda:
         raise ValueError(f"{name}: must be on a CUDA device, not {t.device}")
     return t.device
 
 
-def _on(device, stream, call, what):
-    """`call(stream)` with `device` current, on `stream` (default: that device's current
-    one); raises DsaError for a status other than DSA_OK."""
-    if device.index == torch.cuda.current_device():
-        rc = call((torch.cuda.current_stream() if stream is None else stream).cuda_stream)
+# The current stream as a number (torch.cuda.current_stream() makes an object of it, which
+# takes longer than the launch it is for).
+_current_stream = torch._C._cuda_getCurrentRawStream if hasattr(
+    torch._C, "_cuda_getCurrentRawStream") else (
+        lambda index: torch.cuda.current_stream(index).cuda_stream)
+
+
+def _on(device, stream, what, call, *args):
+    """call(*args, stream) with `device` current, on `stream` (default: that device's
+    current one); raises DsaError for a status other than DSA_OK."""
+    index = device.index
+    raw = _current_stream(index) if stream is None else stream.cuda_stream
+    if index == torch.cuda.current_device():
+        rc = call(*args, raw)
     else:
-        with torch.cuda.device(device):
-            rc = call((torch.cuda.current_stream() if stream is None else stream).cuda_stream)
+        with torch.cuda.device(index):
+            rc = call(*args, raw)
     if rc != DSA_OK:
         raise DsaError(rc, what)
 
@@ -528,8 +538,8 @@ def _rope(x, pos, freq, offset, interleaved, mscale, out, stream, flags, what):
     xs, os_ = x.stride(), out.stride()
     p = DsaRopeProblem(n, heads, dim, offset, 2 * freq.numel(), _dtype_code(x), mscale, xs[0],
                        xs[1], os_[0], os_[1], flags | (DSA_FLAG_INTERLEAVED if interleaved else 0))
-    _on(dev, stream, lambda st: lib.dsa_rope(C.byref(p), x.data_ptr(), pos.data_ptr(),
-                                             freq.data_ptr(), out.data_ptr(), st), what)
+    _on(dev, stream, what, lib.dsa_rope, C.byref(p), x.data_ptr(), pos.data_ptr(),
+        freq.data_ptr(), out.data_ptr())
     return out
 
 
@@ -560,29 +570,35 @@ class PagedCache:
         if (codes is None) != (scale is None):
             raise ValueError("codes and scale come together")
         first = raw if codes is None else codes
-        dev = self.device = _cuda_device("raw" if codes is None else "codes", first)
+        self.device = _cuda_device("raw" if codes is None else "codes", first)
         self.codes, self.scale, self.raw = codes, scale, raw
-        c = self.c = DsaCache()
         if first.dim() != 3:
             raise ValueError("planes: must be [pages, page, width]")
-        c.n_pages, c.page_size = first.shape[0], first.shape[1]
-        if codes is not None:
-            c.dim_q = codes.shape[2]
-            c.codes, c.codes_page_stride = self._plane("codes", codes, _CODES, c.dim_q)
-            c.scale, c.scale_page_stride = self._plane("scale", scale, _F32, c.dim_q // 128)
+        pages, page, dim_q = first.shape
+        dim_raw, codes_ps, scale_ps, raw_ps = 0, 0, 0, 0
+        codes_p = scale_p = raw_p = None
+        if codes is None:
+            dim_q = 0
+        else:
+            codes_ps = self._plane("codes", codes, _CODES, pages, page, dim_q)
+            scale_ps = self._plane("scale", scale, _F32, pages, page, dim_q // 128)
+            codes_p, scale_p = codes.data_ptr(), scale.data_ptr()
         if raw is not None:
-            c.dim_raw = raw.shape[2]
-            c.raw, c.raw_page_stride = self._plane("raw", raw, (torch.bfloat16,), c.dim_raw)
+            dim_raw = raw.shape[-1]
+            raw_ps = self._plane("raw", raw, (torch.bfloat16,), pages, page, dim_raw)
+            raw_p = raw.data_ptr()
+        self.c = DsaCache(pages, page, dim_q, dim_raw, codes_p, scale_p, raw_p, codes_ps, scale_ps,
+                          raw_ps)
 
-    def _plane(self, name, t, dtypes, width):
+    def _plane(self, name, t, dtypes, pages, page, width):
+        """Page stride of a plane of rows of `width`."""
         _need(name, t, dtypes, self.device, strided=True)
-        pages, page = self.c.n_pages, self.c.page_size
-        if t.dim() != 3 or tuple(t.shape) != (pages, page, width):
+        if t.shape != (pages, page, width):
             raise ValueError(f"{name}: shape {tuple(t.shape)}, expected {(pages, page, width)}")
         ps, rs, vs = t.stride()
         if (vs != 1 and width > 1) or (rs != width and page > 1):
             raise ValueError(f"{name}: the rows of a page must be contiguous")
-        return t.data_ptr(), page * width if pages == 1 else ps
+        return page * width if pages == 1 else ps
 
     @staticmethod
     def empty(n_pages, page_size, dim_q, dim_raw, device="cuda"):
@@ -622,9 +638,8 @@ def cache_write(cache, x, slots, pow2=False, freq=None, pos=None, offset=0, inte
                                       flags=DSA_FLAG_INTERLEAVED if interleaved else 0))
         pos_p, freq_p = pos.data_ptr(), freq.data_ptr()
     flags = DSA_FLAG_POW2_SCALE if pow2 else 0
-    _on(dev, stream, lambda st: lib.dsa_cache_write(
-        C.byref(c), x.data_ptr(), _dtype_code(x), x.stride(0), n, slots.data_ptr(), turn, pos_p,
-        freq_p, flags, st), "dsa_cache_write")
+    _on(dev, stream, "dsa_cache_write", lib.dsa_cache_write, C.byref(c), x.data_ptr(),
+        _dtype_code(x), x.stride(0), n, slots.data_ptr(), turn, pos_p, freq_p, flags)
 
 
 def _table(cache, block_table, n_k, k_len):
@@ -649,10 +664,9 @@ def cache_read(cache, block_table, n_k, k_len=None, dtype=torch.bfloat16, out=No
     _need("out", out, _ROWS, dev)
     if tuple(out.shape) != shape:
         raise ValueError(f"out: shape {tuple(out.shape)}, expected {shape}")
-    _on(dev, stream, lambda st: lib.dsa_cache_read(
-        C.byref(c), block_table.data_ptr(), shape[0], block_table.shape[1], n_k,
-        None if k_len is None else k_len.data_ptr(), out.data_ptr(), _dtype_code(out), st),
-        "dsa_cache_read")
+    _on(dev, stream, "dsa_cache_read", lib.dsa_cache_read, C.byref(c), block_table.data_ptr(),
+        shape[0], block_table.shape[1], n_k, None if k_len is None else k_len.data_ptr(),
+        out.data_ptr(), _dtype_code(out))
     return out
 
 
@@ -674,10 +688,9 @@ def cache_read_codes(cache, block_table, n_k, k_len=None, out=None, stream=None)
     _need("scale", scale, _F32, dev)
     if tuple(codes.shape) != (batch, n_k, c.dim_q) or scale.numel() != batch * n_k * groups:
         raise ValueError(f"out: shapes {tuple(codes.shape)}, {tuple(scale.shape)}")
-    _on(dev, stream, lambda st: lib.dsa_cache_read_codes(
-        C.byref(c), block_table.data_ptr(), batch, block_table.shape[1], n_k,
-        None if k_len is None else k_len.data_ptr(), codes.data_ptr(), scale.data_ptr(), st),
-        "dsa_cache_read_codes")
+    _on(dev, stream, "dsa_cache_read_codes", lib.dsa_cache_read_codes, C.byref(c),
+        block_table.data_ptr(), batch, block_table.shape[1], n_k,
+        None if k_len is None else k_len.data_ptr(), codes.data_ptr(), scale.data_ptr())
     return codes, scale
 
 
@@ -710,8 +723,6 @@ def paged_mla(q, cache, block_table, k_len, scale, q_len=None, flags=0, out=None
             raise ValueError(f"q_len: {q_len.numel()} lengths for {batch} sequences")
     p = DsaPagedMlaProblem(batch, n_q, heads, dim, 512, block_table.shape[1], cache.c.page_size,
                            scale, flags)
-    n = C.c_size_t(0)
-    _check(lib.dsa_paged_mla_workspace_size(C.byref(p), C.byref(n)), "dsa_paged_mla")
     if out is None:
         out = _new(stream, lambda: torch.empty((batch, n_q, heads, 512), dtype=torch.bfloat16,
                                                device=dev))
@@ -726,13 +737,15 @@ def paged_mla(q, cache, block_table, k_len, scale, q_len=None, flags=0, out=None
         if out_lse.numel() != batch * n_q * heads:
             raise ValueError(f"out_lse: shape {tuple(out_lse.shape)}")
     if workspace is None:
+        n = C.c_size_t(0)
+        _check(lib.dsa_paged_mla_workspace_size(C.byref(p), C.byref(n)), "dsa_paged_mla")
         workspace = _new(stream, lambda: torch.empty(n.value, dtype=torch.uint8, device=dev))
     else:
         _need("workspace", workspace, _U8, dev)
-    _on(dev, stream, lambda st: lib.dsa_paged_mla(
-        C.byref(p), C.byref(cache.c), q.data_ptr(), block_table.data_ptr(), k_len.data_ptr(),
+    _on(dev, stream, "dsa_paged_mla", lib.dsa_paged_mla, C.byref(p), C.byref(cache.c),
+        q.data_ptr(), block_table.data_ptr(), k_len.data_ptr(),
         None if q_len is None else q_len.data_ptr(), out.data_ptr(), out_lse.data_ptr(),
-        workspace.data_ptr(), workspace.numel(), st), "dsa_paged_mla")
+        workspace.data_ptr(), workspace.numel())
     return out, out_lse
 
 

@@ -187,7 +187,7 @@ bool map_rows(CUtensorMap* m, const dsa_cache* c, bool codes, uint32_t box_rows)
 struct PagedMlaPlan {
   int row_tiles, clusters;
   int64_t pairs;
-  size_t off_plan, off_ml, off_o, bytes;
+  size_t off_states, off_plan, off_ml, off_o, bytes;
 };
 
 int plan_paged_mla(const dsa_paged_mla_problem* p, PagedMlaPlan* pl) {
@@ -207,7 +207,8 @@ int plan_paged_mla(const dsa_paged_mla_problem* p, PagedMlaPlan* pl) {
   const int64_t tiles = pl->pairs * key_tiles;
   pl->clusters = tiles < kPmClusters ? (int)tiles : kPmClusters;
   auto up = [](size_t x) { return (x + 255) / 256 * 256; };
-  pl->off_plan = kWsHeaderBytes;
+  pl->off_states = kWsHeaderBytes;
+  pl->off_plan = pl->off_states + up((size_t)pl->clusters * 2 * sizeof(int32_t));
   pl->off_ml = pl->off_plan + up((size_t)(1 + pl->pairs) * sizeof(int32_t));
   pl->off_o = pl->off_ml + up((size_t)2 * pl->clusters * kPmRows * sizeof(float2));
   pl->bytes = pl->off_o + (size_t)2 * pl->clusters * kPmRows * kPmDv * sizeof(float);
@@ -405,7 +406,6 @@ int dsa_paged_mla(const dsa_paged_mla_problem* p, const dsa_cache* c, const void
   if (!aligned16(workspace)) return DSA_ERR_INVALID;
   cudaStream_t st = reinterpret_cast<cudaStream_t>(stream);
   uint8_t* ws = reinterpret_cast<uint8_t*>(workspace);
-  if (cudaMemsetAsync(ws, 0, kWsHeaderBytes, st) != cudaSuccess) return DSA_ERR_CUDA;
   CUtensorMap qm{}, km{}, vm{}, rm{};
   if (!map_query(&qm, q, (uint64_t)p->batch * p->n_q * p->heads)) return DSA_ERR_CUDA;
   const uint32_t page = (uint32_t)c->page_size;
@@ -435,6 +435,8 @@ int dsa_paged_mla(const dsa_paged_mla_problem* p, const dsa_cache* c, const void
   a.out = reinterpret_cast<uint16_t*>(out);
   a.lse = out_lse;
   a.status = reinterpret_cast<int32_t*>(ws);
+  a.states = reinterpret_cast<int32_t*>(ws + pl.off_states);
+  a.clusters = pl.clusters;
   a.plan = reinterpret_cast<int32_t*>(ws + pl.off_plan);
   a.part_ml = reinterpret_cast<float2*>(ws + pl.off_ml);
   a.part_o = reinterpret_cast<float*>(ws + pl.off_o);
@@ -446,9 +448,20 @@ int dsa_paged_mla(const dsa_paged_mla_problem* p, const dsa_cache* c, const void
       qm, km, vm, rm, a);
   if (launch_status() != DSA_OK) return DSA_ERR_CUDA;
   const int64_t rows = (int64_t)p->n_q * p->heads;
-  const dim3 grid((unsigned)pl.pairs, (unsigned)(rows < kPmRows ? rows : kPmRows));
-  paged_mla_join_kernel<<<grid, kPmJoinThreads, 0, st>>>(a);
-  if (launch_status() != DSA_OK) return DSA_ERR_CUDA;
+  // the join is launched while the attention kernel drains, and waits for its end itself
+  cudaLaunchConfig_t join{};
+  join.gridDim = dim3((unsigned)pl.pairs, (unsigned)(rows < kPmRows ? rows : kPmRows));
+  join.blockDim = dim3(kPmJoinThreads);
+  join.stream = st;
+  cudaLaunchAttribute early{};
+  early.id = cudaLaunchAttributeProgrammaticStreamSerialization;
+  early.val.programmaticStreamSerializationAllowed = 1;
+  join.attrs = &early;
+  join.numAttrs = 1;
+  if (cudaLaunchKernelEx(&join, paged_mla_join_kernel, a) != cudaSuccess) {
+    cudaGetLastError();
+    return DSA_ERR_CUDA;
+  }
   if (p->flags & DSA_FLAG_CHECK) return dsa_read_status(workspace, stream);
   return DSA_OK;
 }

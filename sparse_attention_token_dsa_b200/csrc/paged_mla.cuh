@@ -69,10 +69,12 @@ struct PagedMlaArgs {
   int32_t batch, n_q, heads, max_pages;
   int32_t row_tiles;       // row tiles of a sequence of n_q tokens
   int32_t pairs;           // batch * row_tiles
+  int32_t clusters;
   float scale_log2;        // softmax scale * log2(e)
   uint16_t* out;           // [batch][n_q][heads][512] bf16
   float* lse;              // [batch][n_q][heads] or null
-  int32_t* status;
+  int32_t* status;         // of the call (written by the join)
+  int32_t* states;         // [clusters][2]: status of a cluster, and the wait that gave up
   int32_t* plan;           // [0]: tiles of a share; [1 + pair]: the pair's first tile
   float* part_o;           // [2 * clusters][128][512]
   float2* part_ml;         // [2 * clusters][128] maximum (log2 units), denominator
@@ -303,6 +305,7 @@ __global__ void __cluster_dims__(2, 1, 1)
   const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
   const int rank = (int)cluster_rank();
   const int cl = blockIdx.x >> 1, clusters = gridDim.x >> 1;
+  int32_t* const state = a.states + 2 * cl;
 
   if (threadIdx.x == 0) {
     mbar_init(&T->q_full, 1);
@@ -331,6 +334,7 @@ __global__ void __cluster_dims__(2, 1, 1)
       mbar_init(&T->drain[i], 1);
     }
     T->abort = 0;
+    if (rank == 0) state[0] = DSA_OK;
     fence_barrier_init();
     prefetch_tmap(&qmap);
     prefetch_tmap(&kmap);
@@ -383,12 +387,12 @@ __global__ void __cluster_dims__(2, 1, 1)
   PmSegment s;
 
   auto wait = [&](uint64_t* bar, uint32_t parity, int where) -> bool {
-    return mbar_wait_far(bar, parity, abort, a.status, where);
+    return mbar_wait_far(bar, parity, abort, state, where);
   };
   // The result of `wait`, asked for earlier: a slot's barrier is looked at before the
   // matrix instructions of the slot before it are issued.
   auto wait_seen = [&](bool seen, uint64_t* bar, uint32_t parity, int where) -> bool {
-    return seen || mbar_poll(bar, parity, abort, a.status, where);
+    return seen || mbar_poll(bar, parity, abort, state, where);
   };
 
   // The roles of warps 4 and up (but for the conversion of codes) run in one lane.
@@ -515,7 +519,7 @@ __global__ void __cluster_dims__(2, 1, 1)
     auto page_at = [&](int key) -> int {
       if (key >= s.pair.kl) return a.c.n_pages;
       const int p = page_of(table, key, shift, a.c.n_pages);
-      if (p < 0) set_status(a.status, DSA_ERR_INVALID, 61);
+      if (p < 0) set_status(state, DSA_ERR_INVALID, 61);
       return p < 0 ? a.c.n_pages : p;
     };
     if constexpr (!CODES) {
@@ -887,7 +891,7 @@ __global__ void __cluster_dims__(2, 1, 1)
       return T->peer[at][t ^ 64];
     };
     auto wait_all = [&](uint64_t* bar, uint32_t parity, int where) {
-      if (ok) ok = mbar_wait_far(bar, parity, abort, a.status, where);
+      if (ok) ok = mbar_wait_far(bar, parity, abort, state, where);
       ok = __all_sync(0xffffffffu, ok);
     };
     while (pm_next(a, walk, s)) {
@@ -1024,6 +1028,7 @@ __global__ void __cluster_dims__(2, 1, 1)
   }
   tc_fence_before();
   __syncthreads();
+  asm volatile("griddepcontrol.launch_dependents;");   // the join may be set up meanwhile
   __syncwarp();
   cluster_sync();
   if (warp == 4) {
@@ -1039,6 +1044,19 @@ __global__ void __launch_bounds__(kPmJoinThreads) paged_mla_join_kernel(const Pa
   __shared__ float red[2][kPmJoinThreads / 32];
   const int p = blockIdx.x, row = blockIdx.y, t = threadIdx.x;
   const PmPair pr = pm_pair(a, p);
+  asm volatile("griddepcontrol.wait;" ::: "memory");   // all of the attention kernel is done
+  if (p == 0 && row == 0 && t < 32) {                // status of the call: the first cluster's
+    int code = DSA_OK, where = 0;
+    for (int c = t; c < a.clusters && code == DSA_OK; c += 32) {
+      code = a.states[2 * c];
+      if (code != DSA_OK) where = a.states[2 * c + 1];
+    }
+    const uint32_t bad = __ballot_sync(0xffffffffu, code != DSA_OK);
+    if (bad ? t == __ffs(bad) - 1 : t == 0) {
+      a.status[0] = code;
+      a.status[1] = where;
+    }
+  }
   if (row >= pr.rows) return;
   const int64_t grow = (int64_t)pr.b * a.n_q * a.heads + pr.row0 + row;
   uint2* out = reinterpret_cast<uint2*>(a.out + grow * kPmDv) + t;
