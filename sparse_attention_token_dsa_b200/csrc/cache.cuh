@@ -87,6 +87,7 @@ struct RopeArgs {
   int32_t heads, offset, rot;
   int32_t pairs;           // pair units of a head (see below)
   int32_t units;           // pair and copy units of a head
+  uint32_t per_unit;       // 2^32 / units, rounded up (0: one unit)
   int32_t tpb;             // tokens of a block
   int32_t span;            // units that one block of a token takes (blockIdx.y of them)
   float mscale;
@@ -105,7 +106,7 @@ constexpr int kRopeBatch = 4;    // units a thread holds at once
 // 16 bytes take the same path one pair at a time (VEC = false).
 // Measured: see the table of the operators.
 template <typename T, bool VEC, bool INTER>
-__global__ void __launch_bounds__(kRopeThreads) rope_kernel(const RopeArgs a) {
+__global__ void __launch_bounds__(kRopeThreads, 4) rope_kernel(const RopeArgs a) {
   using R = RowType<T>;
   constexpr int N = VEC ? R::kVec : 1;
   extern __shared__ float2 turns[];                  // [tpb][rot / 2]: m cos, m sin
@@ -131,7 +132,7 @@ __global__ void __launch_bounds__(kRopeThreads) rope_kernel(const RopeArgs a) {
       if (i >= last) continue;
       const uint32_t tl = a.tpb > 1 ? i / per_token : 0;
       const uint32_t r = i - tl * per_token;
-      const uint32_t h = r / (uint32_t)a.units;
+      const uint32_t h = a.per_unit ? __umulhi(r, a.per_unit) : r;
       const int u = (int)(r - h * a.units);
       int d;
       if (u < a.pairs) {
@@ -147,8 +148,8 @@ __global__ void __launch_bounds__(kRopeThreads) rope_kernel(const RopeArgs a) {
       oa[k] = (t0 + tl) * a.o_ts + (int64_t)h * a.o_hs + d;
       const int part = INTER ? 1 : half;             // distance of the partner
       if constexpr (VEC) {
-        va[k] = *reinterpret_cast<const uint4*>(px);
-        if (!INTER && tab[k] >= 0) vb[k] = *reinterpret_cast<const uint4*>(px + half);
+        va[k] = __ldcs(reinterpret_cast<const uint4*>(px));
+        if (!INTER && tab[k] >= 0) vb[k] = __ldcs(reinterpret_cast<const uint4*>(px + half));
       } else {
         sa[k] = R::get(px);
         if (tab[k] >= 0) sb[k] = R::get(px + part);
@@ -170,7 +171,7 @@ __global__ void __launch_bounds__(kRopeThreads) rope_kernel(const RopeArgs a) {
       T* po = out + oa[k];
       if (tab[k] < 0) {
         if constexpr (VEC)
-          *reinterpret_cast<uint4*>(po) = va[k];
+          __stcs(reinterpret_cast<uint4*>(po), va[k]);
         else
           R::put(po, sa[k]);
       } else if constexpr (!VEC) {
@@ -187,7 +188,7 @@ __global__ void __launch_bounds__(kRopeThreads) rope_kernel(const RopeArgs a) {
           v[2 * j] = p * cs.x - q * cs.y;
           v[2 * j + 1] = q * cs.x + p * cs.y;
         }
-        *reinterpret_cast<uint4*>(po) = R::pack(v);
+        __stcs(reinterpret_cast<uint4*>(po), R::pack(v));
       } else {
         float v[N], w[N];
         R::unpack(va[k], v);
@@ -199,8 +200,8 @@ __global__ void __launch_bounds__(kRopeThreads) rope_kernel(const RopeArgs a) {
           v[j] = p * cs.x - q * cs.y;
           w[j] = q * cs.x + p * cs.y;
         }
-        *reinterpret_cast<uint4*>(po) = R::pack(v);
-        *reinterpret_cast<uint4*>(po + half) = R::pack(w);
+        __stcs(reinterpret_cast<uint4*>(po), R::pack(v));
+        __stcs(reinterpret_cast<uint4*>(po + half), R::pack(w));
       }
     }
   }
@@ -216,7 +217,8 @@ struct CachePlanes {
 };
 
 constexpr int kCacheThreads = 256;
-constexpr int kCacheUnits = kCacheThreads / 8;   // 8 lanes take one chunk of 128 values
+constexpr int kCacheUnits = kCacheThreads / 8;   // 8 lanes take a row, in chunks of 128 values
+constexpr int kCacheBatch = 4;                   // chunks a lane holds at once
 
 struct CacheWriteArgs {
   CachePlanes c;
@@ -229,38 +231,48 @@ struct CacheWriteArgs {
   int32_t offset, rot, inter;
   float mscale;
   float sign;              // +1, or -1 for the transpose
+  int32_t items;           // chunks of a row
   int32_t pow2;            // scale: least power of two >= amax / 448 (else amax / 448)
 };
 
-// The 8 values of a row that start at d (a multiple of 8), rotated where they lie in
-// the rotated part.
+// 8 consecutive values of a row as they were loaded.
 template <typename T, bool VEC>
-__device__ __forceinline__ void load8(const T* row, int d, float (&v)[8]) {
+struct Run8 {
   using R = RowType<T>;
-  if constexpr (VEC) {
-    if constexpr (R::kVec == 8) {
-      R::unpack(*reinterpret_cast<const uint4*>(row + d), v);
+  static constexpr int kWords = 8 / R::kVec;
+  uint4 word[VEC ? kWords : 1];
+  float value[VEC ? 1 : 8];
+  __device__ __forceinline__ void load(const T* p) {
+    if constexpr (VEC) {
+#pragma unroll
+      for (int i = 0; i < kWords; ++i) word[i] = *reinterpret_cast<const uint4*>(p + i * R::kVec);
     } else {
-      float lo[4], hi[4];
-      R::unpack(*reinterpret_cast<const uint4*>(row + d), lo);
-      R::unpack(*reinterpret_cast<const uint4*>(row + d + 4), hi);
 #pragma unroll
-      for (int j = 0; j < 4; ++j) {
-        v[j] = lo[j];
-        v[j + 4] = hi[j];
-      }
+      for (int j = 0; j < 8; ++j) value[j] = R::get(p + j);
     }
-  } else {
-#pragma unroll
-    for (int j = 0; j < 8; ++j) v[j] = R::get(row + d + j);
   }
-}
+  __device__ __forceinline__ void get(float (&v)[8]) const {
+    if constexpr (VEC) {
+#pragma unroll
+      for (int i = 0; i < kWords; ++i) {
+        float u[R::kVec];
+        R::unpack(word[i], u);
+#pragma unroll
+        for (int j = 0; j < R::kVec; ++j) v[i * R::kVec + j] = u[j];
+      }
+    } else {
+#pragma unroll
+      for (int j = 0; j < 8; ++j) v[j] = value[j];
+    }
+  }
+};
 
+// Rotates the 8 values of a row that start at d (a multiple of 8) where they lie in the
+// rotated part (in the half layout with their partners, read here).
 template <typename T, bool VEC>
-__device__ __forceinline__ void load8_turned(const CacheWriteArgs& a, const T* row, int64_t token,
-                                             int d, float (&v)[8]) {
-  load8<T, VEC>(row, d, v);
-  if (!a.pos || d < a.offset || d >= a.offset + a.rot) return;
+__device__ __forceinline__ void turn8(const CacheWriteArgs& a, const T* row, int64_t token, int d,
+                                      float (&v)[8]) {
+  if (d < a.offset || d >= a.offset + a.rot) return;
   const int r = d - a.offset, half = a.rot >> 1;
   const int32_t p = a.pos[token];
   if (a.inter) {
@@ -275,8 +287,10 @@ __device__ __forceinline__ void load8_turned(const CacheWriteArgs& a, const T* r
     }
   } else {
     const bool low = r < half;
+    Run8<T, VEC> mate;
+    mate.load(row + (low ? d + half : d - half));
     float w[8];
-    load8<T, VEC>(row, low ? d + half : d - half, w);
+    mate.get(w);
 #pragma unroll
     for (int j = 0; j < 8; ++j) {
       float2 cs = turn_of(p, a.freq[(low ? r : r - half) + j]);
@@ -287,75 +301,129 @@ __device__ __forceinline__ void load8_turned(const CacheWriteArgs& a, const T* r
   }
 }
 
-// 8 lanes take one chunk of 128 values of a row (two runs of 8 values a lane, 64
-// apart, so each access of the 8 lanes is one contiguous run); the group's largest
-// magnitude is a three-step exchange between them and the chunk is never reread.
-// A scale that is a power of two makes code * scale exact in bf16, so attention on the
-// tensor cores reads the quantised values without a second rounding; e4m3 being a
-// floating format, it costs at most one binade at the bottom of its range.
-template <typename T, bool VEC>
+// Codes of 8 values: f turns a value into its quotient by the scale.
+template <typename F>
+__device__ __forceinline__ uint2 codes8(const float (&v)[8], F f) {
+  uint32_t w[2];
+#pragma unroll
+  for (int h = 0; h < 2; ++h) {
+    const uint32_t lo = __nv_cvt_float2_to_fp8x2(make_float2(f(v[4 * h]), f(v[4 * h + 1])),
+                                                 __NV_SATFINITE, __NV_E4M3);
+    const uint32_t hi = __nv_cvt_float2_to_fp8x2(make_float2(f(v[4 * h + 2]), f(v[4 * h + 3])),
+                                                 __NV_SATFINITE, __NV_E4M3);
+    w[h] = lo | (hi << 16);
+  }
+  return make_uint2(w[0], w[1]);
+}
+
+// Scale of a group and its codes: two runs of 8 values a lane.
+__device__ __forceinline__ float quantise(const float (&v)[2][8], float amax, bool pow2,
+                                          uint2 (&code)[2]) {
+  float s = 1.f;
+  if (pow2) {
+    // amax = m 2^e with m in [1/2, 1), 448 = 0.875 2^9
+    int e;
+    const float m = frexpf(amax, &e);
+    e = amax > 3.0e38f ? 120 : max(m > 0.875f ? e - 8 : e - 9, -126);
+    float inv = 1.f;
+    if (amax > 0.f) {
+      s = __int_as_float((e + 127) << 23);
+      inv = __int_as_float((127 - e) << 23);         // 2^-e
+    }
+#pragma unroll
+    for (int h = 0; h < 2; ++h) code[h] = codes8(v[h], [&](float x) { return x * inv; });
+    return s;
+  }
+  if (amax > 0.f) s = __fdiv_rn(amax, 448.f);
+  if (s > 0x1p-90f && s < 0x1p90f) {
+    // The IEEE quotient by Markstein's method: from the correctly rounded reciprocal y,
+    // q = x y, its exact remainder r = x - q s, and q + r y rounds to x / s.  (Where x is so
+    // small that r is not exact, q is far below the smallest code.)
+    const float y = __frcp_rn(s);
+#pragma unroll
+    for (int h = 0; h < 2; ++h)
+      code[h] = codes8(v[h], [&](float x) {
+        const float q = x * y;
+        return fmaf(fmaf(-q, s, x), y, q);
+      });
+  } else {
+#pragma unroll
+    for (int h = 0; h < 2; ++h) code[h] = codes8(v[h], [&](float x) { return __fdiv_rn(x, s); });
+  }
+  return s;
+}
+
+// 8 lanes take a row and hold four chunks of 128 values of it at once (rows of less than
+// four chunks: one chunk of each of four rows), two runs of 8 values a lane, 64 apart, so
+// each access of the 8 lanes is one contiguous run; a group's largest magnitude is a
+// three-step exchange between them and nothing is reread.  A scale that is a power of two
+// makes code * scale exact in bf16, so attention on the tensor cores reads the quantised
+// values without a second rounding; e4m3 being a floating format, it costs at most one
+// binade at the bottom of its range.
+template <typename T, bool VEC, bool TURN, int ROWS>
 __global__ void __launch_bounds__(kCacheThreads) cache_write_kernel(const CacheWriteArgs a) {
-  const int l = threadIdx.x & 7;
-  const int chunks = a.c.dim_q / 128 + (a.c.dim_raw + 127) / 128;
-  const int64_t unit = (int64_t)blockIdx.x * kCacheUnits + (threadIdx.x >> 3);
-  const int64_t token = unit / chunks;
-  const int c = (int)(unit - token * chunks);
-  bool live = token < a.n_tokens;
-  int64_t slot = live ? a.slots[token] : -1;
-  live = slot >= 0 && (slot >> a.c.page_shift) < a.c.n_pages;
-  const int64_t page = slot >> a.c.page_shift;
-  const int64_t row = slot & ((1 << a.c.page_shift) - 1);
-  const T* x = reinterpret_cast<const T*>(a.x) + token * a.x_ts;
-  const int q_chunks = a.c.dim_q / 128;
-  if (c < q_chunks) {
-    float v[2][8];
-    float amax = 0.f;
-    if (live) {
+  constexpr int CHUNKS = kCacheBatch / ROWS;
+  const int l = threadIdx.x & 7, q_chunks = a.c.dim_q >> 7, width = a.c.dim_q + a.c.dim_raw;
+  const uint32_t mates = 0xffu << (threadIdx.x & 24);
+  const T* x[ROWS];
+  int64_t token[ROWS], page[ROWS];
+  int row[ROWS];
+#pragma unroll
+  for (int r = 0; r < ROWS; ++r) {
+    token[r] = ((int64_t)blockIdx.x * ROWS + r) * kCacheUnits + (threadIdx.x >> 3);
+    const int64_t slot = token[r] < a.n_tokens ? a.slots[token[r]] : -1;
+    page[r] = slot >> a.c.page_shift;                // -1 for a negative slot
+    row[r] = (int)slot & ((1 << a.c.page_shift) - 1);
+    if (slot < 0 || page[r] >= a.c.n_pages) page[r] = -1;
+    x[r] = reinterpret_cast<const T*>(a.x) + token[r] * a.x_ts;
+  }
+#pragma unroll 1
+  for (int c0 = 0; c0 < a.items; c0 += CHUNKS) {
+    Run8<T, VEC> held[kCacheBatch][2];
+#pragma unroll
+    for (int k = 0; k < kCacheBatch; ++k)
 #pragma unroll
       for (int h = 0; h < 2; ++h) {
-        load8_turned<T, VEC>(a, x, token, c * 128 + h * 64 + l * 8, v[h]);
-#pragma unroll
-        for (int j = 0; j < 8; ++j) amax = fmaxf(amax, fabsf(v[h][j]));
+        const int d = (c0 + k % CHUNKS) * 128 + h * 64 + l * 8;
+        if (page[k / CHUNKS] >= 0 && d < width) held[k][h].load(x[k / CHUNKS] + d);
       }
-    }
-    const uint32_t mates = 0xffu << (threadIdx.x & 24);
-    amax = fmaxf(amax, __shfl_xor_sync(mates, amax, 1));
-    amax = fmaxf(amax, __shfl_xor_sync(mates, amax, 2));
-    amax = fmaxf(amax, __shfl_xor_sync(mates, amax, 4));
-    if (!live) return;
-    float s = 1.f;
-    if (amax > 0.f) {
-      if (a.pow2) {
-        int e;
-        const float m = frexpf(amax, &e);            // amax = m 2^e, m in [1/2, 1)
-        e = m > 0.875f ? e - 8 : e - 9;              // 448 = 0.875 2^9
-        s = ldexpf(1.f, amax > 3.0e38f ? 120 : (e < -126 ? -126 : e));
+#pragma unroll
+    for (int k = 0; k < kCacheBatch; ++k) {
+      const int r = k / CHUNKS, c = c0 + k % CHUNKS;
+      if (page[r] < 0 || c >= a.items) continue;     // the same for the 8 lanes
+      float v[2][8];
+#pragma unroll
+      for (int h = 0; h < 2; ++h) {
+        held[k][h].get(v[h]);
+        if constexpr (TURN) {
+          const int d = c * 128 + h * 64 + l * 8;
+          if (d < width) turn8<T, VEC>(a, x[r], token[r], d, v[h]);
+        }
+      }
+      if (c < q_chunks) {
+        float amax = 0.f;
+#pragma unroll
+        for (int h = 0; h < 2; ++h)
+#pragma unroll
+          for (int j = 0; j < 8; ++j) amax = fmaxf(amax, fabsf(v[h][j]));
+        amax = fmaxf(amax, __shfl_xor_sync(mates, amax, 1));
+        amax = fmaxf(amax, __shfl_xor_sync(mates, amax, 2));
+        amax = fmaxf(amax, __shfl_xor_sync(mates, amax, 4));
+        uint2 code[2];
+        const float s = quantise(v, amax, a.pow2, code);
+        uint8_t* dst = a.c.codes + page[r] * a.c.codes_ps + (int64_t)row[r] * a.c.dim_q + c * 128;
+        *reinterpret_cast<uint2*>(dst + l * 8) = code[0];
+        *reinterpret_cast<uint2*>(dst + 64 + l * 8) = code[1];
+        if (l == 0) a.c.scale[page[r] * a.c.scale_ps + row[r] * q_chunks + c] = s;
       } else {
-        s = __fdiv_rn(amax, 448.f);
+        __nv_bfloat16* dst = a.c.raw + page[r] * a.c.raw_ps + (int64_t)row[r] * a.c.dim_raw;
+#pragma unroll
+        for (int h = 0; h < 2; ++h) {
+          const int d = (c - q_chunks) * 128 + h * 64 + l * 8;
+          if (d < a.c.dim_raw)
+            *reinterpret_cast<uint4*>(dst + d) = RowType<__nv_bfloat16>::pack(v[h]);
+        }
       }
-    }
-    uint8_t* dst = a.c.codes + page * a.c.codes_ps + row * a.c.dim_q + c * 128 + l * 8;
-    const float inv = __fdiv_rn(1.f, s);             // exact where s is a power of two
-#pragma unroll
-    for (int h = 0; h < 2; ++h) {
-      uint32_t w[2] = {0u, 0u};
-#pragma unroll
-      for (int j = 0; j < 8; ++j) {
-        const float u = a.pow2 ? v[h][j] * inv : __fdiv_rn(v[h][j], s);
-        w[j >> 2] |= (uint32_t)e4m3_rn_sat(u) << (8 * (j & 3));
-      }
-      *reinterpret_cast<uint2*>(dst + h * 64) = make_uint2(w[0], w[1]);
-    }
-    if (l == 0) a.c.scale[page * a.c.scale_ps + row * q_chunks + c] = s;
-  } else if (live) {
-    __nv_bfloat16* dst = a.c.raw + page * a.c.raw_ps + row * a.c.dim_raw;
-#pragma unroll
-    for (int h = 0; h < 2; ++h) {
-      const int d = (c - q_chunks) * 128 + h * 64 + l * 8;
-      if (d >= a.c.dim_raw) continue;
-      float v[8];
-      load8_turned<T, VEC>(a, x, token, a.c.dim_q + d, v);
-      *reinterpret_cast<uint4*>(dst + d) = RowType<__nv_bfloat16>::pack(v);
     }
   }
 }
@@ -398,74 +466,128 @@ __device__ __forceinline__ void store8(T* p, const float (&v)[8]) {
   }
 }
 
-// Values of a sequence's first n_k rows (those before its length; the rest of `out`
-// stays as it was).  8 lanes take one chunk of 128 values as in the write.
-template <typename T>
+// Rows of a sequence for 8 lanes: their pages, -1 behind the length (`out` stays as it
+// was there), -2 for a table entry outside the cache (zeros).
+template <int ROWS>
+__device__ __forceinline__ void rows_to_read(const CacheReadArgs& a, int (&s)[ROWS],
+                                             int (&page)[ROWS]) {
+  const int b = blockIdx.y;
+  const int len = a.k_len ? min(a.k_len[b], a.n_k) : a.n_k;
+  const int32_t* table = a.table + (int64_t)b * a.max_pages;
+#pragma unroll
+  for (int r = 0; r < ROWS; ++r) {
+    s[r] = (blockIdx.x * ROWS + r) * kCacheUnits + (threadIdx.x >> 3);
+    page[r] = -1;
+    if (s[r] < len) {
+      page[r] = page_of(table, s[r], a.c.page_shift, a.c.n_pages);
+      if (page[r] < 0) page[r] = -2;
+    }
+  }
+}
+
+// Values of a sequence's first n_k rows.  8 lanes take a row and hold four chunks of 128
+// values of it at once (or one chunk of each of four rows), 16 contiguous codes a lane.
+template <typename T, int ROWS>
 __global__ void __launch_bounds__(kCacheThreads) cache_read_kernel(const CacheReadArgs a) {
-  const int l = threadIdx.x & 7;
-  const int q_chunks = a.c.dim_q / 128;
-  const int chunks = q_chunks + (a.c.dim_raw + 127) / 128;
-  const int64_t unit = (int64_t)blockIdx.x * kCacheUnits + (threadIdx.x >> 3);
-  const int64_t r = unit / chunks;
-  const int c = (int)(unit - r * chunks);
-  const int b = (int)(r / a.n_k);
-  const int s = (int)(r - (int64_t)b * a.n_k);
-  if (b >= a.batch || (a.k_len && s >= a.k_len[b])) return;
-  const int32_t page = page_of(a.table + (int64_t)b * a.max_pages, s, a.c.page_shift, a.c.n_pages);
-  const int row = s & ((1 << a.c.page_shift) - 1);
-  T* out = reinterpret_cast<T*>(a.out) + r * (a.c.dim_q + a.c.dim_raw);
-  if (c < q_chunks) {
-    uint2 w[2] = {make_uint2(0, 0), make_uint2(0, 0)};
-    float sc = 1.f;
-    if (page >= 0) {
-      const uint8_t* src = a.c.codes + page * a.c.codes_ps + row * a.c.dim_q + c * 128 + l * 8;
-      w[0] = *reinterpret_cast<const uint2*>(src);
-      w[1] = *reinterpret_cast<const uint2*>(src + 64);
-      sc = a.c.scale[page * a.c.scale_ps + row * q_chunks + c];
+  constexpr int CHUNKS = kCacheBatch / ROWS;
+  const int l = threadIdx.x & 7, q_chunks = a.c.dim_q >> 7, width = a.c.dim_q + a.c.dim_raw;
+  int s[ROWS], page[ROWS];
+  rows_to_read<ROWS>(a, s, page);
+  const uint8_t* codes[ROWS];
+  const float* scale[ROWS];
+  const __nv_bfloat16* raw[ROWS];
+  T* out[ROWS];
+#pragma unroll
+  for (int r = 0; r < ROWS; ++r) {
+    const int64_t p = max(page[r], 0);
+    const int at = s[r] & ((1 << a.c.page_shift) - 1);
+    codes[r] = a.c.codes + p * a.c.codes_ps + (int64_t)at * a.c.dim_q + l * 16;
+    scale[r] = a.c.scale + p * a.c.scale_ps + at * q_chunks;
+    raw[r] = a.c.raw + p * a.c.raw_ps + (int64_t)at * a.c.dim_raw;
+    out[r] = reinterpret_cast<T*>(a.out) + ((int64_t)blockIdx.y * a.n_k + s[r]) * width;
+  }
+  const int q_last = q_chunks - q_chunks % CHUNKS;   // chunks that come in whole batches
+#pragma unroll 1
+  for (int c0 = 0; c0 < q_chunks; c0 += CHUNKS) {
+    uint4 w[kCacheBatch];
+    float sc[kCacheBatch];
+#pragma unroll
+    for (int k = 0; k < kCacheBatch; ++k) {
+      const int r = k / CHUNKS, c = c0 + k % CHUNKS;
+      w[k] = make_uint4(0, 0, 0, 0);
+      sc[k] = 1.f;
+      if (page[r] >= 0 && (c0 < q_last || c < q_chunks)) {
+        w[k] = *reinterpret_cast<const uint4*>(codes[r] + c * 128);
+        sc[k] = scale[r][c];
+      }
     }
 #pragma unroll
-    for (int h = 0; h < 2; ++h) {
-      float v[8];
-      e4m3x4_values(w[h].x, sc, v);
-      e4m3x4_values(w[h].y, sc, v + 4);
-      store8(out + c * 128 + h * 64 + l * 8, v);
-    }
-  } else {
+    for (int k = 0; k < kCacheBatch; ++k) {
+      const int r = k / CHUNKS, c = c0 + k % CHUNKS;
+      if (page[r] == -1 || c >= q_chunks) continue;
+      const uint32_t u[4] = {w[k].x, w[k].y, w[k].z, w[k].w};
 #pragma unroll
-    for (int h = 0; h < 2; ++h) {
-      const int d = (c - q_chunks) * 128 + h * 64 + l * 8;
-      if (d >= a.c.dim_raw) continue;
-      uint4 w = make_uint4(0, 0, 0, 0);
-      if (page >= 0)
-        w = *reinterpret_cast<const uint4*>(a.c.raw + page * a.c.raw_ps + row * a.c.dim_raw + d);
+      for (int h = 0; h < 2; ++h) {
+        float v[8];
+        e4m3x4_values(u[2 * h], sc[k], v);
+        e4m3x4_values(u[2 * h + 1], sc[k], v + 4);
+        store8(out[r] + c * 128 + l * 16 + h * 8, v);
+      }
+    }
+  }
+#pragma unroll 1
+  for (int d0 = l * 8; d0 < a.c.dim_raw; d0 += 64 * CHUNKS) {
+    uint4 w[kCacheBatch];
+#pragma unroll
+    for (int k = 0; k < kCacheBatch; ++k) {
+      const int r = k / CHUNKS, d = d0 + k % CHUNKS * 64;
+      w[k] = make_uint4(0, 0, 0, 0);
+      if (page[r] >= 0 && d < a.c.dim_raw) w[k] = *reinterpret_cast<const uint4*>(raw[r] + d);
+    }
+#pragma unroll
+    for (int k = 0; k < kCacheBatch; ++k) {
+      const int r = k / CHUNKS, d = d0 + k % CHUNKS * 64;
+      if (page[r] == -1 || d >= a.c.dim_raw) continue;
       float v[8];
-      RowType<__nv_bfloat16>::unpack(w, v);
-      store8(out + a.c.dim_q + d, v);
+      RowType<__nv_bfloat16>::unpack(w[k], v);
+      store8(out[r] + a.c.dim_q + d, v);
     }
   }
 }
 
 // Codes and scales as they stand (the operands of the indexer's e4m3 scan).
+template <int ROWS>
 __global__ void __launch_bounds__(kCacheThreads) cache_read_codes_kernel(const CacheReadArgs a) {
-  const int l = threadIdx.x & 7;
-  const int chunks = a.c.dim_q / 128;
-  const int64_t unit = (int64_t)blockIdx.x * kCacheUnits + (threadIdx.x >> 3);
-  const int64_t r = unit / chunks;
-  const int c = (int)(unit - r * chunks);
-  const int b = (int)(r / a.n_k);
-  const int s = (int)(r - (int64_t)b * a.n_k);
-  if (b >= a.batch || (a.k_len && s >= a.k_len[b])) return;
-  const int32_t page = page_of(a.table + (int64_t)b * a.max_pages, s, a.c.page_shift, a.c.n_pages);
-  const int row = s & ((1 << a.c.page_shift) - 1);
-  uint4 w = make_uint4(0, 0, 0, 0);
-  float sc = 1.f;
-  if (page >= 0) {
-    w = *reinterpret_cast<const uint4*>(a.c.codes + page * a.c.codes_ps + row * a.c.dim_q +
-                                        c * 128 + l * 16);
-    sc = a.c.scale[page * a.c.scale_ps + row * chunks + c];
+  constexpr int CHUNKS = kCacheBatch / ROWS;
+  const int l = threadIdx.x & 7, q_chunks = a.c.dim_q >> 7;
+  int s[ROWS], page[ROWS];
+  rows_to_read<ROWS>(a, s, page);
+#pragma unroll 1
+  for (int c0 = 0; c0 < q_chunks; c0 += CHUNKS) {
+    uint4 w[kCacheBatch];
+    float sc[kCacheBatch];
+#pragma unroll
+    for (int k = 0; k < kCacheBatch; ++k) {
+      const int r = k / CHUNKS, c = c0 + k % CHUNKS;
+      w[k] = make_uint4(0, 0, 0, 0);
+      sc[k] = 1.f;
+      if (page[r] >= 0 && c < q_chunks) {
+        const int at = s[r] & ((1 << a.c.page_shift) - 1);
+        w[k] = *reinterpret_cast<const uint4*>(a.c.codes + page[r] * a.c.codes_ps +
+                                               (int64_t)at * a.c.dim_q + c * 128 + l * 16);
+        sc[k] = a.c.scale[page[r] * a.c.scale_ps + at * q_chunks + c];
+      }
+    }
+#pragma unroll
+    for (int k = 0; k < kCacheBatch; ++k) {
+      const int r = k / CHUNKS, c = c0 + k % CHUNKS;
+      if (page[r] == -1 || c >= q_chunks) continue;
+      const int64_t to = (int64_t)blockIdx.y * a.n_k + s[r];
+      *reinterpret_cast<uint4*>(reinterpret_cast<uint8_t*>(a.out) + to * a.c.dim_q + c * 128 +
+                                l * 16) = w[k];
+      if (l == 0) a.out_scale[to * q_chunks + c] = sc[k];
+    }
   }
-  *reinterpret_cast<uint4*>(reinterpret_cast<uint8_t*>(a.out) + r * a.c.dim_q + c * 128 + l * 16) = w;
-  if (l == 0) a.out_scale[r * chunks + c] = sc;
 }
 
 }  // namespace dsa

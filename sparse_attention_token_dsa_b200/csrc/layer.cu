@@ -38,6 +38,8 @@ int launch_rope(RopeArgs& a, int dim, bool vec, bool inter, bool in_place, cudaS
   const int n = vec ? RowType<T>::kVec : 1;
   a.pairs = vec && inter ? a.rot / n : a.rot / 2 / n;
   a.units = a.pairs + (in_place ? 0 : (dim - a.rot) / n);
+  // exact for the numbers below 2^17 that a block divides (see launch_rope's limits)
+  a.per_unit = a.units > 1 ? (uint32_t)((0x100000000ull + a.units - 1) / a.units) : 0;
   // a block takes about 1024 units (four a thread): several tokens of few heads, or a
   // part of one token's heads
   const int64_t per_token = (int64_t)a.heads * a.units;
@@ -114,18 +116,34 @@ CachePlanes planes(const dsa_cache* c) {
 
 int chunks_of(const dsa_cache* c) { return c->dim_q / 128 + (c->dim_raw + 127) / 128; }
 
-// Arguments shared by the two reads; *blocks: the grid (0: nothing to read).
+// Rows that 8 lanes hold at once: four chunks are in flight either way.
+bool few_chunks(int chunks) { return chunks < 4; }
+unsigned row_blocks(int64_t rows, bool few) {
+  const int span = kCacheUnits * (few ? 4 : 1);
+  return (unsigned)((rows + span - 1) / span);
+}
+
+typedef void (*WriteKernel)(const CacheWriteArgs);
+template <typename T>
+WriteKernel write_kernel(bool vec, bool turn, bool few) {
+  if (few)
+    return vec ? (turn ? cache_write_kernel<T, true, true, 4> : cache_write_kernel<T, true, false, 4>)
+               : (turn ? cache_write_kernel<T, false, true, 4> : cache_write_kernel<T, false, false, 4>);
+  return vec ? (turn ? cache_write_kernel<T, true, true, 1> : cache_write_kernel<T, true, false, 1>)
+             : (turn ? cache_write_kernel<T, false, true, 1> : cache_write_kernel<T, false, false, 1>);
+}
+
+// Arguments shared by the two reads; *grid: x is 0 where there is nothing to read.
 int read_args(const dsa_cache* c, const int32_t* table, int32_t batch, int32_t max_pages,
-              int32_t n_k, const int32_t* k_len, void* out, int chunks, CacheReadArgs* a,
-              unsigned* blocks) {
+              int32_t n_k, const int32_t* k_len, void* out, bool few, CacheReadArgs* a,
+              dim3* grid) {
   const int v = validate_cache(c);
   if (v != DSA_OK) return v;
   if (!table || !out || batch < 1 || n_k < 0 || max_pages < 0) return DSA_ERR_INVALID;
   if (!aligned(table, 4) || !aligned(k_len, 4)) return DSA_ERR_INVALID;
   if ((int64_t)max_pages * c->page_size < n_k || !aligned16(out)) return DSA_ERR_INVALID;
-  const int64_t n = ((int64_t)batch * n_k * chunks + kCacheUnits - 1) / kCacheUnits;
-  if (n > 0x7fffffffll) return DSA_ERR_UNSUPPORTED;
-  *blocks = (unsigned)n;
+  if (batch > 65535 || n_k > (1 << 30)) return DSA_ERR_UNSUPPORTED;
+  *grid = dim3(row_blocks(n_k, few), (unsigned)batch);
   a->c = planes(c);
   a->table = table;
   a->k_len = k_len;
@@ -330,15 +348,14 @@ int dsa_cache_write(const dsa_cache* c, const void* x, int32_t x_dtype, int64_t 
     a.sign = rope->flags & DSA_FLAG_INVERSE ? -1.f : 1.f;
   }
   a.pow2 = (flags & DSA_FLAG_POW2_SCALE) != 0;
-  const int64_t blocks = (n_tokens * chunks_of(c) + kCacheUnits - 1) / kCacheUnits;
-  if (n_tokens > (1ll << 40) || blocks > 0x7fffffffll) return DSA_ERR_UNSUPPORTED;
+  if (n_tokens > 0x7fffffffll) return DSA_ERR_UNSUPPORTED;
+  a.items = chunks_of(c);
+  const bool few = few_chunks(a.items);
   const bool vec = aligned16(x) && x_stride % (int64_t)(16 / esz) == 0;
   cudaStream_t st = reinterpret_cast<cudaStream_t>(stream);
-  void (*kern)(const CacheWriteArgs) =
-      x_dtype == DSA_BF16
-          ? (vec ? cache_write_kernel<__nv_bfloat16, true> : cache_write_kernel<__nv_bfloat16, false>)
-          : (vec ? cache_write_kernel<float, true> : cache_write_kernel<float, false>);
-  kern<<<(unsigned)blocks, kCacheThreads, 0, st>>>(a);
+  auto kern = x_dtype == DSA_BF16 ? write_kernel<__nv_bfloat16>(vec, rope != nullptr, few)
+                                  : write_kernel<float>(vec, rope != nullptr, few);
+  kern<<<row_blocks(n_tokens, few), kCacheThreads, 0, st>>>(a);
   return launch_status();
 }
 
@@ -346,17 +363,18 @@ int dsa_cache_read(const dsa_cache* c, const int32_t* block_table, int32_t batch
                    int32_t max_pages, int32_t n_k, const int32_t* k_len, void* out,
                    int32_t out_dtype, void* stream) {
   CacheReadArgs a{};
-  unsigned blocks = 0;
-  const int v = read_args(c, block_table, batch, max_pages, n_k, k_len, out,
-                          c ? chunks_of(c) : 0, &a, &blocks);
+  dim3 blocks;
+  const bool few = c && few_chunks(chunks_of(c));
+  const int v = read_args(c, block_table, batch, max_pages, n_k, k_len, out, few, &a,
+                          &blocks);
   if (v != DSA_OK) return v;
   if (out_dtype != DSA_BF16 && out_dtype != DSA_F32) return DSA_ERR_UNSUPPORTED;
-  if (blocks == 0) return DSA_OK;
+  if (blocks.x == 0) return DSA_OK;
   cudaStream_t st = reinterpret_cast<cudaStream_t>(stream);
-  if (out_dtype == DSA_BF16)
-    cache_read_kernel<__nv_bfloat16><<<blocks, kCacheThreads, 0, st>>>(a);
-  else
-    cache_read_kernel<float><<<blocks, kCacheThreads, 0, st>>>(a);
+  auto kern = out_dtype == DSA_BF16
+                  ? (few ? cache_read_kernel<__nv_bfloat16, 4> : cache_read_kernel<__nv_bfloat16, 1>)
+                  : (few ? cache_read_kernel<float, 4> : cache_read_kernel<float, 1>);
+  kern<<<blocks, kCacheThreads, 0, st>>>(a);
   return launch_status();
 }
 
@@ -364,15 +382,17 @@ int dsa_cache_read_codes(const dsa_cache* c, const int32_t* block_table, int32_t
                          int32_t max_pages, int32_t n_k, const int32_t* k_len, void* out,
                          float* out_scale, void* stream) {
   CacheReadArgs a{};
-  unsigned blocks = 0;
-  const int v = read_args(c, block_table, batch, max_pages, n_k, k_len, out,
-                          c ? c->dim_q / 128 : 0, &a, &blocks);
+  dim3 blocks;
+  const bool few = c && few_chunks(chunks_of(c));
+  const int v = read_args(c, block_table, batch, max_pages, n_k, k_len, out, few, &a,
+                          &blocks);
   if (v != DSA_OK) return v;
   if (!out_scale || !aligned(out_scale, 4) || c->dim_q == 0) return DSA_ERR_INVALID;
   if (c->dim_raw) return DSA_ERR_UNSUPPORTED;
-  if (blocks == 0) return DSA_OK;
+  if (blocks.x == 0) return DSA_OK;
   a.out_scale = out_scale;
-  cache_read_codes_kernel<<<blocks, kCacheThreads, 0, reinterpret_cast<cudaStream_t>(stream)>>>(a);
+  auto kern = few ? cache_read_codes_kernel<4> : cache_read_codes_kernel<1>;
+  kern<<<blocks, kCacheThreads, 0, reinterpret_cast<cudaStream_t>(stream)>>>(a);
   return launch_status();
 }
 
