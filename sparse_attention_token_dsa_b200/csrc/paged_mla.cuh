@@ -51,6 +51,9 @@ struct PmRing {
   static constexpr int kVSlots = CODES ? 2 : 4;      // slices of V
   static constexpr int kKBytes = kChunks * kPmChunk;
   static constexpr int kCodes = CODES ? 4 * 8192 : 0;   // of K, and of V
+  // Chunk of q that meets the k-th chunk of K: in e4m3 the bf16 chunk comes first, as it
+  // needs no conversion.
+  __device__ __forceinline__ static int q_chunk(int k) { return CODES ? (k == 0 ? 8 : k - 1) : k; }
 };
 constexpr int kPmQBytes = 9 * 64 * 128;
 constexpr int kPmPBytes = 2 * 64 * 128;
@@ -223,20 +226,22 @@ __device__ __forceinline__ void tmem_st8(uint32_t taddr, const uint32_t (&r)[8])
 // 16 e4m3 codes times a scale as bf16.  A code's exponent and mantissa, moved to where
 // bf16 has its own, are the value times 2^-120 (also for e4m3's subnormal codes, which
 // become bf16's), so one packed product with 2^120 scale gives two values, exactly, where
-// the scale is a power of two of at most 2^7: five instructions for two codes and none of
-// them a conversion (those run at a quarter of the rate).
+// the scale is a power of two of at most 2^7: five instructions for two codes, none of
+// them a conversion (those run at a quarter of the rate) and only two of them for the
+// integer units: with a code in the lower byte of a half, 16 t moves all of it and leaves
+// the sign at bit 11, and 240 (t & 0x80) = 2^15 - 2^11 carries that on to bit 15.
 __device__ __forceinline__ uint32_t two_codes(uint32_t w, uint32_t sel, uint32_t mul) {
-  const uint32_t t = __byte_perm(w, 0, sel);         // a code in the upper byte of each half
-  const uint32_t v = ((t >> 4) & 0x07f007f0u) | (t & 0x80008000u);
+  const uint32_t t = __byte_perm(w, 0, sel);
+  const uint32_t v = t * 16u + (t & 0x00800080u) * 240u;
   uint32_t r;
   asm("mul.rn.bf16x2 %0, %1, %2;" : "=r"(r) : "r"(v), "r"(mul));
   return r;
 }
 __device__ __forceinline__ void codes_to_bf16(const uint4& w, uint32_t mul, uint4& lo, uint4& hi) {
-  lo = make_uint4(two_codes(w.x, 0x1404, mul), two_codes(w.x, 0x3424, mul),
-                  two_codes(w.y, 0x1404, mul), two_codes(w.y, 0x3424, mul));
-  hi = make_uint4(two_codes(w.z, 0x1404, mul), two_codes(w.z, 0x3424, mul),
-                  two_codes(w.w, 0x1404, mul), two_codes(w.w, 0x3424, mul));
+  lo = make_uint4(two_codes(w.x, 0x4140, mul), two_codes(w.x, 0x4342, mul),
+                  two_codes(w.y, 0x4140, mul), two_codes(w.y, 0x4342, mul));
+  hi = make_uint4(two_codes(w.z, 0x4140, mul), two_codes(w.z, 0x4342, mul),
+                  two_codes(w.w, 0x4140, mul), two_codes(w.w, 0x4342, mul));
 }
 // 2^120 scale in both halves; 0 where the short way does not hold.
 __device__ __forceinline__ uint32_t code_factor(float scale) {
@@ -245,27 +250,53 @@ __device__ __forceinline__ uint32_t code_factor(float scale) {
   const uint32_t h = (u >> 16) + (120u << 7);
   return h | (h << 16);
 }
-// Any scale: in fp32, rounded to bf16 once.
-__device__ __noinline__ void codes_to_bf16_any(const uint4* w, float scale, uint4* lo, uint4* hi) {
-  if (scale == 0.f) {                                // a row past the end: also NaN codes
-    *lo = *hi = make_uint4(0, 0, 0, 0);
-    return;
+// Any scale: four units, in fp32, rounded to bf16 once (out of line, for scales that
+// dsa_cache_write does not make).
+__device__ __noinline__ void four_units_any(const uint8_t* const* from, uint8_t* const* to_lo,
+                                            uint8_t* const* to_hi, float scale) {
+#pragma unroll 1
+  for (int u = 0; u < 4; ++u) {
+    const uint4 w = *reinterpret_cast<const uint4*>(from[u]);
+    float v[16];
+    e4m3x4_values(w.x, scale, v);
+    e4m3x4_values(w.y, scale, v + 4);
+    e4m3x4_values(w.z, scale, v + 8);
+    e4m3x4_values(w.w, scale, v + 12);
+    if (scale == 0.f) {                              // a row past the end: also NaN codes
+#pragma unroll
+      for (int j = 0; j < 16; ++j) v[j] = 0.f;
+    }
+    *reinterpret_cast<uint4*>(to_lo[u]) =
+        make_uint4(bf16x2(v[0], v[1]), bf16x2(v[2], v[3]), bf16x2(v[4], v[5]), bf16x2(v[6], v[7]));
+    *reinterpret_cast<uint4*>(to_hi[u]) = make_uint4(
+        bf16x2(v[8], v[9]), bf16x2(v[10], v[11]), bf16x2(v[12], v[13]), bf16x2(v[14], v[15]));
   }
-  float v[16];
-  e4m3x4_values(w->x, scale, v);
-  e4m3x4_values(w->y, scale, v + 4);
-  e4m3x4_values(w->z, scale, v + 8);
-  e4m3x4_values(w->w, scale, v + 12);
-  *lo = make_uint4(bf16x2(v[0], v[1]), bf16x2(v[2], v[3]), bf16x2(v[4], v[5]), bf16x2(v[6], v[7]));
-  *hi = make_uint4(bf16x2(v[8], v[9]), bf16x2(v[10], v[11]), bf16x2(v[12], v[13]),
-                   bf16x2(v[14], v[15]));
 }
-__device__ __forceinline__ void codes_to_bf16_far(const uint4& w, float scale, uint4& lo, uint4& hi) {
-  const uint4 w1 = w;
-  uint4 a, b;
-  codes_to_bf16_any(&w1, scale, &a, &b);
-  lo = a;
-  hi = b;
+// Four units of 16 codes in shared memory: from(u), to_lo(u), to_hi(u).
+template <typename From, typename To>
+__device__ __forceinline__ void four_units(bool exact, uint32_t f, float scale, From from, To to) {
+  if (exact) {
+    uint4 w[4];
+#pragma unroll
+    for (int u = 0; u < 4; ++u) w[u] = *reinterpret_cast<const uint4*>(from(u));
+#pragma unroll
+    for (int u = 0; u < 4; ++u) {
+      uint4 lo, hi;
+      codes_to_bf16(w[u], f, lo, hi);
+      *reinterpret_cast<uint4*>(to(u, 0)) = lo;
+      *reinterpret_cast<uint4*>(to(u, 1)) = hi;
+    }
+  } else {
+    const uint8_t* a[4];
+    uint8_t *b[4], *c[4];
+#pragma unroll
+    for (int u = 0; u < 4; ++u) {
+      a[u] = from(u);
+      b[u] = to(u, 0);
+      c[u] = to(u, 1);
+    }
+    four_units_any(a, b, c, scale);
+  }
 }
 
 __device__ __forceinline__ void tma_load_4d(void* dst, const CUtensorMap* map, uint64_t* bar,
@@ -321,12 +352,12 @@ __global__ void __cluster_dims__(2, 1, 1)
     }
     for (int i = 0; i < 4; ++i) {
       mbar_init(&T->v_full[i], 1);
-      mbar_init(&T->v_ready[i], CODES ? 2 * kPmLoaders : 2);
+      mbar_init(&T->v_ready[i], CODES ? 4 : 2);
       mbar_init(&T->v_empty[i], 1);
       mbar_init(&T->codes_full[0][i], 1);
       mbar_init(&T->codes_full[1][i], 1);
       mbar_init(&T->codes_empty[0][i], 2);
-      mbar_init(&T->codes_empty[1][i], kPmLoaders);
+      mbar_init(&T->codes_empty[1][i], 2);
     }
     for (int i = 0; i < 2; ++i) {
       mbar_init(&T->s_full[i], 1);
@@ -440,7 +471,7 @@ __global__ void __cluster_dims__(2, 1, 1)
               for (int c = 0; c < Ring::kChunks; ++c)
 #pragma unroll
                 for (int kk = 0; kk < 4; ++kk)       // 16 values
-                  pair_mma_bf16(d, q_desc + (((k + c) * kPmChunk + kk * 32) >> 4),
+                  pair_mma_bf16(d, q_desc + ((Ring::q_chunk(k + c) * kPmChunk + kk * 32) >> 4),
                                 k_desc + ((cur * Ring::kKBytes + c * kPmChunk + kk * 32) >> 4),
                                 idesc, (k | c | kk) != 0);
               pair_commit(&T->k_empty[cur]);
@@ -625,52 +656,54 @@ __global__ void __cluster_dims__(2, 1, 1)
         }
       }
     } else if (warp == 6) {
-      // e4m3: codes of K, in 4 groups of 128 of 64 positions
+      // e4m3: codes of K, in 4 groups of 128 of 64 positions, and the bf16 chunk of K,
+      // straight into its slot
       if (elect_one()) {
-        const int rows = min(1 << shift, 64);        // of a copy
+        const int rows = min(1 << shift, 64), tail_rows = min(1 << shift, 32);   // of a copy
+        auto group = [&](int key, int g) -> bool {
+          if (!wait(&T->codes_empty[0][g], (n & 1) ^ 1, 62)) return false;
+          mbar_arrive_expect_tx(&T->codes_full[0][g], 8192);
+#pragma unroll 1
+          for (int j = 0; j < 64; j += rows)
+            tma_load_3d(Kc + g * 8192 + j * 128, &kmap, &T->codes_full[0][g], g * 128,
+                        (key + j) & mask, page_at(key + j));
+          return true;
+        };
+        uint32_t tails = 0;
         while (ok && pm_next(a, walk, s)) {
           table = a.table + (int64_t)s.pair.b * a.max_pages;
 #pragma unroll 1
           for (int i = s.t0; i < s.t0 + s.n && ok; ++i, ++n) {
             const int key = i * kPmKeys + 64 * rank;
+            ok = group(key, 0) && group(key, 1);
+            const uint32_t u = n * 9, slot = u % Ring::kKSlots, use = u / Ring::kKSlots;
+            // Uses of a slot lie 5 chunks apart and these 9: the parity below tells the last
+            // use from the one before only once the tile before the last has been read.
+            if (n > 1) ok = ok && wait(&T->s_full[n & 1], ((n >> 1) & 1) ^ 1, 61);
+            ok = ok && wait(&T->k_empty[slot], (use & 1) ^ 1, 62);
+            if (!ok) break;
+            mbar_arrive_expect_tx(&T->k_full[0], kPmChunk);
 #pragma unroll 1
-            for (int g = 0; g < 4; ++g) {
-              ok = wait(&T->codes_empty[0][g], (n & 1) ^ 1, 62);
-              if (!ok) break;
-              mbar_arrive_expect_tx(&T->codes_full[0][g], 8192);
-#pragma unroll 1
-              for (int j = 0; j < 64; j += rows)
-                tma_load_3d(Kc + g * 8192 + j * 128, &kmap, &T->codes_full[0][g], g * 128,
-                            (key + j) & mask, page_at(key + j));
-            }
+            for (int j = 0; j < 64; j += tail_rows)
+              tma_load_3d(Ks + slot * kPmChunk + j * 128, &rmap, &T->k_full[0], 0,
+                          (key + j) & mask, page_at(key + j));
+            ++tails;
+            ok = group(key, 2) && group(key, 3);
           }
         }
+        if (!ok && tails) drain_slot(&T->k_full[0], tails);
         for (int g = 0; g < 4 && n; ++g)
           if (ok) wait(&T->codes_empty[0][g], (n & 1) ^ 1, 64);
           else drain_slot(&T->codes_full[0][g], n);
       }
     } else if (warp == 7) {
-      // the bf16 chunk of K, straight into its slot, and the codes of V, in slices of 32
-      // positions
+      // the codes of V, in slices of 32 positions
       if (elect_one()) {
         const int rows = min(1 << shift, 32);
         while (ok && pm_next(a, walk, s)) {
           table = a.table + (int64_t)s.pair.b * a.max_pages;
 #pragma unroll 1
           for (int i = s.t0; i < s.t0 + s.n && ok; ++i, ++n) {
-            const uint32_t u = n * 9 + 8, slot = u % Ring::kKSlots, use = u / Ring::kKSlots;
-            // Uses of a slot lie 5 chunks apart and these 9: the parity below tells the last
-            // use from the one before only once the tile before has been read.
-            if (n) ok = wait(&T->s_full[(n - 1) & 1], ((n - 1) >> 1) & 1, 61);
-            ok = ok && wait(&T->k_empty[slot], (use & 1) ^ 1, 62);
-            if (!ok) break;
-            mbar_arrive_expect_tx(&T->k_full[0], kPmChunk);
-#pragma unroll 1
-            for (int j = 0; j < 64; j += rows) {
-              const int key = i * kPmKeys + 64 * rank + j;
-              tma_load_3d(Ks + slot * kPmChunk + j * 128, &rmap, &T->k_full[0], 0, key & mask,
-                          page_at(key));
-            }
 #pragma unroll 1
             for (int v = 0; v < 4; ++v) {
               ok = wait(&T->codes_empty[1][v], (n & 1) ^ 1, 63);
@@ -688,7 +721,6 @@ __global__ void __cluster_dims__(2, 1, 1)
             }
           }
         }
-        if (!ok) drain_slot(&T->k_full[0], n);
         for (int v = 0; v < 4 && n; ++v)
           if (ok) wait(&T->codes_empty[1][v], (n & 1) ^ 1, 65);
           else drain_slot(&T->codes_full[1][v], n);
@@ -705,15 +737,6 @@ __global__ void __cluster_dims__(2, 1, 1)
         fence_proxy_async_smem();
         __syncwarp();
         if (lane == 0) mbar_arrive_cluster(bar);
-      };
-      // 16 values: two 16-byte units of a swizzled row
-      auto put = [&](uint8_t* row_at, int row, int unit, bool exact, const uint4& w, uint32_t f,
-                     float scale) {
-        uint4 lo, hi;
-        if (exact) codes_to_bf16(w, f, lo, hi);
-        else codes_to_bf16_far(w, scale, lo, hi);
-        *reinterpret_cast<uint4*>(row_at + ((unit ^ (row & 7)) << 4)) = lo;
-        *reinterpret_cast<uint4*>(row_at + (((unit + 1) ^ (row & 7)) << 4)) = hi;
       };
       if (warp < 8 + kPmLoaders) {
         // K: a warp takes every fourth chunk, a lane two of its rows
@@ -752,6 +775,12 @@ __global__ void __cluster_dims__(2, 1, 1)
             }
             if (i + 1 < s.n) load(s.t0 + i + 1);
             if (i + 2 < s.n) look(s.t0 + i + 2);
+            if (w == 0) {                            // the tile's bf16 chunk has landed
+              ok = wait(&T->k_full[0], n & 1, 60);
+              ok = __all_sync(0xffffffffu, ok);
+              if (!ok) break;
+              if (lane == 0) mbar_arrive_cluster(k_ready + (n * 9 % Ring::kKSlots) * 8);
+            }
 #pragma unroll 1
             for (int j = 0; j < 2; ++j) {
               const int c = w + 4 * j, g = c >> 1;
@@ -759,35 +788,22 @@ __global__ void __cluster_dims__(2, 1, 1)
               const uint32_t f0 = code_factor(s0), f1 = code_factor(s1);
               const bool exact =
                   __all_sync(0xffffffffu, (f0 != 0 || !(on & 1)) && (f1 != 0 || !(on & 2)));
-              ok = ok && wait(&T->codes_full[0][g], n & 1, 59);
+              const uint32_t use = n * 9 + 1 + c, slot = use % Ring::kKSlots;
+              ok = ok && wait(&T->codes_full[0][g], n & 1, 59) &&
+                   wait(&T->k_empty[slot], ((use / Ring::kKSlots) & 1) ^ 1, 62);
               ok = __all_sync(0xffffffffu, ok);
               if (!ok) break;
-              uint4 code[8];
-#pragma unroll
-              for (int h = 0; h < 2; ++h)
-#pragma unroll
-                for (int u = 0; u < 4; ++u) {
-                  const int row = h * 32 + lane;
-                  code[4 * h + u] = *reinterpret_cast<const uint4*>(
-                      Kc + g * 8192 + row * 128 + ((((c & 1) * 4 + u) ^ (row & 7)) << 4));
-                }
-              const uint32_t use = n * 9 + c, slot = use % Ring::kKSlots;
-              ok = wait(&T->k_empty[slot], ((use / Ring::kKSlots) & 1) ^ 1, 62);
-              ok = __all_sync(0xffffffffu, ok);
-              if (!ok) break;
-#pragma unroll
-              for (int h = 0; h < 2; ++h)
-#pragma unroll
-                for (int u = 0; u < 4; ++u)
-                  put(Ks + slot * kPmChunk + (h * 32 + lane) * 128, lane, 2 * u, exact,
-                      code[4 * h + u], h ? f1 : f0, h ? s1 : s0);
+#pragma unroll 1
+              for (int h = 0; h < 2; ++h) {          // row h * 32 + lane
+                const uint8_t* from = Kc + g * 8192 + (h * 32 + lane) * 128;
+                uint8_t* to = Ks + slot * kPmChunk + (h * 32 + lane) * 128;
+                four_units(
+                    exact, h ? f1 : f0, h ? s1 : s0,
+                    [&](int u) { return from + ((((c & 1) * 4 + u) ^ (lane & 7)) << 4); },
+                    [&](int u, int e) { return to + (((2 * u + e) ^ (lane & 7)) << 4); });
+              }
               ready(k_ready + slot * 8);
               if (lane == 0) mbar_arrive(&T->codes_empty[0][g]);
-            }
-            if (w == 0 && ok) {                      // the tile's bf16 chunk has landed
-              ok = wait(&T->k_full[0], n & 1, 60);
-              ok = __all_sync(0xffffffffu, ok);
-              if (ok && lane == 0) mbar_arrive_cluster(k_ready + ((n * 9 + 8) % Ring::kKSlots) * 8);
             }
           }
         }
@@ -798,24 +814,26 @@ __global__ void __cluster_dims__(2, 1, 1)
             wait(&T->k_empty[i], (uses & 1) ^ 1, 64);
           }
       } else {
-        // V: the four warps share a slice, four lanes a row
-        const int w = warp - 8 - kPmLoaders, vrow = w * 8 + (lane >> 2), vu = lane & 3;
+        // V: two warps take every second slice, two lanes a row
+        const int w = warp - 8 - kPmLoaders, odd = w >> 1;
+        const int vrow = (w & 1) * 16 + (lane >> 1), vu = lane & 1;
         const uint32_t v_ready = in_cta(&T->v_ready[0], 0);
-        int page[4];
-        float next[4][2];
-        uint32_t live = 0;                           // bit v: the row of next[v] is one
+        int page[2];
+        float next[2][2];                            // [slice odd, odd + 2][group]
+        uint32_t live = 0;                           // bit: the row of `next` is one
         auto look = [&](int tile) {
 #pragma unroll
-          for (int v = 0; v < 4; ++v) page[v] = page_at(tile * kPmKeys + v * 32 + vrow);
+          for (int j = 0; j < 2; ++j) page[j] = page_at(tile * kPmKeys + (odd + 2 * j) * 32 + vrow);
         };
         auto load = [&](int tile) {
           live = 0;
 #pragma unroll
-          for (int v = 0; v < 4; ++v) {
-            const float* sc = scales(page[v], tile * kPmKeys + v * 32 + vrow) + rank * 2;
-            next[v][0] = sc[0];
-            next[v][1] = sc[1];
-            live |= (page[v] < a.c.n_pages ? 1u : 0u) << v;
+          for (int j = 0; j < 2; ++j) {
+            const float* sc =
+                scales(page[j], tile * kPmKeys + (odd + 2 * j) * 32 + vrow) + rank * 2;
+            next[j][0] = sc[0];
+            next[j][1] = sc[1];
+            live |= (page[j] < a.c.n_pages ? 1u : 0u) << j;
           }
         };
         while (ok && pm_next(a, walk, s)) {
@@ -825,39 +843,39 @@ __global__ void __cluster_dims__(2, 1, 1)
           if (s.n > 1) look(s.t0 + 1);
 #pragma unroll 1
           for (int i = 0; i < s.n && ok; ++i, ++n) {
-            float now[4][2];
+            float now[2][2];
             const uint32_t on = live;
 #pragma unroll
-            for (int v = 0; v < 4; ++v) {
-              now[v][0] = on >> v & 1 ? next[v][0] : 0.f;
-              now[v][1] = on >> v & 1 ? next[v][1] : 0.f;
+            for (int j = 0; j < 2; ++j) {
+              now[j][0] = on >> j & 1 ? next[j][0] : 0.f;
+              now[j][1] = on >> j & 1 ? next[j][1] : 0.f;
             }
             if (i + 1 < s.n) load(s.t0 + i + 1);
             if (i + 2 < s.n) look(s.t0 + i + 2);
 #pragma unroll 1
-            for (int v = 0; v < 4; ++v) {
-              const float s0 = v & 2 ? (v & 1 ? now[3][0] : now[2][0]) : (v & 1 ? now[1][0] : now[0][0]);
-              const float s1 = v & 2 ? (v & 1 ? now[3][1] : now[2][1]) : (v & 1 ? now[1][1] : now[0][1]);
+            for (int j = 0; j < 2; ++j) {
+              const int v = odd + 2 * j;
+              const float s0 = j ? now[1][0] : now[0][0], s1 = j ? now[1][1] : now[0][1];
               const uint32_t f0 = code_factor(s0), f1 = code_factor(s1);
-              const bool exact = __all_sync(0xffffffffu, (f0 && f1) || !(on >> v & 1));
-              ok = ok && wait(&T->codes_full[1][v], n & 1, 60);
+              const bool exact = __all_sync(0xffffffffu, (f0 && f1) || !(on >> j & 1));
+              // both uses of a slot in a tile are these two warps'
+              ok = ok && wait(&T->codes_full[1][v], n & 1, 60) && wait(&T->v_empty[odd], j ^ 1, 63);
               ok = __all_sync(0xffffffffu, ok);
               if (!ok) break;
-              uint4 code[4];
-#pragma unroll
-              for (int h = 0; h < 4; ++h)
-                code[h] = *reinterpret_cast<const uint4*>(
-                    Vc + v * 8192 + (h >> 1) * 4096 + vrow * 128 +
-                    (((vu + 4 * (h & 1)) ^ (vrow & 7)) << 4));
-              const uint32_t use = n * 4 + v, slot = use % Ring::kVSlots;
-              ok = wait(&T->v_empty[slot], ((use / Ring::kVSlots) & 1) ^ 1, 63);
-              ok = __all_sync(0xffffffffu, ok);
-              if (!ok) break;
-#pragma unroll
-              for (int h = 0; h < 4; ++h)            // block of 64 values
-                put(Vs + slot * kPmSlice + h * 4096 + vrow * 128, vrow, 2 * vu, exact, code[h],
-                    h < 2 ? f0 : f1, h < 2 ? s0 : s1);
-              ready(v_ready + slot * 8);
+#pragma unroll 1
+              for (int h = 0; h < 2; ++h) {          // group: units 4 (u / 2) + 2 vu + u % 2
+                const uint8_t* from = Vc + v * 8192 + h * 4096 + vrow * 128;
+                uint8_t* to = Vs + odd * kPmSlice + h * 8192 + vrow * 128;
+                four_units(
+                    exact, h ? f1 : f0, h ? s1 : s0,
+                    [&](int u) {
+                      return from + (((2 * vu + (u & 1) + 4 * (u >> 1)) ^ (vrow & 7)) << 4);
+                    },
+                    [&](int u, int e) {
+                      return to + (u >> 1) * 4096 + (((4 * vu + 2 * (u & 1) + e) ^ (vrow & 7)) << 4);
+                    });
+              }
+              ready(v_ready + odd * 8);
               if (lane == 0) mbar_arrive(&T->codes_empty[1][v]);
             }
           }
