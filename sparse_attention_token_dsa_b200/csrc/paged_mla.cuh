@@ -814,25 +814,22 @@ __global__ void __cluster_dims__(2, 1, 1)
             wait(&T->k_empty[i], (uses & 1) ^ 1, 64);
           }
       } else {
-        // V: two warps take every second slice, two lanes a row
-        const int w = warp - 8 - kPmLoaders, odd = w >> 1;
-        const int vrow = (w & 1) * 16 + (lane >> 1), vu = lane & 1;
+        // V: two warps take every second slice, one its first group of 128 values and one its
+        // second, a lane a row (so that neither the loads nor the stores meet in a bank)
+        const int w = warp - 8 - kPmLoaders, odd = w >> 1, b = w & 1;
         const uint32_t v_ready = in_cta(&T->v_ready[0], 0);
         int page[2];
-        float next[2][2];                            // [slice odd, odd + 2][group]
+        float next[2];                               // of slices odd, odd + 2
         uint32_t live = 0;                           // bit: the row of `next` is one
         auto look = [&](int tile) {
 #pragma unroll
-          for (int j = 0; j < 2; ++j) page[j] = page_at(tile * kPmKeys + (odd + 2 * j) * 32 + vrow);
+          for (int j = 0; j < 2; ++j) page[j] = page_at(tile * kPmKeys + (odd + 2 * j) * 32 + lane);
         };
         auto load = [&](int tile) {
           live = 0;
 #pragma unroll
           for (int j = 0; j < 2; ++j) {
-            const float* sc =
-                scales(page[j], tile * kPmKeys + (odd + 2 * j) * 32 + vrow) + rank * 2;
-            next[j][0] = sc[0];
-            next[j][1] = sc[1];
+            next[j] = scales(page[j], tile * kPmKeys + (odd + 2 * j) * 32 + lane)[rank * 2 + b];
             live |= (page[j] < a.c.n_pages ? 1u : 0u) << j;
           }
         };
@@ -843,37 +840,27 @@ __global__ void __cluster_dims__(2, 1, 1)
           if (s.n > 1) look(s.t0 + 1);
 #pragma unroll 1
           for (int i = 0; i < s.n && ok; ++i, ++n) {
-            float now[2][2];
+            const float now[2] = {live & 1 ? next[0] : 0.f, live & 2 ? next[1] : 0.f};
             const uint32_t on = live;
-#pragma unroll
-            for (int j = 0; j < 2; ++j) {
-              now[j][0] = on >> j & 1 ? next[j][0] : 0.f;
-              now[j][1] = on >> j & 1 ? next[j][1] : 0.f;
-            }
             if (i + 1 < s.n) load(s.t0 + i + 1);
             if (i + 2 < s.n) look(s.t0 + i + 2);
 #pragma unroll 1
             for (int j = 0; j < 2; ++j) {
               const int v = odd + 2 * j;
-              const float s0 = j ? now[1][0] : now[0][0], s1 = j ? now[1][1] : now[0][1];
-              const uint32_t f0 = code_factor(s0), f1 = code_factor(s1);
-              const bool exact = __all_sync(0xffffffffu, (f0 && f1) || !(on >> j & 1));
+              const float sc = j ? now[1] : now[0];
+              const uint32_t f = code_factor(sc);
+              const bool exact = __all_sync(0xffffffffu, f != 0 || !(on >> j & 1));
               // both uses of a slot in a tile are these two warps'
               ok = ok && wait(&T->codes_full[1][v], n & 1, 60) && wait(&T->v_empty[odd], j ^ 1, 63);
               ok = __all_sync(0xffffffffu, ok);
               if (!ok) break;
 #pragma unroll 1
-              for (int h = 0; h < 2; ++h) {          // group: units 4 (u / 2) + 2 vu + u % 2
-                const uint8_t* from = Vc + v * 8192 + h * 4096 + vrow * 128;
-                uint8_t* to = Vs + odd * kPmSlice + h * 8192 + vrow * 128;
+              for (int h = 0; h < 2; ++h) {          // block of 64 values
+                const uint8_t* from = Vc + v * 8192 + b * 4096 + lane * 128;
+                uint8_t* to = Vs + odd * kPmSlice + (2 * b + h) * 4096 + lane * 128;
                 four_units(
-                    exact, h ? f1 : f0, h ? s1 : s0,
-                    [&](int u) {
-                      return from + (((2 * vu + (u & 1) + 4 * (u >> 1)) ^ (vrow & 7)) << 4);
-                    },
-                    [&](int u, int e) {
-                      return to + (u >> 1) * 4096 + (((4 * vu + 2 * (u & 1) + e) ^ (vrow & 7)) << 4);
-                    });
+                    exact, f, sc, [&](int u) { return from + (((4 * h + u) ^ (lane & 7)) << 4); },
+                    [&](int u, int e) { return to + (((2 * u + e) ^ (lane & 7)) << 4); });
               }
               ready(v_ready + odd * 8);
               if (lane == 0) mbar_arrive(&T->codes_empty[1][v]);
