@@ -375,8 +375,10 @@ __global__ void __cluster_dims__(2, 1, 1)
   if (warp == 4) pair_tmem_alloc(&T->tmem_base, 512);
   if (warp == 5) {
     // this cluster's share of the line of tiles
-    int total = 0;
-    for (int p0 = 0; p0 < a.pairs; p0 += 32) {
+    const bool few = a.pairs <= 32;                  // a lane each: looked at once
+    const int mine = lane < a.pairs ? pm_pair(a, lane).tiles : 0;
+    int total = few ? __reduce_add_sync(0xffffffffu, mine) : 0;
+    for (int p0 = 0; p0 < a.pairs && !few; p0 += 32) {
       const int p = p0 + lane;
       total += __reduce_add_sync(0xffffffffu, p < a.pairs ? pm_pair(a, p).tiles : 0);
     }
@@ -385,7 +387,7 @@ __global__ void __cluster_dims__(2, 1, 1)
     int before = 0, found = -1, off = 0;
     for (int p0 = 0; p0 < a.pairs && found < 0 && begin < total; p0 += 32) {
       const int p = p0 + lane;
-      const int n = p < a.pairs ? pm_pair(a, p).tiles : 0;
+      const int n = few ? mine : (p < a.pairs ? pm_pair(a, p).tiles : 0);
       int upto = n;
 #pragma unroll
       for (int d = 1; d < 32; d <<= 1) {
@@ -560,8 +562,10 @@ __global__ void __cluster_dims__(2, 1, 1)
           table = a.table + (int64_t)s.pair.b * a.max_pages;
 #pragma unroll 1
           for (int i = s.t0; i < s.t0 + s.n && ok; ++i, ++n) {
+            // pages of the tile, looked up before its slots are free
             const int key = i * kPmKeys + 64 * rank;
-            const int page = page_at(key);
+            const int z0 = page_at(key), z1 = rows < 64 ? page_at(key + rows) : 0;
+            const int z2 = rows < 32 ? page_at(key + 32) : 0, z3 = rows < 32 ? page_at(key + 48) : 0;
 #pragma unroll 1
             for (int k = 0; k < Ring::kKSlots; ++k) {
               ok = wait(&T->k_empty[k], (n & 1) ^ 1, 62);
@@ -569,15 +573,17 @@ __global__ void __cluster_dims__(2, 1, 1)
               mbar_arrive_expect_tx(&T->k_full[k], Ring::kKBytes);
               uint8_t* dst = Ks + k * Ring::kKBytes;
               if (rows == 64) {
-                tma_load_4d(dst, &kmap, &T->k_full[k], 0, key & mask, 3 * k, page);
+                tma_load_4d(dst, &kmap, &T->k_full[k], 0, key & mask, 3 * k, z0);
               } else {                               // chunk by chunk, pages below one another
 #pragma unroll 1
-                for (int j = 0; j < 64; j += rows) {
-                  const int z = page_at(key + j);
-#pragma unroll 1
-                  for (int c = 0; c < 3; ++c)
-                    tma_load_4d(dst + c * kPmChunk + j * 128, &kmap, &T->k_full[k], 0, 0,
-                                3 * k + c, z);
+                for (int c = 0; c < 3; ++c) {
+                  uint8_t* to = dst + c * kPmChunk;
+                  tma_load_4d(to, &kmap, &T->k_full[k], 0, 0, 3 * k + c, z0);
+                  tma_load_4d(to + rows * 128, &kmap, &T->k_full[k], 0, 0, 3 * k + c, z1);
+                  if (rows < 32) {
+                    tma_load_4d(to + 32 * 128, &kmap, &T->k_full[k], 0, 0, 3 * k + c, z2);
+                    tma_load_4d(to + 48 * 128, &kmap, &T->k_full[k], 0, 0, 3 * k + c, z3);
+                  }
                 }
               }
             }
