@@ -435,9 +435,9 @@ int dsa_paged_mla(const dsa_paged_mla_problem* p, const dsa_cache* c, const void
         !map_rows(&rm, c, false, page < 32 ? page : 32))
       return DSA_ERR_CUDA;
   } else {
-    // one copy a slot where a page holds its rows, else one a page and chunk
+    // K: one copy a slot where a page holds its rows, else one a page and chunk; V: one a page
     if (!map_pages(&km, c, page < 64 ? page : 64, page < 64 ? 1 : 3) ||
-        !map_pages(&vm, c, page < 32 ? page : 32, page < 32 ? 1 : 4))
+        !map_pages(&vm, c, page < 32 ? page : 32, 4))
       return DSA_ERR_CUDA;
   }
   PagedMlaArgs a{};

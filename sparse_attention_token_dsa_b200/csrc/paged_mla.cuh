@@ -308,6 +308,15 @@ __device__ __forceinline__ void tma_load_4d(void* dst, const CUtensorMap* map, u
       : "memory");
 }
 
+// A slice of V: 4 blocks of 64 values of 32 positions, or, where a page has 16, twice 4
+// blocks of 16 (so that a page is still one copy).
+struct VLayout {
+  uint32_t block, half;    // bytes from block to block, from 16 positions to the next 16
+  __device__ __forceinline__ explicit VLayout(bool halves)
+      : block(halves ? 2048 : 4096), half(halves ? 8192 : 2048) {}
+  __device__ __forceinline__ uint32_t row(int r) const { return (r >> 4) * half + (r & 15) * 128; }
+};
+
 // Abort path: let a slot's last copies land.  `n` tiles were begun; the slot's last fill
 // belongs to the n-th or, where the loader gave up before it, to the one before, which
 // the wait's limit then covers.
@@ -497,7 +506,9 @@ __global__ void __cluster_dims__(2, 1, 1)
     // ---------------------------------------------------------------- O += P V --
     if (rank == 0 && elect_one()) {
       const uint32_t idesc = make_idesc<MmaKind::BF16>(256) | (1u << 16);   // B MN-major
-      const uint64_t p_desc = make_sdesc(smem_u32(Ps)), v_desc = make_sdesc_mn(smem_u32(Vs), 4096);
+      const VLayout at(!CODES && a.c.page_shift == 4);
+      const uint64_t p_desc = make_sdesc(smem_u32(Ps));
+      const uint64_t v_desc = make_sdesc_mn(smem_u32(Vs), at.block);
       uint32_t pc = 0, qc = 0;
       int slot = 0, parity = 0;                      // of the next V slot
       bool ok = true;
@@ -525,7 +536,7 @@ __global__ void __cluster_dims__(2, 1, 1)
 #pragma unroll
               for (int h = 0; h < 2; ++h)            // 128 values of each CTA
                 pair_mma_bf16(tmem + h * 128, ad,
-                              v_desc + ((cur * kPmSlice + h * 8192 + kk * 2048) >> 4), idesc,
+                              v_desc + ((cur * kPmSlice + h * 2 * at.block + kk * at.half) >> 4), idesc,
                               (i | k16) != 0);
             }
             pair_commit(&T->v_empty[cur]);
@@ -608,18 +619,9 @@ __global__ void __cluster_dims__(2, 1, 1)
               if (!ok) break;
               mbar_arrive_expect_tx(&T->v_full[v], kPmSlice);
               uint8_t* dst = Vs + v * kPmSlice;
-              if (rows == 32) {
-                tma_load_4d(dst, &vmap, &T->v_full[v], 0, key & mask, rank * 4, page);
-              } else {
-#pragma unroll 1
-                for (int j = 0; j < 32; j += rows) {
-                  const int z = page_at(key + j);
-#pragma unroll 1
-                  for (int c = 0; c < 4; ++c)
-                    tma_load_4d(dst + c * 4096 + j * 128, &vmap, &T->v_full[v], 0, 0, rank * 4 + c,
-                                z);
-                }
-              }
+              tma_load_4d(dst, &vmap, &T->v_full[v], 0, key & mask, rank * 4, page);
+              if (rows == 16)
+                tma_load_4d(dst + 8192, &vmap, &T->v_full[v], 0, 0, rank * 4, page_at(key + 16));
             }
           }
         }
@@ -639,6 +641,7 @@ __global__ void __cluster_dims__(2, 1, 1)
       } else if (warp == 9) {
         // V slots to the matrix warp, after zeroing the rows behind k_len
         const uint32_t v_ready = in_cta(&T->v_ready[0], 0);
+        const VLayout at(shift == 4);
         while (ok && pm_next(a, walk, s)) {
           for (int i = s.t0; i < s.t0 + s.n && ok; ++i, ++n) {
             for (int v = 0; v < Ring::kVSlots; ++v) {
@@ -650,7 +653,7 @@ __global__ void __cluster_dims__(2, 1, 1)
                 const int from = max(live, 0);
                 for (int u = lane; u < (32 - from) * 32; u += 32) {
                   const int r = from + (u >> 5), blk = (u >> 3) & 3, k = u & 7;
-                  *reinterpret_cast<uint4*>(Vs + v * kPmSlice + blk * 4096 + r * 128 + k * 16) =
+                  *reinterpret_cast<uint4*>(Vs + v * kPmSlice + blk * at.block + at.row(r) + k * 16) =
                       make_uint4(0, 0, 0, 0);
                 }
                 fence_proxy_async_smem();
