@@ -87,7 +87,7 @@ struct RopeArgs {
   int32_t heads, offset, rot;
   int32_t pairs;           // pair units of a head (see below)
   int32_t units;           // pair and copy units of a head
-  uint32_t per_unit;       // 2^32 / units, rounded up (0: one unit)
+  uint32_t per_unit;       // 2^32 / units, rounded up; 0 where that is not exact
   int32_t tpb;             // tokens of a block
   int32_t span;            // units that one block of a token takes (blockIdx.y of them)
   float mscale;
@@ -132,7 +132,7 @@ __global__ void __launch_bounds__(kRopeThreads, 4) rope_kernel(const RopeArgs a)
       if (i >= last) continue;
       const uint32_t tl = a.tpb > 1 ? i / per_token : 0;
       const uint32_t r = i - tl * per_token;
-      const uint32_t h = a.per_unit ? __umulhi(r, a.per_unit) : r;
+      const uint32_t h = a.per_unit ? __umulhi(r, a.per_unit) : r / (uint32_t)a.units;
       const int u = (int)(r - h * a.units);
       int d;
       if (u < a.pairs) {

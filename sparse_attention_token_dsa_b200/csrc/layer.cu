@@ -38,8 +38,11 @@ int launch_rope(RopeArgs& a, int dim, bool vec, bool inter, bool in_place, cudaS
   const int n = vec ? RowType<T>::kVec : 1;
   a.pairs = vec && inter ? a.rot / n : a.rot / 2 / n;
   a.units = a.pairs + (in_place ? 0 : (dim - a.rot) / n);
-  // exact for the numbers below 2^17 that a block divides (see launch_rope's limits)
-  a.per_unit = a.units > 1 ? (uint32_t)((0x100000000ull + a.units - 1) / a.units) : 0;
+  // r / units as the upper word of r ceil(2^32 / units): exact while r units < 2^32
+  if ((uint64_t)a.heads * a.units >= 1ull << 31) return DSA_ERR_UNSUPPORTED;
+  a.per_unit = a.units > 1 && (uint64_t)a.heads * a.units * a.units < 1ull << 32
+                   ? (uint32_t)(((1ull << 32) + a.units - 1) / a.units)
+                   : 0;
   // a block takes about 1024 units (four a thread): several tokens of few heads, or a
   // part of one token's heads
   const int64_t per_token = (int64_t)a.heads * a.units;
@@ -470,7 +473,9 @@ int dsa_paged_mla(const dsa_paged_mla_problem* p, const dsa_cache* c, const void
   const int64_t rows = (int64_t)p->n_q * p->heads;
   // the join is launched while the attention kernel drains, and waits for its end itself
   cudaLaunchConfig_t join{};
-  join.gridDim = dim3((unsigned)pl.pairs, (unsigned)(rows < kPmRows ? rows : kPmRows));
+  a.join_rows = pl.pairs >= 256 ? 32 : (pl.pairs >= 64 ? 8 : 1);
+  const int64_t most = rows < kPmRows ? rows : kPmRows;
+  join.gridDim = dim3((unsigned)pl.pairs, (unsigned)((most + a.join_rows - 1) / a.join_rows));
   join.blockDim = dim3(kPmJoinThreads);
   join.stream = st;
   cudaLaunchAttribute early{};

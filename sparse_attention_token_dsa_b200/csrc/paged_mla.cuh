@@ -73,6 +73,7 @@ struct PagedMlaArgs {
   int32_t row_tiles;       // row tiles of a sequence of n_q tokens
   int32_t pairs;           // batch * row_tiles
   int32_t clusters;
+  int32_t join_rows;       // rows that a block of the join takes
   float scale_log2;        // softmax scale * log2(e)
   uint16_t* out;           // [batch][n_q][heads][512] bf16
   float* lse;              // [batch][n_q][heads] or null
@@ -146,7 +147,8 @@ __device__ __noinline__ bool pm_next_far(const PagedMlaArgs& a, PmWalk* walk, Pm
   while (w.p < a.pairs) {
     s.pair = pm_pair(a, w.p);
     if (s.pair.tiles > 0) break;
-    ++w.p;
+    // behind a sequence's last token there are only empty row tiles
+    w.p = s.pair.rows > 0 ? w.p + 1 : (s.pair.b + 1) * a.row_tiles;
   }
   if (w.p >= a.pairs) return false;
   s.p = w.p;
@@ -1052,14 +1054,16 @@ __global__ void __cluster_dims__(2, 1, 1)
 }
 
 // Rows whose positions more than one cluster read: o = sum_i w_i O_i / sum_i w_i l_i with
-// w_i = 2^(m_i - max m); rows that see nothing: o = 0, lse = -inf.  One block a row.
+// w_i = 2^(m_i - max m); rows that see nothing: o = 0, lse = -inf.  A block takes a few
+// rows of a pair, one where there are few pairs (most pairs of a large call were read by
+// one cluster, and their blocks only find that out).
 __global__ void __launch_bounds__(kPmJoinThreads) paged_mla_join_kernel(const PagedMlaArgs a) {
   __shared__ float w[2 * kPmClusters];
   __shared__ float red[2][kPmJoinThreads / 32];
-  const int p = blockIdx.x, row = blockIdx.y, t = threadIdx.x;
+  const int p = blockIdx.x, t = threadIdx.x;
   const PmPair pr = pm_pair(a, p);
   asm volatile("griddepcontrol.wait;" ::: "memory");   // all of the attention kernel is done
-  if (p == 0 && row == 0 && t < 32) {                // status of the call: the first cluster's
+  if (p == 0 && blockIdx.y == 0 && t < 32) {         // status of the call: the first cluster's
     int code = DSA_OK, where = 0;
     for (int c = t; c < a.clusters && code == DSA_OK; c += 32) {
       code = a.states[2 * c];
@@ -1071,56 +1075,57 @@ __global__ void __launch_bounds__(kPmJoinThreads) paged_mla_join_kernel(const Pa
       a.status[1] = where;
     }
   }
-  if (row >= pr.rows) return;
-  const int64_t grow = (int64_t)pr.b * a.n_q * a.heads + pr.row0 + row;
-  uint2* out = reinterpret_cast<uint2*>(a.out + grow * kPmDv) + t;
+  const int first_row = blockIdx.y * a.join_rows;
+  const int rows = min(pr.rows - first_row, a.join_rows);
+  if (rows <= 0) return;
   const float inf = __int_as_float(0x7f800000);
-  if (pr.tiles == 0) {
-    *out = make_uint2(0, 0);
-    if (t == 0 && a.lse) a.lse[grow] = -inf;
-    return;
-  }
-  const int share = a.plan[0], first = a.plan[1 + p];
+  const int share = pr.tiles ? a.plan[0] : 1, first = pr.tiles ? a.plan[1 + p] : 0;
   const int c0 = first / share, c1 = (first + pr.tiles - 1) / share;
-  if (c0 == c1) return;                              // written whole
+  if (pr.tiles && c0 == c1) return;                  // written whole
   const int n = c1 - c0 + 1;
   // the pair's run in cluster c is that cluster's first unless it starts inside its share
   const int head = first > c0 * share ? 1 : 0;
-  float m = -inf;
-  float2 ml = make_float2(-inf, 0.f);
-  if (t < n) {
-    const int slot = 2 * (c0 + t) + (t == 0 ? head : 0);
-    ml = a.part_ml[(int64_t)slot * kPmRows + row];
-    m = ml.x;
-  }
+  for (int row = first_row; row < first_row + rows; ++row) {
+    const int64_t grow = (int64_t)pr.b * a.n_q * a.heads + pr.row0 + row;
+    uint2* out = reinterpret_cast<uint2*>(a.out + grow * kPmDv) + t;
+    if (pr.tiles == 0) {
+      *out = make_uint2(0, 0);
+      if (t == 0 && a.lse) a.lse[grow] = -inf;
+      continue;
+    }
+    float2 ml = make_float2(-inf, 0.f);
+    if (t < n) ml = a.part_ml[(int64_t)(2 * (c0 + t) + (t == 0 ? head : 0)) * kPmRows + row];
+    float m = ml.x;
 #pragma unroll
-  for (int d = 16; d > 0; d >>= 1) m = fmaxf(m, __shfl_xor_sync(0xffffffffu, m, d));
-  if ((t & 31) == 0) red[0][t >> 5] = m;
-  __syncthreads();
-  m = fmaxf(fmaxf(red[0][0], red[0][1]), fmaxf(red[0][2], red[0][3]));
-  const float wt = ml.x == -inf ? 0.f : ex2(ml.x - m);
-  float l = wt * ml.y;
-  if (t < n) w[t] = wt;
+    for (int d = 16; d > 0; d >>= 1) m = fmaxf(m, __shfl_xor_sync(0xffffffffu, m, d));
+    if ((t & 31) == 0) red[0][t >> 5] = m;
+    __syncthreads();
+    m = fmaxf(fmaxf(red[0][0], red[0][1]), fmaxf(red[0][2], red[0][3]));
+    const float wt = ml.x == -inf ? 0.f : ex2(ml.x - m);
+    float l = wt * ml.y;
+    if (t < n) w[t] = wt;
 #pragma unroll
-  for (int d = 16; d > 0; d >>= 1) l += __shfl_xor_sync(0xffffffffu, l, d);
-  if ((t & 31) == 0) red[1][t >> 5] = l;
-  __syncthreads();
-  l = (red[1][0] + red[1][1]) + (red[1][2] + red[1][3]);
-  float4 o = make_float4(0.f, 0.f, 0.f, 0.f);
+    for (int d = 16; d > 0; d >>= 1) l += __shfl_xor_sync(0xffffffffu, l, d);
+    if ((t & 31) == 0) red[1][t >> 5] = l;
+    __syncthreads();
+    l = (red[1][0] + red[1][1]) + (red[1][2] + red[1][3]);
+    float4 o = make_float4(0.f, 0.f, 0.f, 0.f);
 #pragma unroll 4
-  for (int i = 0; i < n; ++i) {
-    const int slot = 2 * (c0 + i) + (i == 0 ? head : 0);
-    const float4 v =
-        *(reinterpret_cast<const float4*>(a.part_o + ((int64_t)slot * kPmRows + row) * kPmDv) + t);
-    const float wi = w[i];
-    o.x = fmaf(wi, v.x, o.x);
-    o.y = fmaf(wi, v.y, o.y);
-    o.z = fmaf(wi, v.z, o.z);
-    o.w = fmaf(wi, v.w, o.w);
+    for (int i = 0; i < n; ++i) {
+      const int slot = 2 * (c0 + i) + (i == 0 ? head : 0);
+      const float4 v =
+          *(reinterpret_cast<const float4*>(a.part_o + ((int64_t)slot * kPmRows + row) * kPmDv) + t);
+      const float wi = w[i];
+      o.x = fmaf(wi, v.x, o.x);
+      o.y = fmaf(wi, v.y, o.y);
+      o.z = fmaf(wi, v.z, o.z);
+      o.w = fmaf(wi, v.w, o.w);
+    }
+    const float inv = l == 0.f ? 0.f : 1.f / l;
+    *out = make_uint2(bf16x2(o.x * inv, o.y * inv), bf16x2(o.z * inv, o.w * inv));
+    if (t == 0 && a.lse) a.lse[grow] = l == 0.f ? -inf : (m + log2f(l)) * 0.6931471805599453f;
+    __syncthreads();                                 // the next row writes the same places
   }
-  const float inv = l == 0.f ? 0.f : 1.f / l;
-  *out = make_uint2(bf16x2(o.x * inv, o.y * inv), bf16x2(o.z * inv, o.w * inv));
-  if (t == 0 && a.lse) a.lse[grow] = l == 0.f ? -inf : (m + log2f(l)) * 0.6931471805599453f;
 }
 
 }  // namespace dsa

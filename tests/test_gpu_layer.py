@@ -51,7 +51,8 @@ def near(got, want, scale, dtype):
 # and parts that are not aligned to 16 bytes
 SHAPES = [(1, 1, 128, 0, 64), (33, 64, 128, 0, 64), (5, 16, 576, 512, 64), (1000, 1, 128, 0, 128),
           (7, 3, 64, 0, 64), (3, 5, 50, 3, 20), (2, 2, 2, 0, 2), (9, 128, 192, 128, 64),
-          (65, 1, 33, 1, 32), (2, 1, 1024, 512, 512), (1, 700, 72, 8, 48)]
+          (65, 1, 33, 1, 32), (2, 1, 1024, 512, 512), (1, 700, 72, 8, 48), (2, 90, 65536, 64, 64),
+          (1, 65536, 64, 0, 64)]
 
 
 @pytest.mark.parametrize("shape", SHAPES)

@@ -163,6 +163,16 @@ def test_many_sequences_and_room_in_the_table(B, form):
 
 
 @pytest.mark.parametrize("form", ["bf16", "e4m3"])
+def test_padded_batch(B, form):
+    """A batch padded to a long prompt: most row tiles are empty, rows of padding tokens
+    stay as they were."""
+    q_lens = [1, 300, 0, 7, 2, 512, 1]
+    p = Problem(B, 18, [700, 300, 50, 3, 1500, 600, 1], q_lens, 512, 48, 32, form)
+    out, lse = p.run(B)
+    p.check(out, lse, tokens=[0, 1, 2, 6, 150, 299, 300, 511])
+
+
+@pytest.mark.parametrize("form", ["bf16", "e4m3"])
 def test_large_logits(B, form):
     """Logits of hundreds: the maximum is raised many times, weights vanish."""
     p = Problem(B, 7, [3000, 400], None, 2, 64, 64, form, spread=40.0)

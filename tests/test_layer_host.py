@@ -86,7 +86,10 @@ def rope(B, p, x=FAKE, pos=FAKE, freq=FAKE, out=2 * FAKE):
     # an output whose places coincide
     (dict(out_head_stride=0), -1), (dict(out_token_stride=0), -1), (dict(out_head_stride=127), -1),
     (dict(out_token_stride=1023), -1), (dict(out_token_stride=-1024), -1),
-    (dict(offset=2 ** 31 - 64), -1)])
+    (dict(offset=2 ** 31 - 64), -1),
+    # more units of a token than 32 bits count
+    (dict(heads=65536, dim=65536, out_head_stride=65536, out_token_stride=1 << 33,
+          x_head_stride=65535, x_token_stride=1 << 33), -2)])
 def test_rope_problem_refusals(B, kw, status):
     assert rope(B, rope_problem(B, **kw)) == status
 
