@@ -354,7 +354,7 @@ __device__ __forceinline__ float quantise(const float (&v)[2][8], float amax, bo
 }
 
 // 8 lanes take a row and hold four chunks of 128 values of it at once (rows of less than
-// four chunks: one chunk of each of four rows), two runs of 8 values a lane, 64 apart, so
+// four chunks: one chunk of each of two rows; of four took registers that cost more threads), two runs of 8 values a lane, 64 apart, so
 // each access of the 8 lanes is one contiguous run; a group's largest magnitude is a
 // three-step exchange between them and nothing is reread.  A scale that is a power of two
 // makes code * scale exact in bf16, so attention on the tensor cores reads the quantised
@@ -362,33 +362,35 @@ __device__ __forceinline__ float quantise(const float (&v)[2][8], float amax, bo
 // binade at the bottom of its range.
 template <typename T, bool VEC, bool TURN, int ROWS>
 __global__ void __launch_bounds__(kCacheThreads) cache_write_kernel(const CacheWriteArgs a) {
-  constexpr int CHUNKS = kCacheBatch / ROWS;
+  constexpr int BATCH = ROWS > 1 ? ROWS : kCacheBatch, CHUNKS = BATCH / ROWS;
   const int l = threadIdx.x & 7, q_chunks = a.c.dim_q >> 7, width = a.c.dim_q + a.c.dim_raw;
   const uint32_t mates = 0xffu << (threadIdx.x & 24);
-  const T* x[ROWS];
-  int64_t token[ROWS], page[ROWS];
-  int row[ROWS];
+  // (tokens and pages fit 32 bits; their places do not)
+  const uint32_t token0 = blockIdx.x * (uint32_t)(ROWS * kCacheUnits) + (threadIdx.x >> 3);
+  int page[ROWS], row[ROWS];
 #pragma unroll
   for (int r = 0; r < ROWS; ++r) {
-    token[r] = ((int64_t)blockIdx.x * ROWS + r) * kCacheUnits + (threadIdx.x >> 3);
-    const int64_t slot = token[r] < a.n_tokens ? a.slots[token[r]] : -1;
-    page[r] = slot >> a.c.page_shift;                // -1 for a negative slot
+    const uint32_t token = token0 + r * kCacheUnits;
+    const int64_t slot = token < a.n_tokens ? a.slots[token] : -1;
+    const bool in = slot >= 0 && (slot >> a.c.page_shift) < a.c.n_pages;
+    page[r] = in ? (int)(slot >> a.c.page_shift) : -1;
     row[r] = (int)slot & ((1 << a.c.page_shift) - 1);
-    if (slot < 0 || page[r] >= a.c.n_pages) page[r] = -1;
-    x[r] = reinterpret_cast<const T*>(a.x) + token[r] * a.x_ts;
   }
+  auto x_at = [&](int r) {
+    return reinterpret_cast<const T*>(a.x) + (int64_t)(token0 + r * kCacheUnits) * a.x_ts;
+  };
 #pragma unroll 1
   for (int c0 = 0; c0 < a.items; c0 += CHUNKS) {
-    Run8<T, VEC> held[kCacheBatch][2];
+    Run8<T, VEC> held[BATCH][2];
 #pragma unroll
-    for (int k = 0; k < kCacheBatch; ++k)
+    for (int k = 0; k < BATCH; ++k)
 #pragma unroll
       for (int h = 0; h < 2; ++h) {
         const int d = (c0 + k % CHUNKS) * 128 + h * 64 + l * 8;
-        if (page[k / CHUNKS] >= 0 && d < width) held[k][h].load(x[k / CHUNKS] + d);
+        if (page[k / CHUNKS] >= 0 && d < width) held[k][h].load(x_at(k / CHUNKS) + d);
       }
 #pragma unroll
-    for (int k = 0; k < kCacheBatch; ++k) {
+    for (int k = 0; k < BATCH; ++k) {
       const int r = k / CHUNKS, c = c0 + k % CHUNKS;
       if (page[r] < 0 || c >= a.items) continue;     // the same for the 8 lanes
       float v[2][8];
@@ -397,7 +399,7 @@ __global__ void __launch_bounds__(kCacheThreads) cache_write_kernel(const CacheW
         held[k][h].get(v[h]);
         if constexpr (TURN) {
           const int d = c * 128 + h * 64 + l * 8;
-          if (d < width) turn8<T, VEC>(a, x[r], token[r], d, v[h]);
+          if (d < width) turn8<T, VEC>(a, x_at(r), token0 + r * kCacheUnits, d, v[h]);
         }
       }
       if (c < q_chunks) {
@@ -486,7 +488,8 @@ __device__ __forceinline__ void rows_to_read(const CacheReadArgs& a, int (&s)[RO
 }
 
 // Values of a sequence's first n_k rows.  8 lanes take a row and hold four chunks of 128
-// values of it at once (or one chunk of each of four rows), 16 contiguous codes a lane.
+// values of it at once (or one chunk of each of four rows), two runs of 8 values a lane, 64
+// apart, so that each store of the 8 lanes is one contiguous run.
 template <typename T, int ROWS>
 __global__ void __launch_bounds__(kCacheThreads) cache_read_kernel(const CacheReadArgs a) {
   constexpr int CHUNKS = kCacheBatch / ROWS;
@@ -501,23 +504,23 @@ __global__ void __launch_bounds__(kCacheThreads) cache_read_kernel(const CacheRe
   for (int r = 0; r < ROWS; ++r) {
     const int64_t p = max(page[r], 0);
     const int at = s[r] & ((1 << a.c.page_shift) - 1);
-    codes[r] = a.c.codes + p * a.c.codes_ps + (int64_t)at * a.c.dim_q + l * 16;
+    codes[r] = a.c.codes + p * a.c.codes_ps + (int64_t)at * a.c.dim_q + l * 8;
     scale[r] = a.c.scale + p * a.c.scale_ps + at * q_chunks;
     raw[r] = a.c.raw + p * a.c.raw_ps + (int64_t)at * a.c.dim_raw;
     out[r] = reinterpret_cast<T*>(a.out) + ((int64_t)blockIdx.y * a.n_k + s[r]) * width;
   }
-  const int q_last = q_chunks - q_chunks % CHUNKS;   // chunks that come in whole batches
 #pragma unroll 1
   for (int c0 = 0; c0 < q_chunks; c0 += CHUNKS) {
-    uint4 w[kCacheBatch];
+    uint2 w[kCacheBatch][2];
     float sc[kCacheBatch];
 #pragma unroll
     for (int k = 0; k < kCacheBatch; ++k) {
       const int r = k / CHUNKS, c = c0 + k % CHUNKS;
-      w[k] = make_uint4(0, 0, 0, 0);
+      w[k][0] = w[k][1] = make_uint2(0, 0);
       sc[k] = 1.f;
-      if (page[r] >= 0 && (c0 < q_last || c < q_chunks)) {
-        w[k] = *reinterpret_cast<const uint4*>(codes[r] + c * 128);
+      if (page[r] >= 0 && c < q_chunks) {
+        w[k][0] = *reinterpret_cast<const uint2*>(codes[r] + c * 128);
+        w[k][1] = *reinterpret_cast<const uint2*>(codes[r] + c * 128 + 64);
         sc[k] = scale[r][c];
       }
     }
@@ -525,13 +528,12 @@ __global__ void __launch_bounds__(kCacheThreads) cache_read_kernel(const CacheRe
     for (int k = 0; k < kCacheBatch; ++k) {
       const int r = k / CHUNKS, c = c0 + k % CHUNKS;
       if (page[r] == -1 || c >= q_chunks) continue;
-      const uint32_t u[4] = {w[k].x, w[k].y, w[k].z, w[k].w};
 #pragma unroll
       for (int h = 0; h < 2; ++h) {
         float v[8];
-        e4m3x4_values(u[2 * h], sc[k], v);
-        e4m3x4_values(u[2 * h + 1], sc[k], v + 4);
-        store8(out[r] + c * 128 + l * 16 + h * 8, v);
+        e4m3x4_values(w[k][h].x, sc[k], v);
+        e4m3x4_values(w[k][h].y, sc[k], v + 4);
+        store8(out[r] + c * 128 + h * 64 + l * 8, v);
       }
     }
   }

@@ -119,10 +119,10 @@ CachePlanes planes(const dsa_cache* c) {
 
 int chunks_of(const dsa_cache* c) { return c->dim_q / 128 + (c->dim_raw + 127) / 128; }
 
-// Rows that 8 lanes hold at once: four chunks are in flight either way.
+// Whether 8 lanes hold chunks of several rows at once and not several of one.
 bool few_chunks(int chunks) { return chunks < 4; }
-unsigned row_blocks(int64_t rows, bool few) {
-  const int span = kCacheUnits * (few ? 4 : 1);
+unsigned row_blocks(int64_t rows, int at_once) {
+  const int span = kCacheUnits * at_once;
   return (unsigned)((rows + span - 1) / span);
 }
 
@@ -130,8 +130,8 @@ typedef void (*WriteKernel)(const CacheWriteArgs);
 template <typename T>
 WriteKernel write_kernel(bool vec, bool turn, bool few) {
   if (few)
-    return vec ? (turn ? cache_write_kernel<T, true, true, 4> : cache_write_kernel<T, true, false, 4>)
-               : (turn ? cache_write_kernel<T, false, true, 4> : cache_write_kernel<T, false, false, 4>);
+    return vec ? (turn ? cache_write_kernel<T, true, true, 2> : cache_write_kernel<T, true, false, 2>)
+               : (turn ? cache_write_kernel<T, false, true, 2> : cache_write_kernel<T, false, false, 2>);
   return vec ? (turn ? cache_write_kernel<T, true, true, 1> : cache_write_kernel<T, true, false, 1>)
              : (turn ? cache_write_kernel<T, false, true, 1> : cache_write_kernel<T, false, false, 1>);
 }
@@ -146,7 +146,7 @@ int read_args(const dsa_cache* c, const int32_t* table, int32_t batch, int32_t m
   if (!aligned(table, 4) || !aligned(k_len, 4)) return DSA_ERR_INVALID;
   if ((int64_t)max_pages * c->page_size < n_k || !aligned16(out)) return DSA_ERR_INVALID;
   if (batch > 65535 || n_k > (1 << 30)) return DSA_ERR_UNSUPPORTED;
-  *grid = dim3(row_blocks(n_k, few), (unsigned)batch);
+  *grid = dim3(row_blocks(n_k, few ? 4 : 1), (unsigned)batch);
   a->c = planes(c);
   a->table = table;
   a->k_len = k_len;
@@ -358,7 +358,7 @@ int dsa_cache_write(const dsa_cache* c, const void* x, int32_t x_dtype, int64_t 
   cudaStream_t st = reinterpret_cast<cudaStream_t>(stream);
   auto kern = x_dtype == DSA_BF16 ? write_kernel<__nv_bfloat16>(vec, rope != nullptr, few)
                                   : write_kernel<float>(vec, rope != nullptr, few);
-  kern<<<row_blocks(n_tokens, few), kCacheThreads, 0, st>>>(a);
+  kern<<<row_blocks(n_tokens, few ? 2 : 1), kCacheThreads, 0, st>>>(a);
   return launch_status();
 }
 
