@@ -446,47 +446,50 @@ def dsa_quantize_e4m3(x: torch.Tensor, stream=None):
 
 
 # ------------------------------------------------------ a cached DSA layer --
-# Calls of a decode step are short, so their checks are written out: each tensor's
-# dtype, device and layout is looked at once, and the call runs on the tensors' device.
+# A call of a decode step takes a few microseconds on the GPU, so what is right is found
+# out in a few attribute reads (numbers rather than objects for devices and streams).
 
 _F64, _I64 = (torch.float64,), (torch.int64,)
 _ROWS = (torch.bfloat16, torch.float32)
 _CODES = (torch.uint8, torch.float8_e4m3fn)
+_BF16 = (torch.bfloat16,)
+_ROW_CODE = {torch.bfloat16: DSA_BF16, torch.float32: DSA_F32}
+_Tensor = torch.Tensor
 
 
 def _need(name, t, dtypes, device, strided=False):
-    """Checks of one tensor, in the order in which they are cheapest to pass."""
-    if not isinstance(t, torch.Tensor):
+    """Raise for the first thing that is wrong with a tensor; `device`: its index."""
+    if not isinstance(t, _Tensor):
         raise TypeError(f"{name}: expected a torch.Tensor, got {type(t).__name__}")
     if t.dtype not in dtypes:
         raise TypeError(f"{name}: dtype {t.dtype}, expected one of {dtypes}")
-    if t.device != device:
-        raise ValueError(f"{name}: must be on {device}, not {t.device}")
+    if t.get_device() != device:
+        raise ValueError(f"{name}: must be on cuda:{device}, not {t.device}")
     if not strided and not t.is_contiguous():
         raise ValueError(f"{name}: must be contiguous")
 
 
-def _cuda_device(name, t):
-    if not isinstance(t, torch.Tensor):
+def _cuda_index(name, t):
+    """Index of a tensor's CUDA device."""
+    if not isinstance(t, _Tensor):
         raise TypeError(f"{name}: expected a torch.Tensor, got {type(t).__name__}")
     if not t.is_cuda:
         raise ValueError(f"{name}: must be on a CUDA device, not {t.device}")
-    return t.device
+    return t.get_device()
 
 
-# The current stream as a number (torch.cuda.current_stream() makes an object of it, which
-# takes longer than the launch it is for).
-_current_stream = torch._C._cuda_getCurrentRawStream if hasattr(
-    torch._C, "_cuda_getCurrentRawStream") else (
-        lambda index: torch.cuda.current_stream(index).cuda_stream)
+# The current stream and device as numbers (torch.cuda.current_stream() makes an object,
+# which takes longer than the launch it is for).
+_current_stream = getattr(torch._C, "_cuda_getCurrentRawStream", None) or (
+    lambda index: torch.cuda.current_stream(index).cuda_stream)
+_current_device = getattr(torch._C, "_cuda_getDevice", None) or torch.cuda.current_device
 
 
-def _on(device, stream, what, call, *args):
-    """call(*args, stream) with `device` current, on `stream` (default: that device's
+def _on(index, stream, what, call, *args):
+    """call(*args, stream) with device `index` current, on `stream` (default: that device's
     current one); raises DsaError for a status other than DSA_OK."""
-    index = device.index
     raw = _current_stream(index) if stream is None else stream.cuda_stream
-    if index == torch.cuda.current_device():
+    if index == _current_device():
         rc = call(*args, raw)
     else:
         with torch.cuda.device(index):
@@ -518,26 +521,35 @@ def rope_frequencies(rot_dim, base=10000.0, scaling="plain", factor=1.0, origina
 
 
 def _rope(x, pos, freq, offset, interleaved, mscale, out, stream, flags, what):
-    dev = _cuda_device("x", x)
-    _need("x", x, _ROWS, dev, strided=True)
-    if x.dim() != 3 or (x.stride(2) != 1 and x.shape[2] > 1):
+    dev = _cuda_index("x", x)
+    code = _ROW_CODE.get(x.dtype)
+    if code is None:
+        _need("x", x, _ROWS, dev, strided=True)
+    shape = x.shape
+    if len(shape) != 3:
         raise ValueError("x: must be [tokens, heads, dim] with contiguous values")
-    n, heads, dim = x.shape
+    n, heads, dim = shape
+    xt, xh, xv = x.stride()
+    if xv != 1 and dim > 1:
+        raise ValueError("x: must be [tokens, heads, dim] with contiguous values")
     _need("pos", pos, _I32, dev)
     _need("freq", freq, _F64, dev)
     if pos.numel() != n:
         raise ValueError(f"pos: {pos.numel()} positions for {n} tokens")
     if out is None:
-        out = _new(stream, lambda: torch.empty((n, heads, dim), dtype=x.dtype, device=dev))
+        out = _new(stream, lambda: torch.empty((n, heads, dim), dtype=x.dtype, device=x.device))
+        ot, oh = heads * dim, dim
     else:
         _need("out", out, (x.dtype,), dev, strided=True)
-        if out.shape != x.shape or (out.stride(2) != 1 and dim > 1):
+        if out.shape != shape:
+            raise ValueError("out: must have x's shape and contiguous values")
+        ot, oh, ov = out.stride()
+        if ov != 1 and dim > 1:
             raise ValueError("out: must have x's shape and contiguous values")
     if n == 0 or heads == 0:
         return out
-    xs, os_ = x.stride(), out.stride()
-    p = DsaRopeProblem(n, heads, dim, offset, 2 * freq.numel(), _dtype_code(x), mscale, xs[0],
-                       xs[1], os_[0], os_[1], flags | (DSA_FLAG_INTERLEAVED if interleaved else 0))
+    p = DsaRopeProblem(n, heads, dim, offset, 2 * freq.numel(), code, mscale, xt, xh, ot, oh,
+                       flags | DSA_FLAG_INTERLEAVED if interleaved else flags)
     _on(dev, stream, what, lib.dsa_rope, C.byref(p), x.data_ptr(), pos.data_ptr(),
         freq.data_ptr(), out.data_ptr())
     return out
@@ -556,13 +568,24 @@ def rope_backward(grad, pos, freq, offset=0, interleaved=False, mscale=1.0, out=
                  "rope_backward")
 
 
+def _page_stride(name, t, dtypes, dev, pages, page, width):
+    """Page stride of a plane of rows of `width`."""
+    _need(name, t, dtypes, dev, strided=True)
+    if t.shape != (pages, page, width):
+        raise ValueError(f"{name}: shape {tuple(t.shape)}, expected {(pages, page, width)}")
+    ps, rs, vs = t.stride()
+    if (vs != 1 and width > 1) or (rs != width and page > 1):
+        raise ValueError(f"{name}: the rows of a page must be contiguous")
+    return page * width if pages == 1 else ps
+
+
 class PagedCache:
     """The planes of a paged cache (dsa_cache of include/dsaidx.h): codes [pages, page,
     dim_q] e4m3 (or uint8), scale [pages, page, dim_q / 128] fp32, raw [pages, page,
     dim_raw] bf16; codes and scale, or raw, may be None.  The pages of a plane may be
     strided (a layer of a larger block); the rest of it is contiguous."""
 
-    __slots__ = ("codes", "scale", "raw", "c", "device")
+    __slots__ = ("codes", "scale", "raw", "c", "index")
 
     def __init__(self, codes=None, scale=None, raw=None):
         if codes is None and raw is None:
@@ -570,35 +593,26 @@ class PagedCache:
         if (codes is None) != (scale is None):
             raise ValueError("codes and scale come together")
         first = raw if codes is None else codes
-        self.device = _cuda_device("raw" if codes is None else "codes", first)
+        dev = self.index = _cuda_index("raw" if codes is None else "codes", first)
         self.codes, self.scale, self.raw = codes, scale, raw
         if first.dim() != 3:
             raise ValueError("planes: must be [pages, page, width]")
         pages, page, dim_q = first.shape
-        dim_raw, codes_ps, scale_ps, raw_ps = 0, 0, 0, 0
+        dim_raw = codes_ps = scale_ps = raw_ps = 0
         codes_p = scale_p = raw_p = None
         if codes is None:
             dim_q = 0
         else:
-            codes_ps = self._plane("codes", codes, _CODES, pages, page, dim_q)
-            scale_ps = self._plane("scale", scale, _F32, pages, page, dim_q // 128)
+            codes_ps = _page_stride("codes", codes, _CODES, dev, pages, page, dim_q)
+            scale_ps = _page_stride("scale", scale, _F32, dev, pages, page, dim_q // 128)
             codes_p, scale_p = codes.data_ptr(), scale.data_ptr()
         if raw is not None:
-            dim_raw = raw.shape[-1]
-            raw_ps = self._plane("raw", raw, (torch.bfloat16,), pages, page, dim_raw)
+            _need("raw", raw, _BF16, dev, strided=True)
+            dim_raw = raw.shape[-1] if raw.dim() else 0
+            raw_ps = _page_stride("raw", raw, _BF16, dev, pages, page, dim_raw)
             raw_p = raw.data_ptr()
         self.c = DsaCache(pages, page, dim_q, dim_raw, codes_p, scale_p, raw_p, codes_ps, scale_ps,
                           raw_ps)
-
-    def _plane(self, name, t, dtypes, pages, page, width):
-        """Page stride of a plane of rows of `width`."""
-        _need(name, t, dtypes, self.device, strided=True)
-        if t.shape != (pages, page, width):
-            raise ValueError(f"{name}: shape {tuple(t.shape)}, expected {(pages, page, width)}")
-        ps, rs, vs = t.stride()
-        if (vs != 1 and width > 1) or (rs != width and page > 1):
-            raise ValueError(f"{name}: the rows of a page must be contiguous")
-        return page * width if pages == 1 else ps
 
     @staticmethod
     def empty(n_pages, page_size, dim_q, dim_raw, device="cuda"):
@@ -618,55 +632,61 @@ def cache_write(cache, x, slots, pow2=False, freq=None, pos=None, offset=0, inte
     """Write rows x [tokens, dim_q + dim_raw] (bf16 or fp32, rows may be strided) at slots
     [tokens] int64 (page * page_size + row; -1 skips).  With freq and pos the values at
     `offset` are rotated first.  pow2: scales that are powers of two (for paged_mla)."""
-    dev, c = cache.device, cache.c
+    dev, c = cache.index, cache.c
     _need("x", x, _ROWS, dev, strided=True)
     _need("slots", slots, _I64, dev)
-    n = x.shape[0]
-    if x.dim() != 2 or x.shape[1] != c.dim_q + c.dim_raw or (x.stride(1) != 1 and x.shape[1] > 1):
-        raise ValueError(f"x: must be [tokens, {c.dim_q + c.dim_raw}] with contiguous rows")
+    width = c.dim_q + c.dim_raw
+    if x.dim() != 2 or x.shape[1] != width:
+        raise ValueError(f"x: must be [tokens, {width}] with contiguous rows")
+    n, (xt, xv) = x.shape[0], x.stride()
+    if xv != 1 and width > 1:
+        raise ValueError(f"x: must be [tokens, {width}] with contiguous rows")
     if slots.numel() != n:
         raise ValueError(f"slots: {slots.numel()} slots for {n} tokens")
     turn = pos_p = freq_p = None
-    if (freq is None) != (pos is None):
-        raise ValueError("freq and pos come together")
-    if freq is not None:
+    if freq is not None and pos is not None:
         _need("freq", freq, _F64, dev)
         _need("pos", pos, _I32, dev)
         if pos.numel() != n:
             raise ValueError(f"pos: {pos.numel()} positions for {n} tokens")
-        turn = C.byref(DsaRopeProblem(offset=offset, rot_dim=2 * freq.numel(), mscale=mscale,
-                                      flags=DSA_FLAG_INTERLEAVED if interleaved else 0))
+        turn = C.byref(DsaRopeProblem(n, 1, width, offset, 2 * freq.numel(), 0, mscale, 0, 0, 0, 0,
+                                      DSA_FLAG_INTERLEAVED if interleaved else 0))
         pos_p, freq_p = pos.data_ptr(), freq.data_ptr()
-    flags = DSA_FLAG_POW2_SCALE if pow2 else 0
+    elif freq is not None or pos is not None:
+        raise ValueError("freq and pos come together")
     _on(dev, stream, "dsa_cache_write", lib.dsa_cache_write, C.byref(c), x.data_ptr(),
-        _dtype_code(x), x.stride(0), n, slots.data_ptr(), turn, pos_p, freq_p, flags)
+        _ROW_CODE[x.dtype], xt, n, slots.data_ptr(), turn, pos_p, freq_p,
+        DSA_FLAG_POW2_SCALE if pow2 else 0)
 
 
-def _table(cache, block_table, n_k, k_len):
-    _need("block_table", block_table, _I32, cache.device)
+def _table(cache, block_table, k_len):
+    """Sequences and pages of a block table; pointer of the lengths."""
+    _need("block_table", block_table, _I32, cache.index)
     if block_table.dim() != 2:
         raise ValueError("block_table: must be [batch, max_pages]")
-    if k_len is not None:
-        _need("k_len", k_len, _I32, cache.device)
-        if k_len.numel() != block_table.shape[0]:
-            raise ValueError(f"k_len: {k_len.numel()} lengths for {block_table.shape[0]} sequences")
+    batch, pages = block_table.shape
+    if k_len is None:
+        return batch, pages, None
+    _need("k_len", k_len, _I32, cache.index)
+    if k_len.numel() != batch:
+        raise ValueError(f"k_len: {k_len.numel()} lengths for {batch} sequences")
+    return batch, pages, k_len.data_ptr()
 
 
 def cache_read(cache, block_table, n_k, k_len=None, dtype=torch.bfloat16, out=None, stream=None):
     """Positions [0, n_k) of each sequence as rows [batch, n_k, dim_q + dim_raw] of bf16
     (the kv of sparse_mla) or fp32.  Rows at or behind k_len[b] are left as they were
     (zeros in a new tensor)."""
-    dev, c = cache.device, cache.c
-    _table(cache, block_table, n_k, k_len)
-    shape = (block_table.shape[0], n_k, c.dim_q + c.dim_raw)
+    dev, c = cache.index, cache.c
+    batch, pages, lens = _table(cache, block_table, k_len)
+    shape = (batch, n_k, c.dim_q + c.dim_raw)
     if out is None:
-        out = _new(stream, lambda: torch.zeros(shape, dtype=dtype, device=dev))
+        out = _new(stream, lambda: torch.zeros(shape, dtype=dtype, device=block_table.device))
     _need("out", out, _ROWS, dev)
-    if tuple(out.shape) != shape:
+    if out.shape != shape:
         raise ValueError(f"out: shape {tuple(out.shape)}, expected {shape}")
     _on(dev, stream, "dsa_cache_read", lib.dsa_cache_read, C.byref(c), block_table.data_ptr(),
-        shape[0], block_table.shape[1], n_k, None if k_len is None else k_len.data_ptr(),
-        out.data_ptr(), _dtype_code(out))
+        batch, pages, n_k, lens, out.data_ptr(), _ROW_CODE[out.dtype])
     return out
 
 
@@ -675,22 +695,22 @@ def cache_read_codes(cache, block_table, n_k, k_len=None, out=None, stream=None)
     scale [batch, n_k] or [batch, n_k, dim_q / 128]), with dim_q = 128 the k and k_scale of
     dsa_index.  Rows at or behind k_len[b] are left as they were (codes 0, scale 1 in new
     tensors)."""
-    dev, c = cache.device, cache.c
-    _table(cache, block_table, n_k, k_len)
-    batch, groups = block_table.shape[0], c.dim_q // 128
+    dev, c = cache.index, cache.c
+    batch, pages, lens = _table(cache, block_table, k_len)
+    dim_q = c.dim_q
+    groups = dim_q // 128
     if out is None:
         per_row = (batch, n_k) if groups == 1 else (batch, n_k, groups)
         out = _new(stream, lambda: (
-            torch.zeros((batch, n_k, c.dim_q), dtype=torch.uint8, device=dev)
-            .view(torch.float8_e4m3fn), torch.ones(per_row, device=dev)))
+            torch.zeros((batch, n_k, dim_q), dtype=torch.uint8, device=block_table.device)
+            .view(torch.float8_e4m3fn), torch.ones(per_row, device=block_table.device)))
     codes, scale = out
     _need("codes", codes, _CODES, dev)
     _need("scale", scale, _F32, dev)
-    if tuple(codes.shape) != (batch, n_k, c.dim_q) or scale.numel() != batch * n_k * groups:
+    if codes.shape != (batch, n_k, dim_q) or scale.numel() != batch * n_k * groups:
         raise ValueError(f"out: shapes {tuple(codes.shape)}, {tuple(scale.shape)}")
     _on(dev, stream, "dsa_cache_read_codes", lib.dsa_cache_read_codes, C.byref(c),
-        block_table.data_ptr(), batch, block_table.shape[1], n_k,
-        None if k_len is None else k_len.data_ptr(), codes.data_ptr(), scale.data_ptr())
+        block_table.data_ptr(), batch, pages, n_k, lens, codes.data_ptr(), scale.data_ptr())
     return codes, scale
 
 
@@ -709,42 +729,44 @@ def paged_mla(q, cache, block_table, k_len, scale, q_len=None, flags=0, out=None
     k_len [batch] cached positions (the queries' own included), q_len [batch] query tokens
     (default n_q).  Returns (out [batch, n_q, heads, 512] bf16, lse [batch, n_q, heads] fp32);
     rows of tokens at or behind q_len are left as they were."""
-    dev = cache.device
-    _need("q", q, (torch.bfloat16,), dev)
-    if q.dim() != 4:
+    dev, c = cache.index, cache.c
+    _need("q", q, _BF16, dev)
+    shape = q.shape
+    if len(shape) != 4:
         raise ValueError("q: must be [batch, n_q, heads, 576]")
-    batch, n_q, heads, dim = q.shape
-    _table(cache, block_table, 0, k_len)
-    if k_len is None or block_table.shape[0] != batch:
-        raise ValueError(f"block_table, k_len: {block_table.shape[0]} sequences for {batch} in q")
+    batch, n_q, heads, dim = shape
+    seqs, pages, lens = _table(cache, block_table, k_len)
+    if lens is None or seqs != batch:
+        raise ValueError(f"block_table, k_len: {seqs} sequences for {batch} in q")
+    q_lens = None
     if q_len is not None:
         _need("q_len", q_len, _I32, dev)
         if q_len.numel() != batch:
             raise ValueError(f"q_len: {q_len.numel()} lengths for {batch} sequences")
-    p = DsaPagedMlaProblem(batch, n_q, heads, dim, 512, block_table.shape[1], cache.c.page_size,
-                           scale, flags)
+        q_lens = q_len.data_ptr()
+    p = DsaPagedMlaProblem(batch, n_q, heads, dim, 512, pages, c.page_size, scale, flags)
+    rows = batch * n_q * heads
     if out is None:
         out = _new(stream, lambda: torch.empty((batch, n_q, heads, 512), dtype=torch.bfloat16,
-                                               device=dev))
+                                               device=q.device))
     else:
-        _need("out", out, (torch.bfloat16,), dev)
-        if out.numel() != batch * n_q * heads * 512:
+        _need("out", out, _BF16, dev)
+        if out.numel() != rows * 512:
             raise ValueError(f"out: shape {tuple(out.shape)}")
     if out_lse is None:
-        out_lse = _new(stream, lambda: torch.empty((batch, n_q, heads), device=dev))
+        out_lse = _new(stream, lambda: torch.empty((batch, n_q, heads), device=q.device))
     else:
         _need("out_lse", out_lse, _F32, dev)
-        if out_lse.numel() != batch * n_q * heads:
+        if out_lse.numel() != rows:
             raise ValueError(f"out_lse: shape {tuple(out_lse.shape)}")
     if workspace is None:
         n = C.c_size_t(0)
         _check(lib.dsa_paged_mla_workspace_size(C.byref(p), C.byref(n)), "dsa_paged_mla")
-        workspace = _new(stream, lambda: torch.empty(n.value, dtype=torch.uint8, device=dev))
+        workspace = _new(stream, lambda: torch.empty(n.value, dtype=torch.uint8, device=q.device))
     else:
         _need("workspace", workspace, _U8, dev)
-    _on(dev, stream, "dsa_paged_mla", lib.dsa_paged_mla, C.byref(p), C.byref(cache.c),
-        q.data_ptr(), block_table.data_ptr(), k_len.data_ptr(),
-        None if q_len is None else q_len.data_ptr(), out.data_ptr(), out_lse.data_ptr(),
+    _on(dev, stream, "dsa_paged_mla", lib.dsa_paged_mla, C.byref(p), C.byref(c), q.data_ptr(),
+        block_table.data_ptr(), lens, q_lens, out.data_ptr(), out_lse.data_ptr(),
         workspace.data_ptr(), workspace.numel())
     return out, out_lse
 
