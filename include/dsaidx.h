@@ -400,7 +400,9 @@ int dsa_rope_frequencies(int32_t rot_dim, double base, int32_t scaling, double f
  *     otherwise x and out must not overlap, and no two places of out may be the same.
  *   pos [n_tokens] int32 (any sign), freq [rot_dim / 2] double, both on the device.
  * Angles are formed in 64 bits and reduced there, so far positions lose nothing.
- * rot_dim even, 2 .. 512, offset + rot_dim <= dim <= 65536, heads <= 65536. */
+ * rot_dim even, 2 .. 512, offset + rot_dim <= dim <= 65536, heads <= 65536, heads * dim and
+ * n_tokens below 2^31.  Pointers on element boundaries; 16-byte ones, with strides and
+ * parts that keep them, take the wide path. */
 #define DSA_FLAG_INTERLEAVED 16u
 #define DSA_FLAG_INVERSE 32u
 typedef struct {
@@ -428,8 +430,8 @@ int dsa_rope(const dsa_rope_problem* p, const void* x, const int32_t* pos, const
  * so a page may lie inside a larger block (other layers beside it).  An indexer key
  * cache has dim_q = 128, dim_raw = 0; a latent cache dim_q = 512, dim_raw = 64, or
  * dim_q = 0, dim_raw = 576 unquantised.  dim_q a multiple of 128, dim_raw of 8, both at
- * most 4096; page_size a power of two in [16, 4096]; codes and raw on 16-byte boundaries with page
- * strides that keep them there.  A plane whose width is 0 is NULL.
+ * most 4096; page_size a power of two in [16, 4096]; codes and raw on 16-byte boundaries
+ * with page strides that keep them there.  A plane whose width is 0 is NULL.
  * A block table [batch, max_pages] int32 (device) names the page that holds positions
  * j * page_size .. of a sequence.  Only the entries that cover k_len are read; one
  * outside [0, n_pages) is never followed: its rows read as zeros. */
@@ -447,7 +449,7 @@ typedef struct {
 /* Write n_tokens rows into the cache: row t of x (dim_q + dim_raw values of x_dtype
  * DSA_BF16 or DSA_F32, x_stride elements apart) goes to slots[t] = page * page_size + row
  * (device int64; a slot outside the cache, such as -1, skips the token).  No two tokens
- * may have the same slot.  Scales: amax / 448 over the group, as dsa_quantize_e4m3 (an
+ * may have the same slot; n_tokens below 2^31.  Scales: amax / 448 over the group, as dsa_quantize_e4m3 (an
  * all-zero group has scale 1), or with DSA_FLAG_POW2_SCALE the least power of two that is
  * at least that, which makes scale * code exact in bf16 (for dsa_paged_mla).
  * rope (optional, else NULL with pos and freq NULL): rotates the rot_dim values at
@@ -460,7 +462,8 @@ int dsa_cache_write(const dsa_cache* c, const void* x, int32_t x_dtype, int64_t 
                     const int32_t* pos, const double* freq, uint32_t flags, void* stream);
 
 /* Read positions [0, n_k) of each sequence into contiguous rows; rows at or behind
- * k_len[b] (device int32, NULL: n_k) are left as they were.  n_k <= max_pages * page_size.
+ * k_len[b] (device int32, NULL: n_k) are left as they were.  n_k <= max_pages * page_size,
+ * batch <= 65535, n_k <= 2^30; out on a 16-byte boundary.
  *   dsa_cache_read        out [batch, n_k, dim_q + dim_raw] of out_dtype DSA_BF16 (the kv
  *                         of dsa_sparse_mla) or DSA_F32
  *   dsa_cache_read_codes  out [batch, n_k, dim_q] e4m3 codes and out_scale [batch, n_k,
@@ -495,7 +498,9 @@ int dsa_cache_read_codes(const dsa_cache* c, const int32_t* block_table, int32_t
  * The softmax weights enter the value product in bf16 (fp32 accumulation); logits, maxima,
  * denominators and partial outputs are fp32.  Results do not depend on the run: the split
  * over positions follows from the lengths alone, and partials are joined in their order.
- * Supported: dim_qk 576, dim_v 512, heads 1 .. 128, max_pages * page_size <= 2^24.
+ * Supported: dim_qk 576, dim_v 512, heads 1 .. 128, max_pages * page_size <= 2^24, scale
+ * positive, batch * n_q * heads below 2^31 and, in tiles of 128, rows times positions of
+ * the whole batch below 2^30; q and out on 16-byte boundaries.
  * workspace: dsa_paged_mla_workspace_size() bytes, 16-byte aligned (status word first). */
 typedef struct {
   int32_t batch;
@@ -516,7 +521,8 @@ int dsa_paged_mla(const dsa_paged_mla_problem* p, const dsa_cache* c, const void
                   void* stream);
 
 /* Device status word recorded in `workspace` by the last call that used it
- * (DSA_OK, DSA_ERR_TIMEOUT or DSA_ERR_NONFINITE).  Synchronises `stream`. */
+ * (DSA_OK, DSA_ERR_TIMEOUT, DSA_ERR_NONFINITE, or DSA_ERR_INVALID from dsa_paged_mla).
+ * Synchronises `stream`. */
 int dsa_read_status(const void* workspace, void* stream);
 
 /* The DoSA block bounds themselves ("The new bottleneck of sparse attention",

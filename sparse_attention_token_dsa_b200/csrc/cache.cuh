@@ -104,7 +104,9 @@ constexpr int kRopeBatch = 4;    // units a thread holds at once
 // four units before it uses any, and the block forms the cosines and sines of its
 // tokens (once for all heads) while they are in flight.  Rows that are not aligned to
 // 16 bytes take the same path one pair at a time (VEC = false).
-// Measured: see the table of the operators.
+// Measured (B200, copy 6545 GB/s): 8192 tokens x 64 heads x 128 bf16 values, 64 of them
+// rotated in halves, 57 us, 4.7 TB/s; 2049 tokens x 64 heads x 576 fp32 values, interleaved,
+// 100 us, 6.0 TB/s.  Three units a thread of 3 blocks an SM took 53 and 103 us.
 template <typename T, bool VEC, bool INTER>
 __global__ void __launch_bounds__(kRopeThreads, 4) rope_kernel(const RopeArgs a) {
   using R = RowType<T>;
@@ -354,12 +356,15 @@ __device__ __forceinline__ float quantise(const float (&v)[2][8], float amax, bo
 }
 
 // 8 lanes take a row and hold four chunks of 128 values of it at once (rows of less than
-// four chunks: one chunk of each of two rows; of four took registers that cost more threads), two runs of 8 values a lane, 64 apart, so
-// each access of the 8 lanes is one contiguous run; a group's largest magnitude is a
-// three-step exchange between them and nothing is reread.  A scale that is a power of two
-// makes code * scale exact in bf16, so attention on the tensor cores reads the quantised
-// values without a second rounding; e4m3 being a floating format, it costs at most one
-// binade at the bottom of its range.
+// four chunks: one chunk of each of two rows; of four took registers that cost more
+// threads), two runs of 8 values a lane, 64 apart, so each access of the 8 lanes is one
+// contiguous run; a group's largest magnitude is a three-step exchange between them and
+// nothing is reread.  A scale that is a power of two makes code * scale exact in bf16, so
+// attention on the tensor cores reads the quantised values without a second rounding;
+// e4m3 being a floating format, it costs at most one binade at the bottom of its range.
+// Measured (B200): 131072 keys of 128 values 12.3 us, 4.2 TB/s (one row at a time took
+// 14.4); 8191 latent rows of 512 + 64 values, the 64 rotated, 6.2 us: as many as 32 rows,
+// so launch and latency (a slot, then its row, then the exchange) are all of it.
 template <typename T, bool VEC, bool TURN, int ROWS>
 __global__ void __launch_bounds__(kCacheThreads) cache_write_kernel(const CacheWriteArgs a) {
   constexpr int BATCH = ROWS > 1 ? ROWS : kCacheBatch, CHUNKS = BATCH / ROWS;
@@ -489,7 +494,10 @@ __device__ __forceinline__ void rows_to_read(const CacheReadArgs& a, int (&s)[RO
 
 // Values of a sequence's first n_k rows.  8 lanes take a row and hold four chunks of 128
 // values of it at once (or one chunk of each of four rows), two runs of 8 values a lane, 64
-// apart, so that each store of the 8 lanes is one contiguous run.
+// apart, so that each store of the 8 lanes is one contiguous run (16 codes a lane took 24
+// us where this takes 20.5).
+// Measured (B200): 49 thousand latent rows of 512 e4m3 + 64 bf16 values to bf16 20.5 us,
+// 4.3 TB/s; a row waits for its page, which waits for nothing else.
 template <typename T, int ROWS>
 __global__ void __launch_bounds__(kCacheThreads) cache_read_kernel(const CacheReadArgs a) {
   constexpr int CHUNKS = kCacheBatch / ROWS;
@@ -557,7 +565,8 @@ __global__ void __launch_bounds__(kCacheThreads) cache_read_kernel(const CacheRe
   }
 }
 
-// Codes and scales as they stand (the operands of the indexer's e4m3 scan).
+// Codes and scales as they stand (the operands of the indexer's e4m3 scan).  Measured
+// (B200): 32 sequences, 270 thousand keys of 128 codes, 14.4 us, 4.9 TB/s.
 template <int ROWS>
 __global__ void __launch_bounds__(kCacheThreads) cache_read_codes_kernel(const CacheReadArgs a) {
   constexpr int CHUNKS = kCacheBatch / ROWS;
