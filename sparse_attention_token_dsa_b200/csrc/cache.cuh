@@ -111,7 +111,11 @@ template <typename T, bool VEC, bool INTER>
 __global__ void __launch_bounds__(kRopeThreads, 4) rope_kernel(const RopeArgs a) {
   using R = RowType<T>;
   constexpr int N = VEC ? R::kVec : 1;
-  extern __shared__ float2 turns[];                  // [tpb][rot / 2]: m cos, m sin
+  // m cos, m sin of the tokens' angles, [tpb][rot / 2]; vectors take them two pairs at a
+  // time, [tpb][two of a unit][unit], so lanes beside one another read places beside one
+  // another
+  constexpr int P = VEC ? (INTER ? N / 2 : N) : 1;   // pairs of a unit
+  extern __shared__ __align__(16) float2 turns[];
   const int64_t t0 = (int64_t)blockIdx.x * a.tpb;
   const int nt = (int)(a.n_tokens - t0 < a.tpb ? a.n_tokens - t0 : a.tpb);
   const int half = a.rot >> 1;
@@ -138,9 +142,8 @@ __global__ void __launch_bounds__(kRopeThreads, 4) rope_kernel(const RopeArgs a)
       const int u = (int)(r - h * a.units);
       int d;
       if (u < a.pairs) {
-        const int j = INTER && VEC ? u * (N / 2) : u * N;   // first pair of the unit
-        d = a.offset + (INTER ? 2 * j : j);
-        tab[k] = (int)tl * half + j;
+        d = a.offset + (INTER ? 2 * P : P) * u;
+        tab[k] = (int)tl * half + (VEC ? 2 : 1) * u;
       } else {
         d = (u - a.pairs) * N;
         if (d >= a.offset) d += a.rot;
@@ -159,9 +162,10 @@ __global__ void __launch_bounds__(kRopeThreads, 4) rope_kernel(const RopeArgs a)
     }
     if (!ready) {
       for (int i = threadIdx.x; i < nt * half; i += kRopeThreads) {
-        const int tl = i / half;
-        const float2 cs = turn_of(a.pos[t0 + tl], a.freq[i - tl * half]);
-        turns[i] = make_float2(cs.x * a.mscale, cs.y * a.mscale * a.sign);
+        const int tl = i / half, pair = i - tl * half;
+        const float2 cs = turn_of(a.pos[t0 + tl], a.freq[pair]);
+        const int at = VEC ? (pair % P / 2 * a.pairs + pair / P) * 2 + (pair & 1) : pair;
+        turns[tl * half + at] = make_float2(cs.x * a.mscale, cs.y * a.mscale * a.sign);
       }
       __syncthreads();
       ready = true;
@@ -184,11 +188,13 @@ __global__ void __launch_bounds__(kRopeThreads, 4) rope_kernel(const RopeArgs a)
         float v[N];
         R::unpack(va[k], v);
 #pragma unroll
-        for (int j = 0; j < N / 2; ++j) {
-          const float2 cs = turns[tab[k] + j];
-          const float p = v[2 * j], q = v[2 * j + 1];
+        for (int j = 0; j < P; j += 2) {
+          const float4 cs = *reinterpret_cast<const float4*>(turns + tab[k] + j * a.pairs);
+          const float p = v[2 * j], q = v[2 * j + 1], r = v[2 * j + 2], s = v[2 * j + 3];
           v[2 * j] = p * cs.x - q * cs.y;
           v[2 * j + 1] = q * cs.x + p * cs.y;
+          v[2 * j + 2] = r * cs.z - s * cs.w;
+          v[2 * j + 3] = s * cs.z + r * cs.w;
         }
         __stcs(reinterpret_cast<uint4*>(po), R::pack(v));
       } else {
@@ -196,11 +202,13 @@ __global__ void __launch_bounds__(kRopeThreads, 4) rope_kernel(const RopeArgs a)
         R::unpack(va[k], v);
         R::unpack(vb[k], w);
 #pragma unroll
-        for (int j = 0; j < N; ++j) {
-          const float2 cs = turns[tab[k] + j];
-          const float p = v[j], q = w[j];
+        for (int j = 0; j < P; j += 2) {
+          const float4 cs = *reinterpret_cast<const float4*>(turns + tab[k] + j * a.pairs);
+          const float p = v[j], q = w[j], r = v[j + 1], s = w[j + 1];
           v[j] = p * cs.x - q * cs.y;
           w[j] = q * cs.x + p * cs.y;
+          v[j + 1] = r * cs.z - s * cs.w;
+          w[j + 1] = s * cs.z + r * cs.w;
         }
         __stcs(reinterpret_cast<uint4*>(po), R::pack(v));
         __stcs(reinterpret_cast<uint4*>(po + half), R::pack(w));
