@@ -433,7 +433,7 @@ int dsa_rope(const dsa_rope_problem* p, const void* x, const int32_t* pos, const
  * most 4096; page_size a power of two in [16, 4096]; codes and raw on 16-byte boundaries
  * with page strides that keep them there.  A plane whose width is 0 is NULL.
  * A block table [batch, max_pages] int32 (device) names the page that holds positions
- * j * page_size .. of a sequence.  Only the entries that cover k_len are read; one
+ * j * page_size .. of a sequence.  Only the entries that cover k_len matter; one of them
  * outside [0, n_pages) is never followed: its rows read as zeros. */
 typedef struct {
   int32_t n_pages;

@@ -95,20 +95,20 @@ struct RopeArgs {
 };
 
 constexpr int kRopeThreads = 256;
-constexpr int kRopeBatch = 4;    // units a thread holds at once
+constexpr int kRopeBatch = 3;    // units a thread holds at once
 
 // The work of a head is cut into units of one 16-byte vector: in the half layout a
 // pair unit is one vector of the first half and its partner in the second, in the
 // interleaved layout one vector holding whole pairs; the values outside the rotated
 // part are copy units (none when the call is in place).  A thread issues the loads of
-// four units before it uses any, and the block forms the cosines and sines of its
+// three units before it uses any, and the block forms the cosines and sines of its
 // tokens (once for all heads) while they are in flight.  Rows that are not aligned to
 // 16 bytes take the same path one pair at a time (VEC = false).
 // Measured (B200, copy 6545 GB/s): 8192 tokens x 64 heads x 128 bf16 values, 64 of them
-// rotated in halves, 57 us, 4.7 TB/s; 2049 tokens x 64 heads x 576 fp32 values, interleaved,
-// 100 us, 6.0 TB/s.  Three units a thread of 3 blocks an SM took 53 and 103 us.
+// rotated in halves, 48 us, 5.6 TB/s; 2049 tokens x 64 heads x 576 fp32 values, interleaved,
+// 95 us, 6.4 TB/s.  Four units and 4 blocks an SM took 51 and 96 us, two and 6 54 and 99.
 template <typename T, bool VEC, bool INTER>
-__global__ void __launch_bounds__(kRopeThreads, 4) rope_kernel(const RopeArgs a) {
+__global__ void __launch_bounds__(kRopeThreads, 5) rope_kernel(const RopeArgs a) {
   using R = RowType<T>;
   constexpr int N = VEC ? R::kVec : 1;
   // m cos, m sin of the tokens' angles, [tpb][rot / 2]; vectors take them two pairs at a
@@ -229,6 +229,7 @@ struct CachePlanes {
 constexpr int kCacheThreads = 256;
 constexpr int kCacheUnits = kCacheThreads / 8;   // 8 lanes take a row, in chunks of 128 values
 constexpr int kCacheBatch = 4;                   // chunks a lane holds at once
+constexpr int kReadBatch = 5;                    // where it reads values
 
 struct CacheWriteArgs {
   CachePlanes c;
@@ -363,16 +364,16 @@ __device__ __forceinline__ float quantise(const float (&v)[2][8], float amax, bo
   return s;
 }
 
-// 8 lanes take a row and hold four chunks of 128 values of it at once (rows of less than
-// four chunks: one chunk of each of two rows; of four took registers that cost more
-// threads), two runs of 8 values a lane, 64 apart, so each access of the 8 lanes is one
-// contiguous run; a group's largest magnitude is a three-step exchange between them and
+// 8 lanes take four chunks of 128 values of a row (blockIdx.y: which four), or, where rows
+// have less than four chunks, one chunk of each of two rows (of four took registers that
+// cost more threads), and hold them at once, two runs of 8 values a lane, 64 apart, so each
+// access of the 8 lanes is one contiguous run; a group's largest magnitude is a three-step exchange between them and
 // nothing is reread.  A scale that is a power of two makes code * scale exact in bf16, so
 // attention on the tensor cores reads the quantised values without a second rounding;
 // e4m3 being a floating format, it costs at most one binade at the bottom of its range.
-// Measured (B200): 131072 keys of 128 values 12.3 us, 4.2 TB/s (one row at a time took
-// 14.4); 8191 latent rows of 512 + 64 values, the 64 rotated, 6.2 us: as many as 32 rows,
-// so launch and latency (a slot, then its row, then the exchange) are all of it.
+// Measured (B200): 131072 keys of 128 values 10.3 us, 5.0 TB/s (with the values waiting
+// for the slots 12.3, and one row at a time 14.4); 8191 latent rows of 512 + 64 values, the
+// 64 rotated, 6.2 us and 32 of them 4.2: launch and latency.
 template <typename T, bool VEC, bool TURN, int ROWS>
 __global__ void __launch_bounds__(kCacheThreads) cache_write_kernel(const CacheWriteArgs a) {
   constexpr int BATCH = ROWS > 1 ? ROWS : kCacheBatch, CHUNKS = BATCH / ROWS;
@@ -380,64 +381,63 @@ __global__ void __launch_bounds__(kCacheThreads) cache_write_kernel(const CacheW
   const uint32_t mates = 0xffu << (threadIdx.x & 24);
   // (tokens and pages fit 32 bits; their places do not)
   const uint32_t token0 = blockIdx.x * (uint32_t)(ROWS * kCacheUnits) + (threadIdx.x >> 3);
-  int page[ROWS], row[ROWS];
-#pragma unroll
-  for (int r = 0; r < ROWS; ++r) {
-    const uint32_t token = token0 + r * kCacheUnits;
-    const int64_t slot = token < a.n_tokens ? a.slots[token] : -1;
-    const bool in = slot >= 0 && (slot >> a.c.page_shift) < a.c.n_pages;
-    page[r] = in ? (int)(slot >> a.c.page_shift) : -1;
-    row[r] = (int)slot & ((1 << a.c.page_shift) - 1);
-  }
+  const int c0 = blockIdx.y * CHUNKS;
   auto x_at = [&](int r) {
     return reinterpret_cast<const T*>(a.x) + (int64_t)(token0 + r * kCacheUnits) * a.x_ts;
   };
-#pragma unroll 1
-  for (int c0 = 0; c0 < a.items; c0 += CHUNKS) {
-    Run8<T, VEC> held[BATCH][2];
+  int64_t slot[ROWS];
 #pragma unroll
-    for (int k = 0; k < BATCH; ++k)
+  for (int r = 0; r < ROWS; ++r) {
+    const uint32_t token = token0 + r * kCacheUnits;
+    slot[r] = token < a.n_tokens ? a.slots[token] : -1;
+  }
+  // the values do not wait for the slots (a token that is skipped is read for nothing)
+  Run8<T, VEC> held[BATCH][2];
+#pragma unroll
+  for (int k = 0; k < BATCH; ++k)
+#pragma unroll
+    for (int h = 0; h < 2; ++h) {
+      const int d = (c0 + k % CHUNKS) * 128 + h * 64 + l * 8;
+      if (token0 + k / CHUNKS * kCacheUnits < a.n_tokens && d < width)
+        held[k][h].load(x_at(k / CHUNKS) + d);
+    }
+#pragma unroll
+  for (int k = 0; k < BATCH; ++k) {
+    const int r = k / CHUNKS, c = c0 + k % CHUNKS;
+    const int64_t page = slot[r] >> a.c.page_shift;
+    if (slot[r] < 0 || page >= a.c.n_pages || c >= a.items) continue;   // the same for the 8 lanes
+    const int row = (int)slot[r] & ((1 << a.c.page_shift) - 1);
+    float v[2][8];
+#pragma unroll
+    for (int h = 0; h < 2; ++h) {
+      held[k][h].get(v[h]);
+      if constexpr (TURN) {
+        const int d = c * 128 + h * 64 + l * 8;
+        if (d < width) turn8<T, VEC>(a, x_at(r), token0 + r * kCacheUnits, d, v[h]);
+      }
+    }
+    if (c < q_chunks) {
+      float amax = 0.f;
+#pragma unroll
+      for (int h = 0; h < 2; ++h)
+#pragma unroll
+        for (int j = 0; j < 8; ++j) amax = fmaxf(amax, fabsf(v[h][j]));
+      amax = fmaxf(amax, __shfl_xor_sync(mates, amax, 1));
+      amax = fmaxf(amax, __shfl_xor_sync(mates, amax, 2));
+      amax = fmaxf(amax, __shfl_xor_sync(mates, amax, 4));
+      uint2 code[2];
+      const float s = quantise(v, amax, a.pow2, code);
+      uint8_t* dst = a.c.codes + page * a.c.codes_ps + (int64_t)row * a.c.dim_q + c * 128;
+      *reinterpret_cast<uint2*>(dst + l * 8) = code[0];
+      *reinterpret_cast<uint2*>(dst + 64 + l * 8) = code[1];
+      if (l == 0) a.c.scale[page * a.c.scale_ps + row * q_chunks + c] = s;
+    } else {
+      __nv_bfloat16* dst = a.c.raw + page * a.c.raw_ps + (int64_t)row * a.c.dim_raw;
 #pragma unroll
       for (int h = 0; h < 2; ++h) {
-        const int d = (c0 + k % CHUNKS) * 128 + h * 64 + l * 8;
-        if (page[k / CHUNKS] >= 0 && d < width) held[k][h].load(x_at(k / CHUNKS) + d);
-      }
-#pragma unroll
-    for (int k = 0; k < BATCH; ++k) {
-      const int r = k / CHUNKS, c = c0 + k % CHUNKS;
-      if (page[r] < 0 || c >= a.items) continue;     // the same for the 8 lanes
-      float v[2][8];
-#pragma unroll
-      for (int h = 0; h < 2; ++h) {
-        held[k][h].get(v[h]);
-        if constexpr (TURN) {
-          const int d = c * 128 + h * 64 + l * 8;
-          if (d < width) turn8<T, VEC>(a, x_at(r), token0 + r * kCacheUnits, d, v[h]);
-        }
-      }
-      if (c < q_chunks) {
-        float amax = 0.f;
-#pragma unroll
-        for (int h = 0; h < 2; ++h)
-#pragma unroll
-          for (int j = 0; j < 8; ++j) amax = fmaxf(amax, fabsf(v[h][j]));
-        amax = fmaxf(amax, __shfl_xor_sync(mates, amax, 1));
-        amax = fmaxf(amax, __shfl_xor_sync(mates, amax, 2));
-        amax = fmaxf(amax, __shfl_xor_sync(mates, amax, 4));
-        uint2 code[2];
-        const float s = quantise(v, amax, a.pow2, code);
-        uint8_t* dst = a.c.codes + page[r] * a.c.codes_ps + (int64_t)row[r] * a.c.dim_q + c * 128;
-        *reinterpret_cast<uint2*>(dst + l * 8) = code[0];
-        *reinterpret_cast<uint2*>(dst + 64 + l * 8) = code[1];
-        if (l == 0) a.c.scale[page[r] * a.c.scale_ps + row[r] * q_chunks + c] = s;
-      } else {
-        __nv_bfloat16* dst = a.c.raw + page[r] * a.c.raw_ps + (int64_t)row[r] * a.c.dim_raw;
-#pragma unroll
-        for (int h = 0; h < 2; ++h) {
-          const int d = (c - q_chunks) * 128 + h * 64 + l * 8;
-          if (d < a.c.dim_raw)
-            *reinterpret_cast<uint4*>(dst + d) = RowType<__nv_bfloat16>::pack(v[h]);
-        }
+        const int d = (c - q_chunks) * 128 + h * 64 + l * 8;
+        if (d < a.c.dim_raw)
+          *reinterpret_cast<uint4*>(dst + d) = RowType<__nv_bfloat16>::pack(v[h]);
       }
     }
   }
@@ -492,120 +492,106 @@ __device__ __forceinline__ void rows_to_read(const CacheReadArgs& a, int (&s)[RO
 #pragma unroll
   for (int r = 0; r < ROWS; ++r) {
     s[r] = (blockIdx.x * ROWS + r) * kCacheUnits + (threadIdx.x >> 3);
-    page[r] = -1;
-    if (s[r] < len) {
-      page[r] = page_of(table, s[r], a.c.page_shift, a.c.n_pages);
-      if (page[r] < 0) page[r] = -2;
-    }
+    // (the table is read up to n_k, so as not to wait for the length)
+    const int p = s[r] < a.n_k ? page_of(table, s[r], a.c.page_shift, a.c.n_pages) : -1;
+    page[r] = s[r] < len ? (p < 0 ? -2 : p) : -1;
   }
 }
 
-// Values of a sequence's first n_k rows.  8 lanes take a row and hold four chunks of 128
-// values of it at once (or one chunk of each of four rows), two runs of 8 values a lane, 64
-// apart, so that each store of the 8 lanes is one contiguous run (16 codes a lane took 24
-// us where this takes 20.5).
-// Measured (B200): 49 thousand latent rows of 512 e4m3 + 64 bf16 values to bf16 20.5 us,
-// 4.3 TB/s; a row waits for its page, which waits for nothing else.
+// Values of a sequence's first n_k rows.  8 lanes take five chunks of 128 values of a row
+// (blockIdx.z: which five; a latent row is one run) or one chunk of each of four rows, and
+// hold them at once, two runs of 8 values a lane, 64 apart, so that each store of the 8
+// lanes is one contiguous run (16 codes a lane took 24 us where this takes 20).
+// Measured (B200): 49 thousand latent rows of 512 e4m3 + 64 bf16 values to bf16 19.7 us,
+// 4.5 TB/s, and four times as many 52 us, 5.2 TB/s.  Runs of four chunks took 22.6 us: the
+// second run of a row holds 64 values and looks its page up again.
 template <typename T, int ROWS>
 __global__ void __launch_bounds__(kCacheThreads) cache_read_kernel(const CacheReadArgs a) {
-  constexpr int CHUNKS = kCacheBatch / ROWS;
+  constexpr int BATCH = ROWS > 1 ? ROWS : kReadBatch, CHUNKS = BATCH / ROWS;
   const int l = threadIdx.x & 7, q_chunks = a.c.dim_q >> 7, width = a.c.dim_q + a.c.dim_raw;
+  const int c0 = blockIdx.z * CHUNKS;
   int s[ROWS], page[ROWS];
   rows_to_read<ROWS>(a, s, page);
-  const uint8_t* codes[ROWS];
-  const float* scale[ROWS];
-  const __nv_bfloat16* raw[ROWS];
-  T* out[ROWS];
+  uint4 w[BATCH][2];                           // 8 codes in half of one, or 8 bf16 values
+  float sc[BATCH];
 #pragma unroll
-  for (int r = 0; r < ROWS; ++r) {
-    const int64_t p = max(page[r], 0);
+  for (int k = 0; k < BATCH; ++k) {
+    const int r = k / CHUNKS, c = c0 + k % CHUNKS;
     const int at = s[r] & ((1 << a.c.page_shift) - 1);
-    codes[r] = a.c.codes + p * a.c.codes_ps + (int64_t)at * a.c.dim_q + l * 8;
-    scale[r] = a.c.scale + p * a.c.scale_ps + at * q_chunks;
-    raw[r] = a.c.raw + p * a.c.raw_ps + (int64_t)at * a.c.dim_raw;
-    out[r] = reinterpret_cast<T*>(a.out) + ((int64_t)blockIdx.y * a.n_k + s[r]) * width;
-  }
-#pragma unroll 1
-  for (int c0 = 0; c0 < q_chunks; c0 += CHUNKS) {
-    uint2 w[kCacheBatch][2];
-    float sc[kCacheBatch];
-#pragma unroll
-    for (int k = 0; k < kCacheBatch; ++k) {
-      const int r = k / CHUNKS, c = c0 + k % CHUNKS;
-      w[k][0] = w[k][1] = make_uint2(0, 0);
-      sc[k] = 1.f;
-      if (page[r] >= 0 && c < q_chunks) {
-        w[k][0] = *reinterpret_cast<const uint2*>(codes[r] + c * 128);
-        w[k][1] = *reinterpret_cast<const uint2*>(codes[r] + c * 128 + 64);
-        sc[k] = scale[r][c];
-      }
-    }
-#pragma unroll
-    for (int k = 0; k < kCacheBatch; ++k) {
-      const int r = k / CHUNKS, c = c0 + k % CHUNKS;
-      if (page[r] == -1 || c >= q_chunks) continue;
+    w[k][0] = w[k][1] = make_uint4(0, 0, 0, 0);
+    sc[k] = 1.f;
+    if (page[r] < 0) continue;
+    const int64_t p = page[r];
+    if (c < q_chunks) {
+      const uint8_t* from = a.c.codes + p * a.c.codes_ps + (int64_t)at * a.c.dim_q + c * 128 + l * 8;
 #pragma unroll
       for (int h = 0; h < 2; ++h) {
-        float v[8];
-        e4m3x4_values(w[k][h].x, sc[k], v);
-        e4m3x4_values(w[k][h].y, sc[k], v + 4);
-        store8(out[r] + c * 128 + h * 64 + l * 8, v);
+        const uint2 u = *reinterpret_cast<const uint2*>(from + h * 64);
+        w[k][h].x = u.x;
+        w[k][h].y = u.y;
+      }
+      sc[k] = a.c.scale[p * a.c.scale_ps + at * q_chunks + c];
+    } else {
+      const __nv_bfloat16* from = a.c.raw + p * a.c.raw_ps + (int64_t)at * a.c.dim_raw;
+#pragma unroll
+      for (int h = 0; h < 2; ++h) {
+        const int d = (c - q_chunks) * 128 + h * 64 + l * 8;
+        if (d < a.c.dim_raw) w[k][h] = *reinterpret_cast<const uint4*>(from + d);
       }
     }
   }
-#pragma unroll 1
-  for (int d0 = l * 8; d0 < a.c.dim_raw; d0 += 64 * CHUNKS) {
-    uint4 w[kCacheBatch];
 #pragma unroll
-    for (int k = 0; k < kCacheBatch; ++k) {
-      const int r = k / CHUNKS, d = d0 + k % CHUNKS * 64;
-      w[k] = make_uint4(0, 0, 0, 0);
-      if (page[r] >= 0 && d < a.c.dim_raw) w[k] = *reinterpret_cast<const uint4*>(raw[r] + d);
-    }
+  for (int k = 0; k < BATCH; ++k) {
+    const int r = k / CHUNKS, c = c0 + k % CHUNKS;
+    if (page[r] == -1) continue;
+    T* out = reinterpret_cast<T*>(a.out) + ((int64_t)blockIdx.y * a.n_k + s[r]) * width;
 #pragma unroll
-    for (int k = 0; k < kCacheBatch; ++k) {
-      const int r = k / CHUNKS, d = d0 + k % CHUNKS * 64;
-      if (page[r] == -1 || d >= a.c.dim_raw) continue;
+    for (int h = 0; h < 2; ++h) {
+      const int d = c * 128 + h * 64 + l * 8;
+      if (d >= width) continue;
       float v[8];
-      RowType<__nv_bfloat16>::unpack(w[k], v);
-      store8(out[r] + a.c.dim_q + d, v);
+      if (c < q_chunks) {
+        e4m3x4_values(w[k][h].x, sc[k], v);
+        e4m3x4_values(w[k][h].y, sc[k], v + 4);
+      } else {
+        RowType<__nv_bfloat16>::unpack(w[k][h], v);
+      }
+      store8(out + d, v);
     }
   }
 }
 
 // Codes and scales as they stand (the operands of the indexer's e4m3 scan).  Measured
-// (B200): 32 sequences, 270 thousand keys of 128 codes, 14.4 us, 4.9 TB/s.
+// (B200): 32 sequences, 270 thousand keys of 128 codes, 12.3 us, 5.8 TB/s.
 template <int ROWS>
 __global__ void __launch_bounds__(kCacheThreads) cache_read_codes_kernel(const CacheReadArgs a) {
   constexpr int CHUNKS = kCacheBatch / ROWS;
   const int l = threadIdx.x & 7, q_chunks = a.c.dim_q >> 7;
   int s[ROWS], page[ROWS];
   rows_to_read<ROWS>(a, s, page);
-#pragma unroll 1
-  for (int c0 = 0; c0 < q_chunks; c0 += CHUNKS) {
-    uint4 w[kCacheBatch];
-    float sc[kCacheBatch];
+  const int c0 = blockIdx.z * CHUNKS;
+  uint4 w[kCacheBatch];
+  float sc[kCacheBatch];
 #pragma unroll
-    for (int k = 0; k < kCacheBatch; ++k) {
-      const int r = k / CHUNKS, c = c0 + k % CHUNKS;
-      w[k] = make_uint4(0, 0, 0, 0);
-      sc[k] = 1.f;
-      if (page[r] >= 0 && c < q_chunks) {
-        const int at = s[r] & ((1 << a.c.page_shift) - 1);
-        w[k] = *reinterpret_cast<const uint4*>(a.c.codes + page[r] * a.c.codes_ps +
-                                               (int64_t)at * a.c.dim_q + c * 128 + l * 16);
-        sc[k] = a.c.scale[page[r] * a.c.scale_ps + at * q_chunks + c];
-      }
+  for (int k = 0; k < kCacheBatch; ++k) {
+    const int r = k / CHUNKS, c = c0 + k % CHUNKS;
+    w[k] = make_uint4(0, 0, 0, 0);
+    sc[k] = 1.f;
+    if (page[r] >= 0 && c < q_chunks) {
+      const int at = s[r] & ((1 << a.c.page_shift) - 1);
+      w[k] = *reinterpret_cast<const uint4*>(a.c.codes + page[r] * a.c.codes_ps +
+                                             (int64_t)at * a.c.dim_q + c * 128 + l * 16);
+      sc[k] = a.c.scale[page[r] * a.c.scale_ps + at * q_chunks + c];
     }
+  }
 #pragma unroll
-    for (int k = 0; k < kCacheBatch; ++k) {
-      const int r = k / CHUNKS, c = c0 + k % CHUNKS;
-      if (page[r] == -1 || c >= q_chunks) continue;
-      const int64_t to = (int64_t)blockIdx.y * a.n_k + s[r];
-      *reinterpret_cast<uint4*>(reinterpret_cast<uint8_t*>(a.out) + to * a.c.dim_q + c * 128 +
-                                l * 16) = w[k];
-      if (l == 0) a.out_scale[to * q_chunks + c] = sc[k];
-    }
+  for (int k = 0; k < kCacheBatch; ++k) {
+    const int r = k / CHUNKS, c = c0 + k % CHUNKS;
+    if (page[r] == -1 || c >= q_chunks) continue;
+    const int64_t to = (int64_t)blockIdx.y * a.n_k + s[r];
+    *reinterpret_cast<uint4*>(reinterpret_cast<uint8_t*>(a.out) + to * a.c.dim_q + c * 128 +
+                              l * 16) = w[k];
+    if (l == 0) a.out_scale[to * q_chunks + c] = sc[k];
   }
 }
 

@@ -43,7 +43,7 @@ int launch_rope(RopeArgs& a, int dim, bool vec, bool inter, bool in_place, cudaS
   a.per_unit = a.units > 1 && (uint64_t)a.heads * a.units * a.units < 1ull << 32
                    ? (uint32_t)(((1ull << 32) + a.units - 1) / a.units)
                    : 0;
-  // a block takes about 1024 units (four a thread): several tokens of few heads, or a
+  // a block takes about 768 units (three a thread): several tokens of few heads, or a
   // part of one token's heads
   const int64_t per_token = (int64_t)a.heads * a.units;
   const int64_t target = kRopeThreads * kRopeBatch;
@@ -136,17 +136,19 @@ WriteKernel write_kernel(bool vec, bool turn, bool few) {
              : (turn ? cache_write_kernel<T, false, true, 1> : cache_write_kernel<T, false, false, 1>);
 }
 
-// Arguments shared by the two reads; *grid: x is 0 where there is nothing to read.
+// Arguments shared by the two reads; *grid: x is 0 where there is nothing to read, z
+// counts the threads' runs of chunks.
 int read_args(const dsa_cache* c, const int32_t* table, int32_t batch, int32_t max_pages,
-              int32_t n_k, const int32_t* k_len, void* out, bool few, CacheReadArgs* a,
-              dim3* grid) {
+              int32_t n_k, const int32_t* k_len, void* out, bool few, int at_once,
+              CacheReadArgs* a, dim3* grid) {
   const int v = validate_cache(c);
   if (v != DSA_OK) return v;
   if (!table || !out || batch < 1 || n_k < 0 || max_pages < 0) return DSA_ERR_INVALID;
   if (!aligned(table, 4) || !aligned(k_len, 4)) return DSA_ERR_INVALID;
   if ((int64_t)max_pages * c->page_size < n_k || !aligned16(out)) return DSA_ERR_INVALID;
   if (batch > 65535 || n_k > (1 << 30)) return DSA_ERR_UNSUPPORTED;
-  *grid = dim3(row_blocks(n_k, few ? 4 : 1), (unsigned)batch);
+  *grid = dim3(row_blocks(n_k, few ? 4 : 1), (unsigned)batch,
+               few ? chunks_of(c) : (chunks_of(c) + at_once - 1) / at_once);
   a->c = planes(c);
   a->table = table;
   a->k_len = k_len;
@@ -358,7 +360,9 @@ int dsa_cache_write(const dsa_cache* c, const void* x, int32_t x_dtype, int64_t 
   cudaStream_t st = reinterpret_cast<cudaStream_t>(stream);
   auto kern = x_dtype == DSA_BF16 ? write_kernel<__nv_bfloat16>(vec, rope != nullptr, few)
                                   : write_kernel<float>(vec, rope != nullptr, few);
-  kern<<<row_blocks(n_tokens, few ? 2 : 1), kCacheThreads, 0, st>>>(a);
+  const dim3 grid(row_blocks(n_tokens, few ? 2 : 1),
+                  few ? a.items : (a.items + kCacheBatch - 1) / kCacheBatch);
+  kern<<<grid, kCacheThreads, 0, st>>>(a);
   return launch_status();
 }
 
@@ -368,7 +372,7 @@ int dsa_cache_read(const dsa_cache* c, const int32_t* block_table, int32_t batch
   CacheReadArgs a{};
   dim3 blocks;
   const bool few = c && few_chunks(chunks_of(c));
-  const int v = read_args(c, block_table, batch, max_pages, n_k, k_len, out, few, &a,
+  const int v = read_args(c, block_table, batch, max_pages, n_k, k_len, out, few, kReadBatch, &a,
                           &blocks);
   if (v != DSA_OK) return v;
   if (out_dtype != DSA_BF16 && out_dtype != DSA_F32) return DSA_ERR_UNSUPPORTED;
@@ -387,7 +391,7 @@ int dsa_cache_read_codes(const dsa_cache* c, const int32_t* block_table, int32_t
   CacheReadArgs a{};
   dim3 blocks;
   const bool few = c && few_chunks(chunks_of(c));
-  const int v = read_args(c, block_table, batch, max_pages, n_k, k_len, out, few, &a,
+  const int v = read_args(c, block_table, batch, max_pages, n_k, k_len, out, few, kCacheBatch, &a,
                           &blocks);
   if (v != DSA_OK) return v;
   if (!out_scale || !aligned(out_scale, 4) || c->dim_q == 0) return DSA_ERR_INVALID;
