@@ -753,8 +753,16 @@ __global__ void __cluster_dims__(2, 1, 1)
       // pages looked up a tile before that.
       const float* const scale0 = a.c.scale;
       auto scales = [&](int page, int key) {         // of a row
-        const int64_t p = page < a.c.n_pages ? page : 0;
+        const int64_t p = (uint32_t)page < (uint32_t)a.c.n_pages ? page : 0;
         return scale0 + p * a.c.scale_ps + (int64_t)(key & mask) * 4;
+      };
+      // page of a row to come, as the table has it: used a tile later, so that nobody waits
+      // for it (a wrong entry has no live rows; the warps that copy record it)
+      auto entry_of = [&](int key) { return key < s.pair.kl ? table[key >> shift] : -1; };
+      // a filled and a free slot, asked for together
+      auto wait_two = [&](uint64_t* full, uint32_t fp, uint64_t* empty, uint32_t ep) -> bool {
+        const bool a0 = mbar_try_wait(full, fp), a1 = mbar_try_wait(empty, ep);
+        return wait_seen(a0, full, fp, 59) && wait_seen(a1, empty, ep, 62);
       };
       auto ready = [&](uint32_t bar) {
         fence_proxy_async_smem();
@@ -770,7 +778,7 @@ __global__ void __cluster_dims__(2, 1, 1)
         uint32_t live = 0;                           // bit: the row of `next` is one
         auto look = [&](int tile) {
 #pragma unroll
-          for (int h = 0; h < 2; ++h) page[h] = page_at(tile * kPmKeys + 64 * rank + h * 32 + lane);
+          for (int h = 0; h < 2; ++h) page[h] = entry_of(tile * kPmKeys + 64 * rank + h * 32 + lane);
         };
         auto load = [&](int tile) {
           live = 0;
@@ -779,7 +787,7 @@ __global__ void __cluster_dims__(2, 1, 1)
             const float* sc = scales(page[h], tile * kPmKeys + 64 * rank + h * 32 + lane);
             next[h][0] = sc[w >> 1];
             next[h][1] = sc[(w >> 1) + 2];
-            live |= (page[h] < a.c.n_pages ? 1u : 0u) << h;
+            live |= ((uint32_t)page[h] < (uint32_t)a.c.n_pages ? 1u : 0u) << h;
           }
         };
         while (ok && pm_next(a, walk, s)) {
@@ -846,14 +854,14 @@ __global__ void __cluster_dims__(2, 1, 1)
         uint32_t live = 0;                           // bit: the row of `next` is one
         auto look = [&](int tile) {
 #pragma unroll
-          for (int j = 0; j < 2; ++j) page[j] = page_at(tile * kPmKeys + (odd + 2 * j) * 32 + lane);
+          for (int j = 0; j < 2; ++j) page[j] = entry_of(tile * kPmKeys + (odd + 2 * j) * 32 + lane);
         };
         auto load = [&](int tile) {
           live = 0;
 #pragma unroll
           for (int j = 0; j < 2; ++j) {
             next[j] = scales(page[j], tile * kPmKeys + (odd + 2 * j) * 32 + lane)[rank * 2 + b];
-            live |= (page[j] < a.c.n_pages ? 1u : 0u) << j;
+            live |= ((uint32_t)page[j] < (uint32_t)a.c.n_pages ? 1u : 0u) << j;
           }
         };
         while (ok && pm_next(a, walk, s)) {
