@@ -190,20 +190,22 @@ bool map_pages(CUtensorMap* m, const dsa_cache* c, uint32_t box_rows, uint32_t b
             CU_TENSOR_MAP_L2_PROMOTION_L2_256B, CU_TENSOR_MAP_FLOAT_OOB_FILL_NONE) == CUDA_SUCCESS;
 }
 
-// 3-D map over rows of a plane [pages][page][width bytes or words]: box of 128 bytes x
-// box_rows x one page; a page past the end reads as zeros.
-bool map_rows(CUtensorMap* m, const dsa_cache* c, bool codes, uint32_t box_rows) {
+// 3-D map over rows of a plane [pages][page][width bytes or words]: box of 64 or 128 bytes x
+// box_rows x one page, swizzled over as many; a page past the end reads as zeros.
+bool map_rows(CUtensorMap* m, const dsa_cache* c, bool codes, uint32_t box_bytes,
+              uint32_t box_rows) {
   EncodeTiledFn fn = encode_fn();
   if (!fn) return false;
   const uint64_t esz = codes ? 1 : 2, width = codes ? kPmDv : kPmDqk - kPmDv;
   const uint64_t stride = (uint64_t)(codes ? c->codes_page_stride : c->raw_page_stride);
   cuuint64_t dims[3] = {width, (cuuint64_t)c->page_size, (cuuint64_t)c->n_pages};
   cuuint64_t strides[2] = {width * esz, stride * esz};
-  cuuint32_t box[3] = {(cuuint32_t)(128 / esz), box_rows, 1};
+  cuuint32_t box[3] = {(cuuint32_t)(box_bytes / esz), box_rows, 1};
   cuuint32_t estr[3] = {1, 1, 1};
   return fn(m, codes ? CU_TENSOR_MAP_DATA_TYPE_UINT8 : CU_TENSOR_MAP_DATA_TYPE_BFLOAT16, 3,
             codes ? c->codes : c->raw, dims, strides, box, estr, CU_TENSOR_MAP_INTERLEAVE_NONE,
-            CU_TENSOR_MAP_SWIZZLE_128B, CU_TENSOR_MAP_L2_PROMOTION_L2_256B,
+            box_bytes == 64 ? CU_TENSOR_MAP_SWIZZLE_64B : CU_TENSOR_MAP_SWIZZLE_128B,
+            CU_TENSOR_MAP_L2_PROMOTION_L2_256B,
             CU_TENSOR_MAP_FLOAT_OOB_FILL_NONE) == CUDA_SUCCESS;
 }
 
@@ -437,9 +439,9 @@ int dsa_paged_mla(const dsa_paged_mla_problem* p, const dsa_cache* c, const void
   if (!map_query(&qm, q, (uint64_t)p->batch * p->n_q * p->heads)) return DSA_ERR_CUDA;
   const uint32_t page = (uint32_t)c->page_size;
   if (codes) {
-    if (!map_rows(&km, c, true, page < 64 ? page : 64) ||
-        !map_rows(&vm, c, true, page < 32 ? page : 32) ||
-        !map_rows(&rm, c, false, page < 32 ? page : 32))
+    if (!map_rows(&km, c, true, 64, page < 64 ? page : 64) ||
+        !map_rows(&vm, c, true, 128, page < 32 ? page : 32) ||
+        !map_rows(&rm, c, false, 128, page < 64 ? page : 64))
       return DSA_ERR_CUDA;
   } else {
     // K: one copy a slot where a page holds its rows, else one a page and chunk; V: one a page

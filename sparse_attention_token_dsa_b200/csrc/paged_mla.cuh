@@ -54,15 +54,15 @@ constexpr int kPmRows = 128;            // rows of a tile (64 a CTA)
 constexpr int kPmKeys = 128;            // positions of a tile
 constexpr int kPmChunk = 64 * 128;      // 64 positions (or rows) x 64 values in bf16
 constexpr int kPmSlice = 4 * 32 * 128;  // 32 positions x 256 values
-// Rings of operand slots: bf16 rows are copied into them, a tile's worth; e4m3 rows are
-// copied as they are (a tile of codes of K and one of V) and converted into shorter rings.
+// Rings of operand slots, a tile's worth.  bf16 rows are copied into them; e4m3 rows are
+// copied into the upper half of where their values go (a chunk of K, half a slice of V) and
+// converted in place, the lower half first.
 template <bool CODES>
 struct PmRing {
-  static constexpr int kKSlots = CODES ? 5 : 3;      // of K
+  static constexpr int kKSlots = CODES ? 9 : 3;      // of K
   static constexpr int kChunks = CODES ? 1 : 3;      // in a slot of K
-  static constexpr int kVSlots = CODES ? 2 : 4;      // slices of V
+  static constexpr int kVSlots = 4;                  // slices of V
   static constexpr int kKBytes = kChunks * kPmChunk;
-  static constexpr int kCodes = CODES ? 4 * 8192 : 0;   // of K, and of V
   // Chunk of q that meets the k-th chunk of K: in e4m3 the bf16 chunk comes first, as it
   // needs no conversion.
   __device__ __forceinline__ static int q_chunk(int k) { return CODES ? (k == 0 ? 8 : k - 1) : k; }
@@ -98,9 +98,8 @@ struct PagedMlaArgs {
 
 struct PagedMlaTail {
   uint64_t q_full, q_empty, q_ready, o_empty, p_full, pv_done, drain[2];
-  uint64_t k_full[5], k_ready[5], k_empty[5];
+  uint64_t k_full[9], k_ready[9], k_empty[9];
   uint64_t v_full[4], v_ready[4], v_empty[4];
-  uint64_t codes_full[2][4], codes_empty[2][4];      // of K, of V
   uint64_t s_full[2], s_empty[2];
   float peer[2][128];      // maxima (and at the end denominators) of a row's two threads
   int32_t start_pair, start_off, count, share;
@@ -113,9 +112,8 @@ constexpr size_t paged_mla_smem_bytes() {
          PmRing<false>::kVSlots * kPmSlice + kPmPBytes + sizeof(PagedMlaTail);
 }
 static_assert(paged_mla_smem_bytes() <= 227 * 1024, "shared memory of one CTA");
-static_assert(PmRing<true>::kKSlots * PmRing<true>::kKBytes + PmRing<true>::kVSlots * kPmSlice +
-                      2 * PmRing<true>::kCodes ==
-                  PmRing<false>::kKSlots * PmRing<false>::kKBytes + PmRing<false>::kVSlots * kPmSlice,
+static_assert(PmRing<true>::kKSlots * PmRing<true>::kKBytes ==
+                  PmRing<false>::kKSlots * PmRing<false>::kKBytes,
               "both forms fill the same space");
 
 // ------------------------------------------------------------------- work --
@@ -240,22 +238,21 @@ __device__ __forceinline__ void tmem_st8(uint32_t taddr, const uint32_t (&r)[8])
 // 16 e4m3 codes times a scale as bf16.  A code's exponent and mantissa, moved to where
 // bf16 has its own, are the value times 2^-120 (also for e4m3's subnormal codes, which
 // become bf16's), so one packed product with 2^120 scale gives two values, exactly, where
-// the scale is a power of two of at most 2^7: five instructions for two codes, none of
-// them a conversion (those run at a quarter of the rate) and only two of them for the
-// integer units: with a code in the lower byte of a half, 16 t moves all of it and leaves
-// the sign at bit 11, and 240 (t & 0x80) = 2^15 - 2^11 carries that on to bit 15.
+// the scale is a power of two of at most 2^7: four instructions for two codes, none of
+// them a conversion (those run at a quarter of the rate).  `sel` spreads two bytes over
+// halves with their signs above them, so a shift by 4 leaves the sign at bit 15 and its
+// copies, masked away, below it.
 __device__ __forceinline__ uint32_t two_codes(uint32_t w, uint32_t sel, uint32_t mul) {
-  const uint32_t t = __byte_perm(w, 0, sel);
-  const uint32_t v = t * 16u + (t & 0x00800080u) * 240u;
-  uint32_t r;
-  asm("mul.rn.bf16x2 %0, %1, %2;" : "=r"(r) : "r"(v), "r"(mul));
+  uint32_t t, r;
+  asm("prmt.b32 %0, %1, 0, %2;" : "=r"(t) : "r"(w), "r"(sel));
+  asm("mul.rn.bf16x2 %0, %1, %2;" : "=r"(r) : "r"((t << 4) & 0x87f087f0u), "r"(mul));
   return r;
 }
 __device__ __forceinline__ void codes_to_bf16(const uint4& w, uint32_t mul, uint4& lo, uint4& hi) {
-  lo = make_uint4(two_codes(w.x, 0x4140, mul), two_codes(w.x, 0x4342, mul),
-                  two_codes(w.y, 0x4140, mul), two_codes(w.y, 0x4342, mul));
-  hi = make_uint4(two_codes(w.z, 0x4140, mul), two_codes(w.z, 0x4342, mul),
-                  two_codes(w.w, 0x4140, mul), two_codes(w.w, 0x4342, mul));
+  lo = make_uint4(two_codes(w.x, 0x9180, mul), two_codes(w.x, 0xb3a2, mul),
+                  two_codes(w.y, 0x9180, mul), two_codes(w.y, 0xb3a2, mul));
+  hi = make_uint4(two_codes(w.z, 0x9180, mul), two_codes(w.z, 0xb3a2, mul),
+                  two_codes(w.w, 0x9180, mul), two_codes(w.w, 0xb3a2, mul));
 }
 // 2^120 scale in both halves; 0 where the short way does not hold.
 __device__ __forceinline__ uint32_t code_factor(float scale) {
@@ -266,11 +263,11 @@ __device__ __forceinline__ uint32_t code_factor(float scale) {
 }
 // Any scale: four units, in fp32, rounded to bf16 once (out of line, for scales that
 // dsa_cache_write does not make).
-__device__ __noinline__ void four_units_any(const uint8_t* const* from, uint8_t* const* to_lo,
+__device__ __noinline__ void four_units_any(const uint4* codes, uint8_t* const* to_lo,
                                             uint8_t* const* to_hi, float scale) {
 #pragma unroll 1
   for (int u = 0; u < 4; ++u) {
-    const uint4 w = *reinterpret_cast<const uint4*>(from[u]);
+    const uint4 w = codes[u];
     float v[16];
     e4m3x4_values(w.x, scale, v);
     e4m3x4_values(w.y, scale, v + 4);
@@ -286,13 +283,15 @@ __device__ __noinline__ void four_units_any(const uint8_t* const* from, uint8_t*
         bf16x2(v[8], v[9]), bf16x2(v[10], v[11]), bf16x2(v[12], v[13]), bf16x2(v[14], v[15]));
   }
 }
-// Four units of 16 codes in shared memory: from(u), to_lo(u), to_hi(u).
+// Four units of 16 codes in shared memory a lane, from(u) to to(u, 0) and to(u, 1).  The
+// warp has read all of them before it writes the first, as values may take codes' places.
 template <typename From, typename To>
 __device__ __forceinline__ void four_units(bool exact, uint32_t f, float scale, From from, To to) {
-  if (exact) {
-    uint4 w[4];
+  uint4 w[4];
 #pragma unroll
-    for (int u = 0; u < 4; ++u) w[u] = *reinterpret_cast<const uint4*>(from(u));
+  for (int u = 0; u < 4; ++u) w[u] = *reinterpret_cast<const uint4*>(from(u));
+  __syncwarp();
+  if (exact) {
 #pragma unroll
     for (int u = 0; u < 4; ++u) {
       uint4 lo, hi;
@@ -301,11 +300,11 @@ __device__ __forceinline__ void four_units(bool exact, uint32_t f, float scale, 
       *reinterpret_cast<uint4*>(to(u, 1)) = hi;
     }
   } else {
-    const uint8_t* a[4];
+    uint4 a[4];
     uint8_t *b[4], *c[4];
 #pragma unroll
     for (int u = 0; u < 4; ++u) {
-      a[u] = from(u);
+      a[u] = w[u];
       b[u] = to(u, 0);
       c[u] = to(u, 1);
     }
@@ -352,9 +351,7 @@ __global__ void __cluster_dims__(2, 1, 1)
   uint8_t* Ks = Qs + kPmQBytes;                      // [slots][chunks][64 positions x 128 B]
   uint8_t* Vs = Ks + Ring::kKSlots * Ring::kKBytes;  // [slots][4 blocks][32 positions x 128 B]
   uint8_t* Ps = Vs + Ring::kVSlots * kPmSlice;       // [2][64 rows x 128 B]
-  uint8_t* Kc = Ps + kPmPBytes;                      // [4 groups][64 positions x 128 codes]
-  uint8_t* Vc = Kc + Ring::kCodes;                   // [4 slices][2 groups][32 positions x 128]
-  PagedMlaTail* T = reinterpret_cast<PagedMlaTail*>(Vc + Ring::kCodes);
+  PagedMlaTail* T = reinterpret_cast<PagedMlaTail*>(Ps + kPmPBytes);
 
   const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
   const int rank = (int)cluster_rank();
@@ -368,7 +365,7 @@ __global__ void __cluster_dims__(2, 1, 1)
     mbar_init(&T->o_empty, 8);
     mbar_init(&T->p_full, 8);
     mbar_init(&T->pv_done, 1);
-    for (int i = 0; i < 5; ++i) {
+    for (int i = 0; i < 9; ++i) {
       mbar_init(&T->k_full[i], 1);
       mbar_init(&T->k_ready[i], 2);
       mbar_init(&T->k_empty[i], 1);
@@ -377,10 +374,6 @@ __global__ void __cluster_dims__(2, 1, 1)
       mbar_init(&T->v_full[i], 1);
       mbar_init(&T->v_ready[i], CODES ? 4 : 2);
       mbar_init(&T->v_empty[i], 1);
-      mbar_init(&T->codes_full[0][i], 1);
-      mbar_init(&T->codes_full[1][i], 1);
-      mbar_init(&T->codes_empty[0][i], 2);
-      mbar_init(&T->codes_empty[1][i], 2);
     }
     for (int i = 0; i < 2; ++i) {
       mbar_init(&T->s_full[i], 1);
@@ -679,45 +672,39 @@ __global__ void __cluster_dims__(2, 1, 1)
         }
       }
     } else if (warp == 6) {
-      // e4m3: codes of K, in 4 groups of 128 of 64 positions, and the bf16 chunk of K,
-      // straight into its slot
+      // e4m3: the bf16 chunk of K, and its codes in chunks of 64
       if (elect_one()) {
-        const int rows = min(1 << shift, 64), tail_rows = min(1 << shift, 32);   // of a copy
-        auto group = [&](int key, int g) -> bool {
-          if (!wait(&T->codes_empty[0][g], (n & 1) ^ 1, 62)) return false;
-          mbar_arrive_expect_tx(&T->codes_full[0][g], 8192);
-#pragma unroll 1
-          for (int j = 0; j < 64; j += rows)
-            tma_load_3d(Kc + g * 8192 + j * 128, &kmap, &T->codes_full[0][g], g * 128,
-                        (key + j) & mask, page_at(key + j));
-          return true;
-        };
-        uint32_t tails = 0;
+        const int rows = min(1 << shift, 64);        // of a copy
         while (ok && pm_next(a, walk, s)) {
           table = a.table + (int64_t)s.pair.b * a.max_pages;
 #pragma unroll 1
           for (int i = s.t0; i < s.t0 + s.n && ok; ++i, ++n) {
             const int key = i * kPmKeys + 64 * rank;
-            ok = group(key, 0) && group(key, 1);
-            const uint32_t u = n * 9, slot = u % Ring::kKSlots, use = u / Ring::kKSlots;
-            // Uses of a slot lie 5 chunks apart and these 9: the parity below tells the last
-            // use from the one before only once the tile before the last has been read.
-            if (n > 1) ok = ok && wait(&T->s_full[n & 1], ((n >> 1) & 1) ^ 1, 61);
-            ok = ok && wait(&T->k_empty[slot], (use & 1) ^ 1, 62);
-            if (!ok) break;
-            mbar_arrive_expect_tx(&T->k_full[0], kPmChunk);
+            const int z0 = page_at(key), z1 = rows < 64 ? page_at(key + rows) : 0;
+            const int z2 = rows < 32 ? page_at(key + 32) : 0, z3 = rows < 32 ? page_at(key + 48) : 0;
 #pragma unroll 1
-            for (int j = 0; j < 64; j += tail_rows)
-              tma_load_3d(Ks + slot * kPmChunk + j * 128, &rmap, &T->k_full[0], 0,
-                          (key + j) & mask, page_at(key + j));
-            ++tails;
-            ok = group(key, 2) && group(key, 3);
+            for (int k = 0; k < Ring::kKSlots; ++k) {
+              ok = wait(&T->k_empty[k], (n & 1) ^ 1, 62);
+              if (!ok) break;
+              const bool tail = k == 0;
+              mbar_arrive_expect_tx(&T->k_full[k], tail ? kPmChunk : kPmChunk / 2);
+              uint8_t* dst = Ks + k * kPmChunk + (tail ? 0 : kPmChunk / 2);
+              const CUtensorMap* map = tail ? &rmap : &kmap;
+              const int x = tail ? 0 : (k - 1) * 64, step = rows * (tail ? 128 : 64);
+              tma_load_3d(dst, map, &T->k_full[k], x, key & mask, z0);
+              if (rows < 64) {                       // pages below one another
+                tma_load_3d(dst + step, map, &T->k_full[k], x, 0, z1);
+                if (rows < 32) {
+                  tma_load_3d(dst + 2 * step, map, &T->k_full[k], x, 0, z2);
+                  tma_load_3d(dst + 3 * step, map, &T->k_full[k], x, 0, z3);
+                }
+              }
+            }
           }
         }
-        if (!ok && tails) drain_slot(&T->k_full[0], tails);
-        for (int g = 0; g < 4 && n; ++g)
-          if (ok) wait(&T->codes_empty[0][g], (n & 1) ^ 1, 64);
-          else drain_slot(&T->codes_full[0][g], n);
+        for (int k = 0; k < Ring::kKSlots && n; ++k)
+          if (ok) wait(&T->k_empty[k], (n & 1) ^ 1, 64);
+          else drain_slot(&T->k_full[k], n);
       }
     } else if (warp == 7) {
       // the codes of V, in slices of 32 positions
@@ -728,28 +715,28 @@ __global__ void __cluster_dims__(2, 1, 1)
 #pragma unroll 1
           for (int i = s.t0; i < s.t0 + s.n && ok; ++i, ++n) {
 #pragma unroll 1
-            for (int v = 0; v < 4; ++v) {
-              ok = wait(&T->codes_empty[1][v], (n & 1) ^ 1, 63);
+            for (int v = 0; v < Ring::kVSlots; ++v) {
+              const int key = i * kPmKeys + v * 32;
+              const int z0 = page_at(key), z1 = rows < 32 ? page_at(key + 16) : 0;
+              ok = wait(&T->v_empty[v], (n & 1) ^ 1, 63);
               if (!ok) break;
-              mbar_arrive_expect_tx(&T->codes_full[1][v], 8192);
+              mbar_arrive_expect_tx(&T->v_full[v], kPmSlice / 2);
 #pragma unroll 1
-              for (int j = 0; j < 32; j += rows) {
-                const int key = i * kPmKeys + v * 32 + j;
-                const int page = page_at(key);
-                tma_load_3d(Vc + v * 8192 + j * 128, &vmap, &T->codes_full[1][v], rank * 256,
-                            key & mask, page);
-                tma_load_3d(Vc + v * 8192 + 4096 + j * 128, &vmap, &T->codes_full[1][v],
-                            rank * 256 + 128, key & mask, page);
+              for (int b = 0; b < 2; ++b) {          // groups of 128 values
+                uint8_t* dst = Vs + v * kPmSlice + b * 8192 + 4096;
+                const int x = rank * 256 + b * 128;
+                tma_load_3d(dst, &vmap, &T->v_full[v], x, key & mask, z0);
+                if (rows < 32) tma_load_3d(dst + 2048, &vmap, &T->v_full[v], x, 0, z1);
               }
             }
           }
         }
-        for (int v = 0; v < 4 && n; ++v)
-          if (ok) wait(&T->codes_empty[1][v], (n & 1) ^ 1, 65);
-          else drain_slot(&T->codes_full[1][v], n);
+        for (int v = 0; v < Ring::kVSlots && n; ++v)
+          if (ok) wait(&T->v_empty[v], (n & 1) ^ 1, 65);
+          else drain_slot(&T->v_full[v], n);
       }
     } else {
-      // Conversion of codes into slots.  Scales are loaded a tile ahead and their rows'
+      // Conversion of codes in their slots.  Scales are loaded a tile ahead and their rows'
       // pages looked up a tile before that.
       const float* const scale0 = a.c.scale;
       auto scales = [&](int page, int key) {         // of a row
@@ -759,11 +746,6 @@ __global__ void __cluster_dims__(2, 1, 1)
       // page of a row to come, as the table has it: used a tile later, so that nobody waits
       // for it (a wrong entry has no live rows; the warps that copy record it)
       auto entry_of = [&](int key) { return key < s.pair.kl ? table[key >> shift] : -1; };
-      // a filled and a free slot, asked for together
-      auto wait_two = [&](uint64_t* full, uint32_t fp, uint64_t* empty, uint32_t ep) -> bool {
-        const bool a0 = mbar_try_wait(full, fp), a1 = mbar_try_wait(empty, ep);
-        return wait_seen(a0, full, fp, 59) && wait_seen(a1, empty, ep, 62);
-      };
       auto ready = [&](uint32_t bar) {
         fence_proxy_async_smem();
         __syncwarp();
@@ -810,40 +792,31 @@ __global__ void __cluster_dims__(2, 1, 1)
               ok = wait(&T->k_full[0], n & 1, 60);
               ok = __all_sync(0xffffffffu, ok);
               if (!ok) break;
-              if (lane == 0) mbar_arrive_cluster(k_ready + (n * 9 % Ring::kKSlots) * 8);
+              if (lane == 0) mbar_arrive_cluster(k_ready);
             }
 #pragma unroll 1
             for (int j = 0; j < 2; ++j) {
-              const int c = w + 4 * j, g = c >> 1;
+              const int slot = 1 + w + 4 * j;
               const float s0 = j ? now[0][1] : now[0][0], s1 = j ? now[1][1] : now[1][0];
               const uint32_t f0 = code_factor(s0), f1 = code_factor(s1);
               const bool exact =
                   __all_sync(0xffffffffu, (f0 != 0 || !(on & 1)) && (f1 != 0 || !(on & 2)));
-              const uint32_t use = n * 9 + 1 + c, slot = use % Ring::kKSlots;
-              ok = ok && wait(&T->codes_full[0][g], n & 1, 59) &&
-                   wait(&T->k_empty[slot], ((use / Ring::kKSlots) & 1) ^ 1, 62);
+              ok = ok && wait(&T->k_full[slot], n & 1, 59);
               ok = __all_sync(0xffffffffu, ok);
               if (!ok) break;
 #pragma unroll 1
               for (int h = 0; h < 2; ++h) {          // row h * 32 + lane
-                const uint8_t* from = Kc + g * 8192 + (h * 32 + lane) * 128;
                 uint8_t* to = Ks + slot * kPmChunk + (h * 32 + lane) * 128;
+                const uint8_t* from = Ks + slot * kPmChunk + kPmChunk / 2 + (h * 32 + lane) * 64;
                 four_units(
                     exact, h ? f1 : f0, h ? s1 : s0,
-                    [&](int u) { return from + ((((c & 1) * 4 + u) ^ (lane & 7)) << 4); },
+                    [&](int u) { return from + ((u ^ (lane >> 1 & 3)) << 4); },
                     [&](int u, int e) { return to + (((2 * u + e) ^ (lane & 7)) << 4); });
               }
               ready(k_ready + slot * 8);
-              if (lane == 0) mbar_arrive(&T->codes_empty[0][g]);
             }
           }
         }
-        // the last arrivals from the MMAs have come before the CTA may end
-        if (ok && w == 0 && lane == 0)
-          for (uint32_t i = 0; i < Ring::kKSlots && n; ++i) {
-            const uint32_t uses = (9 * n + Ring::kKSlots - 1 - i) / Ring::kKSlots;
-            wait(&T->k_empty[i], (uses & 1) ^ 1, 64);
-          }
       } else {
         // V: two warps take every second slice, one its first group of 128 values and one its
         // second, a lane a row (so that neither the loads nor the stores meet in a bank)
@@ -881,28 +854,21 @@ __global__ void __cluster_dims__(2, 1, 1)
               const float sc = j ? now[1] : now[0];
               const uint32_t f = code_factor(sc);
               const bool exact = __all_sync(0xffffffffu, f != 0 || !(on >> j & 1));
-              // both uses of a slot in a tile are these two warps'
-              ok = ok && wait(&T->codes_full[1][v], n & 1, 60) && wait(&T->v_empty[odd], j ^ 1, 63);
+              ok = ok && wait(&T->v_full[v], n & 1, 60);
               ok = __all_sync(0xffffffffu, ok);
               if (!ok) break;
 #pragma unroll 1
               for (int h = 0; h < 2; ++h) {          // block of 64 values
-                const uint8_t* from = Vc + v * 8192 + b * 4096 + lane * 128;
-                uint8_t* to = Vs + odd * kPmSlice + (2 * b + h) * 4096 + lane * 128;
+                const uint8_t* from = Vs + v * kPmSlice + b * 8192 + 4096 + lane * 128;
+                uint8_t* to = Vs + v * kPmSlice + b * 8192 + h * 4096 + lane * 128;
                 four_units(
                     exact, f, sc, [&](int u) { return from + (((4 * h + u) ^ (lane & 7)) << 4); },
                     [&](int u, int e) { return to + (((2 * u + e) ^ (lane & 7)) << 4); });
               }
-              ready(v_ready + odd * 8);
-              if (lane == 0) mbar_arrive(&T->codes_empty[1][v]);
+              ready(v_ready + v * 8);
             }
           }
         }
-        if (ok && w == 0 && lane == 0)
-          for (uint32_t i = 0; i < Ring::kVSlots && n; ++i) {
-            const uint32_t uses = (4 * n + Ring::kVSlots - 1 - i) / Ring::kVSlots;
-            wait(&T->v_empty[i], (uses & 1) ^ 1, 65);
-          }
       }
     }
   } else {
