@@ -997,15 +997,29 @@ __global__ void __cluster_dims__(2, 1, 1)
         if (rank == 0 && row == 0 && s.t0 == 0)
           a.plan[1 + s.p] = cl * T->share + (T->count - walk.left - s.n);
       }
+      // O goes out through the warp's own part of P (32 rows x 128 bytes, free now), so that
+      // a store covers whole lines of four rows: a store of each lane's own row, 32 lines
+      // an instruction, took 16 us a tile of rows.
       const float inv = l_run == 0.f ? 0.f : 1.f / l_run;
+      uint8_t* stage = Ps + warp * 4096;
+      const int first = rank * 64 + (warp & 1) * 32; // row of the tile of lane 0
+      const int step = s.whole ? 64 : 32;            // values in 128 bytes
+      uint8_t* to = s.whole ? reinterpret_cast<uint8_t*>(
+                                  a.out + ((int64_t)s.pair.b * a.n_q * a.heads + s.pair.row0 + first) * kPmDv +
+                                  half * 256)
+                            : reinterpret_cast<uint8_t*>(
+                                  a.part_o + ((int64_t)s.slot * kPmRows + first) * kPmDv + half * 256);
+      const int pitch = kPmDv * (s.whole ? 2 : 4);
+      const int live = s.pair.rows - first - (lane >> 3);   // rows from this lane's first
+      to += (lane >> 3) * pitch + (lane & 7) * 16;
 #pragma unroll 1
-      for (int c0 = 0; c0 < 256; c0 += 32) {
-        uint32_t ov[32];
-        tmem_ld32(tmem + lane_off + c0, ov);
-        tmem_ld_wait(ov);
-        if (mine) {
+      for (int c0 = 0; c0 < 256; c0 += step, to += 128) {
+#pragma unroll 1
+        for (int h = 0; h < step; h += 32) {
+          uint32_t ov[32];
+          tmem_ld32(tmem + lane_off + c0 + h, ov);
+          tmem_ld_wait(ov);
           if (s.whole) {
-            uint16_t* dst = a.out + grow * kPmDv + half * 256 + c0;
 #pragma unroll
             for (int j = 0; j < 32; j += 8) {
               uint32_t w4[4];
@@ -1013,15 +1027,27 @@ __global__ void __cluster_dims__(2, 1, 1)
               for (int u = 0; u < 4; ++u)
                 w4[u] = bf16x2(__uint_as_float(ov[j + 2 * u]) * inv,
                                __uint_as_float(ov[j + 2 * u + 1]) * inv);
-              *reinterpret_cast<uint4*>(dst + j) = make_uint4(w4[0], w4[1], w4[2], w4[3]);
+              *reinterpret_cast<uint4*>(stage + lane * 128 + (((h + j) / 8 ^ (lane & 7)) << 4)) =
+                  make_uint4(w4[0], w4[1], w4[2], w4[3]);
             }
           } else {
-            float* dst = a.part_o + prow * kPmDv + half * 256 + c0;
 #pragma unroll
             for (int j = 0; j < 32; j += 4)
-              *reinterpret_cast<uint4*>(dst + j) = make_uint4(ov[j], ov[j + 1], ov[j + 2], ov[j + 3]);
+              *reinterpret_cast<uint4*>(stage + lane * 128 + ((j / 4 ^ (lane & 7)) << 4)) =
+                  make_uint4(ov[j], ov[j + 1], ov[j + 2], ov[j + 3]);
           }
         }
+        __syncwarp();
+        uint4 line[8];                               // of rows 4 i + lane / 8
+#pragma unroll
+        for (int i = 0; i < 8; ++i) {
+          const int r = i * 4 + (lane >> 3);
+          line[i] = *reinterpret_cast<const uint4*>(stage + r * 128 + (((lane ^ r) & 7) << 4));
+        }
+#pragma unroll
+        for (int i = 0; i < 8; ++i)
+          if (i * 4 < live) *reinterpret_cast<uint4*>(to + (size_t)(i * 4 * pitch)) = line[i];
+        __syncwarp();
       }
       tc_fence_before();
       __syncwarp();
