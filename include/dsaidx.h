@@ -500,7 +500,7 @@ int dsa_cache_read_codes(const dsa_cache* c, const int32_t* block_table, int32_t
  * over positions follows from the lengths alone, and partials are joined in their order.
  * Supported: dim_qk 576, dim_v 512, heads 1 .. 128, max_pages * page_size <= 2^24, scale
  * positive, batch * n_q * heads below 2^31 and, in tiles of 128, rows times positions of
- * the whole batch below 2^30; q and out on 16-byte boundaries.
+ * the whole batch below 2^28; q and out on 16-byte boundaries.
  * workspace: dsa_paged_mla_workspace_size() bytes, 16-byte aligned (status word first). */
 typedef struct {
   int32_t batch;

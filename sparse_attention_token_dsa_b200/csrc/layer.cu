@@ -226,7 +226,7 @@ int plan_paged_mla(const dsa_paged_mla_problem* p, PagedMlaPlan* pl) {
   const int64_t row_tiles = (rows + kPmRows - 1) / kPmRows;
   pl->pairs = row_tiles * p->batch;
   const int64_t key_tiles = ((int64_t)p->max_pages * p->page_size + kPmKeys - 1) / kPmKeys;
-  if (rows * p->batch > 0x7fffffffll || pl->pairs * key_tiles > 0x3fffffffll)
+  if (rows * p->batch > 0x7fffffffll || pl->pairs * key_tiles >= 1 << 28)
     return DSA_ERR_UNSUPPORTED;
   pl->row_tiles = (int)row_tiles;
   const int64_t tiles = pl->pairs * key_tiles;

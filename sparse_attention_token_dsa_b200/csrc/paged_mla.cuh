@@ -24,6 +24,10 @@
 // shares, one for each cluster; a pair that more than one cluster meets leaves partial
 // (maximum, denominator, output) in the workspace, joined by a second kernel.  So long and
 // short sequences, few rows and many use the whole GPU, and the lengths stay on the device.
+// Going from one pair to the next drains the pipeline and costs about two tiles' time, so
+// in long shares a pair counts as two tiles more than it has (24 ragged sequences with a
+// few short ones among them: 124 -> 121 us; with no allowance the cluster that met the
+// short ones ended 30 % after the others).
 //
 // Softmax: fp32, one thread for a row's 64 of 128 positions; the running maximum is raised
 // lazily (by more than 2^8), P is rounded to bf16 for the second product (the matrix
@@ -70,6 +74,8 @@ struct PmRing {
 constexpr int kPmQBytes = 9 * 64 * 128;
 constexpr int kPmPBytes = 2 * 64 * 128;
 constexpr int kPmClusters = 74;         // one CTA an SM
+constexpr int kPmSwitch = 2;            // tiles' worth of time to go to another pair
+constexpr int kPmLongShare = 16;        // shares (in tiles) where that is reckoned
 constexpr float kPmLazy = 8.f;          // log2 headroom before the maximum is raised
 constexpr int kPmLoaders = 4;           // warps that convert e4m3 rows, for K and for V
 constexpr int kPmThreadsRaw = 32 * 10;  // softmax 4, S, PV, K, V, relays of K and V
@@ -91,8 +97,8 @@ struct PagedMlaArgs {
   float* lse;              // [batch][n_q][heads] or null
   int32_t* status;         // of the call (written by the join)
   int32_t* states;         // [clusters][2]: status of a cluster, and the wait that gave up
-  int32_t* plan;           // [0]: tiles of a share; [1 + pair]: the pair's first tile
-  float* part_o;           // [2 * clusters][128][512]
+  int32_t* plan;           // [0]: units of a share; [1 + pair]: place of the pair's first tile
+  float* part_o;           // [clusters][later part, first part of a pair][128][512]
   float2* part_ml;         // [2 * clusters][128] maximum (log2 units), denominator
 };
 
@@ -102,7 +108,7 @@ struct PagedMlaTail {
   uint64_t v_full[4], v_ready[4], v_empty[4];
   uint64_t s_full[2], s_empty[2];
   float peer[2][128];      // maxima (and at the end denominators) of a row's two threads
-  int32_t start_pair, start_off, count, share;
+  int32_t start_pair, start_off, count, share, extra;
   uint32_t tmem_base;
   int32_t abort;
 };
@@ -139,12 +145,17 @@ __device__ __forceinline__ PmPair pm_pair(const PagedMlaArgs& a, int p) {
   return r;
 }
 
+// A cluster's place in its share of the line.  A pair stands there as `extra` units and
+// then its tiles: the units are what it costs a cluster to go from one pair to the next.
 struct PmWalk {
-  int p, off, left, slot;
+  int p, off, left;        // pair, units of it done, units left
+  int at;                  // place on the line
+  int extra, slot;
 };
 struct PmSegment {
   PmPair pair;
   int p, t0, n, slot;
+  int first;               // place of the pair's first tile
   bool whole;
 };
 
@@ -161,15 +172,19 @@ __device__ __noinline__ bool pm_next_far(const PagedMlaArgs& a, PmWalk* walk, Pm
     w.p = s.pair.rows > 0 ? w.p + 1 : (s.pair.b + 1) * a.row_tiles;
   }
   if (w.p >= a.pairs) return false;
+  // (a share may end among a pair's extra units, with no tile of it)
+  const int cost = s.pair.tiles + w.extra, take = min(w.left, cost - w.off), to = w.off + take;
+  if (to <= w.extra) return false;
   s.p = w.p;
-  s.t0 = w.off;
-  s.n = min(w.left, s.pair.tiles - w.off);
+  s.first = w.at - w.off + w.extra;
+  s.t0 = max(w.off - w.extra, 0);
+  s.n = to - w.extra - s.t0;
   s.whole = s.n == s.pair.tiles;
-  s.slot = w.slot;
-  w.slot |= 1;
-  w.left -= s.n;
-  w.off += s.n;
-  if (w.off == s.pair.tiles) {
+  s.slot = w.slot + (s.t0 == 0 ? 1 : 0);             // of a part: a pair's first, or a later one
+  w.left -= take;
+  w.off = to;
+  w.at += take;
+  if (to == cost) {
     w.off = 0;
     ++w.p;
   }
@@ -393,17 +408,23 @@ __global__ void __cluster_dims__(2, 1, 1)
     // this cluster's share of the line of tiles
     const bool few = a.pairs <= 32;                  // a lane each: looked at once
     const int mine = lane < a.pairs ? pm_pair(a, lane).tiles : 0;
-    int total = few ? __reduce_add_sync(0xffffffffu, mine) : 0;
-    for (int p0 = 0; p0 < a.pairs && !few; p0 += 32) {
+    int total = 0, live = 0;                         // tiles, pairs that have some
+    for (int p0 = 0; p0 < a.pairs; p0 += 32) {
       const int p = p0 + lane;
-      total += __reduce_add_sync(0xffffffffu, p < a.pairs ? pm_pair(a, p).tiles : 0);
+      const int n = few ? mine : (p < a.pairs ? pm_pair(a, p).tiles : 0);
+      total += __reduce_add_sync(0xffffffffu, n);
+      live += __popc(__ballot_sync(0xffffffffu, n > 0));
     }
+    // (not in short shares, where it would only unbalance them)
+    const int extra = total / clusters >= kPmLongShare ? kPmSwitch : 0;
+    total += extra * live;
     const int share = max(1, (total + clusters - 1) / clusters);
     const int begin = (int)min((long long)cl * share, (long long)total);
     int before = 0, found = -1, off = 0;
     for (int p0 = 0; p0 < a.pairs && found < 0 && begin < total; p0 += 32) {
       const int p = p0 + lane;
-      const int n = few ? mine : (p < a.pairs ? pm_pair(a, p).tiles : 0);
+      int n = few ? mine : (p < a.pairs ? pm_pair(a, p).tiles : 0);
+      n += n > 0 ? extra : 0;
       int upto = n;
 #pragma unroll
       for (int d = 1; d < 32; d <<= 1) {
@@ -423,6 +444,7 @@ __global__ void __cluster_dims__(2, 1, 1)
       T->start_off = off;
       T->count = found < 0 ? 0 : min(share, total - begin);
       T->share = share;
+      T->extra = extra;
       if (cl == 0 && rank == 0) a.plan[0] = share;
     }
   }
@@ -432,7 +454,7 @@ __global__ void __cluster_dims__(2, 1, 1)
   tc_fence_after();
   const uint32_t tmem = T->tmem_base;
   volatile int* abort = &T->abort;
-  PmWalk walk{T->start_pair, T->start_off, T->count, 2 * cl};
+  PmWalk walk{T->start_pair, T->start_off, T->count, cl * T->share, T->extra, 2 * cl};
   PmSegment s;
 
   auto wait = [&](uint64_t* bar, uint32_t parity, int where) -> bool {
@@ -995,7 +1017,7 @@ __global__ void __cluster_dims__(2, 1, 1)
         else if (a.lse)
           a.lse[grow] = l_run == 0.f ? -inf : (m_run + log2f(l_run)) * 0.6931471805599453f;
         if (rank == 0 && row == 0 && s.t0 == 0)
-          a.plan[1 + s.p] = cl * T->share + (T->count - walk.left - s.n);
+          a.plan[1 + s.p] = s.first;
       }
       // O goes out through the warp's own part of P (32 rows x 128 bytes, free now), so that
       // a store covers whole lines of four rows: a store of each lane's own row, 32 lines
@@ -1097,8 +1119,6 @@ __global__ void __launch_bounds__(kPmJoinThreads) paged_mla_join_kernel(const Pa
   // a cluster whose wait ran out leaves its pair's place unwritten
   if (pr.tiles && (first < 0 || c0 >= c1 || c1 >= a.clusters)) return;
   const int n = c1 - c0 + 1;
-  // the pair's run in cluster c is that cluster's first unless it starts inside its share
-  const int head = first > c0 * share ? 1 : 0;
   for (int row = first_row; row < first_row + rows; ++row) {
     const int64_t grow = (int64_t)pr.b * a.n_q * a.heads + pr.row0 + row;
     uint2* out = reinterpret_cast<uint2*>(a.out + grow * kPmDv) + t;
@@ -1108,7 +1128,7 @@ __global__ void __launch_bounds__(kPmJoinThreads) paged_mla_join_kernel(const Pa
       continue;
     }
     float2 ml = make_float2(-inf, 0.f);
-    if (t < n) ml = a.part_ml[(int64_t)(2 * (c0 + t) + (t == 0 ? head : 0)) * kPmRows + row];
+    if (t < n) ml = a.part_ml[(int64_t)(2 * (c0 + t) + (t == 0)) * kPmRows + row];
     float m = ml.x;
 #pragma unroll
     for (int d = 16; d > 0; d >>= 1) m = fmaxf(m, __shfl_xor_sync(0xffffffffu, m, d));
@@ -1126,7 +1146,7 @@ __global__ void __launch_bounds__(kPmJoinThreads) paged_mla_join_kernel(const Pa
     float4 o = make_float4(0.f, 0.f, 0.f, 0.f);
 #pragma unroll 4
     for (int i = 0; i < n; ++i) {
-      const int slot = 2 * (c0 + i) + (i == 0 ? head : 0);
+      const int slot = 2 * (c0 + i) + (i == 0);
       const float4 v =
           *(reinterpret_cast<const float4*>(a.part_o + ((int64_t)slot * kPmRows + row) * kPmDv) + t);
       const float wi = w[i];
