@@ -479,8 +479,9 @@ int dsa_paged_mla(const dsa_paged_mla_problem* p, const dsa_cache* c, const void
   const int64_t rows = (int64_t)p->n_q * p->heads;
   // the join is launched while the attention kernel drains, and waits for its end itself
   cudaLaunchConfig_t join{};
-  a.join_rows = pl.pairs >= 256 ? 32 : (pl.pairs >= 64 ? 8 : 1);
   const int64_t most = rows < kPmRows ? rows : kPmRows;
+  const bool many = pl.pairs * most > kPmJoinBlocks;   // more rows than the GPU holds blocks
+  a.join_rows = pl.pairs >= 256 ? 32 : (pl.pairs >= 64 ? 8 : (many ? 4 : 1));
   join.gridDim = dim3((unsigned)pl.pairs, (unsigned)((most + a.join_rows - 1) / a.join_rows));
   join.blockDim = dim3(kPmJoinThreads);
   join.stream = st;
@@ -489,7 +490,7 @@ int dsa_paged_mla(const dsa_paged_mla_problem* p, const dsa_cache* c, const void
   early.val.programmaticStreamSerializationAllowed = 1;
   join.attrs = &early;
   join.numAttrs = 1;
-  if (cudaLaunchKernelEx(&join, paged_mla_join_kernel, a) != cudaSuccess) {
+  if (cudaLaunchKernelEx(&join, many ? paged_mla_join_kernel<4> : paged_mla_join_kernel<1>, a) != cudaSuccess) {
     cudaGetLastError();
     return DSA_ERR_CUDA;
   }

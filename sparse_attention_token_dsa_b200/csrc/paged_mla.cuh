@@ -81,6 +81,7 @@ constexpr int kPmLoaders = 4;           // warps that convert e4m3 rows, for K a
 constexpr int kPmThreadsRaw = 32 * 10;  // softmax 4, S, PV, K, V, relays of K and V
 constexpr int kPmThreadsCodes = 32 * (8 + 2 * kPmLoaders);   // 8 as above, converting K 4, V 4
 constexpr int kPmJoinThreads = 128;
+constexpr int kPmJoinBlocks = 148 * 8;  // of the join, resident at once
 
 struct PagedMlaArgs {
   CachePlanes c;
@@ -1088,13 +1089,16 @@ __global__ void __cluster_dims__(2, 1, 1)
 }
 
 // Rows whose positions more than one cluster read: o = sum_i w_i O_i / sum_i w_i l_i with
-// w_i = 2^(m_i - max m); rows that see nothing: o = 0, lse = -inf.  A block takes a few
-// rows of a pair, one where there are few pairs (most pairs of a large call were read by
-// one cluster, and their blocks only find that out).
+// w_i = 2^(m_i - max m); rows that see nothing: o = 0, lse = -inf.  A warp takes a quarter of
+// the values of ROWS rows at once and holds the weights of their parts, a lane a part, so
+// no warp waits for another; either form has eight loads of O in flight a lane, of four rows
+// or, where there are few rows, of eight parts of one.  A block takes several rows of a pair
+// where there are many pairs (most pairs of a large call were read by one cluster, and
+// their blocks only find that out).
+template <int ROWS>
 __global__ void __launch_bounds__(kPmJoinThreads) paged_mla_join_kernel(const PagedMlaArgs a) {
-  __shared__ float w[2 * kPmClusters];
-  __shared__ float red[2][kPmJoinThreads / 32];
-  const int p = blockIdx.x, t = threadIdx.x;
+  constexpr int kHeld = (kPmClusters + 31) / 32, kAhead = 8 / ROWS;
+  const int p = blockIdx.x, t = threadIdx.x, lane = t & 31;
   const PmPair pr = pm_pair(a, p);
   asm volatile("griddepcontrol.wait;" ::: "memory");   // all of the attention kernel is done
   if (p == 0 && blockIdx.y == 0 && t < 32) {         // status of the call: the first cluster's
@@ -1110,55 +1114,81 @@ __global__ void __launch_bounds__(kPmJoinThreads) paged_mla_join_kernel(const Pa
     }
   }
   const int first_row = blockIdx.y * a.join_rows;
-  const int rows = min(pr.rows - first_row, a.join_rows);
-  if (rows <= 0) return;
+  const int last_row = min(pr.rows, first_row + a.join_rows);
+  if (first_row >= last_row) return;
   const float inf = __int_as_float(0x7f800000);
   const int share = pr.tiles ? a.plan[0] : 1, first = pr.tiles ? a.plan[1 + p] : 0;
   const int c0 = first / share, c1 = (int)(((long long)first + pr.tiles - 1) / share);
   if (pr.tiles && c0 == c1) return;                  // written whole
   // a cluster whose wait ran out leaves its pair's place unwritten
   if (pr.tiles && (first < 0 || c0 >= c1 || c1 >= a.clusters)) return;
-  const int n = c1 - c0 + 1;
-  for (int row = first_row; row < first_row + rows; ++row) {
-    const int64_t grow = (int64_t)pr.b * a.n_q * a.heads + pr.row0 + row;
-    uint2* out = reinterpret_cast<uint2*>(a.out + grow * kPmDv) + t;
-    if (pr.tiles == 0) {
-      *out = make_uint2(0, 0);
-      if (t == 0 && a.lse) a.lse[grow] = -inf;
-      continue;
-    }
-    float2 ml = make_float2(-inf, 0.f);
-    if (t < n) ml = a.part_ml[(int64_t)(2 * (c0 + t) + (t == 0)) * kPmRows + row];
-    float m = ml.x;
+  const int n = pr.tiles ? c1 - c0 + 1 : 0;
+  for (int row0 = first_row; row0 < last_row; row0 += ROWS) {
+    float w[ROWS][kHeld], m[ROWS], l[ROWS];
 #pragma unroll
-    for (int d = 16; d > 0; d >>= 1) m = fmaxf(m, __shfl_xor_sync(0xffffffffu, m, d));
-    if ((t & 31) == 0) red[0][t >> 5] = m;
-    __syncthreads();
-    m = fmaxf(fmaxf(red[0][0], red[0][1]), fmaxf(red[0][2], red[0][3]));
-    const float wt = ml.x == -inf ? 0.f : ex2(ml.x - m);
-    float l = wt * ml.y;
-    if (t < n) w[t] = wt;
+    for (int r = 0; r < ROWS; ++r) {
+      const int row = min(row0 + r, last_row - 1);
+      float2 ml[kHeld];
 #pragma unroll
-    for (int d = 16; d > 0; d >>= 1) l += __shfl_xor_sync(0xffffffffu, l, d);
-    if ((t & 31) == 0) red[1][t >> 5] = l;
-    __syncthreads();
-    l = (red[1][0] + red[1][1]) + (red[1][2] + red[1][3]);
-    float4 o = make_float4(0.f, 0.f, 0.f, 0.f);
-#pragma unroll 4
-    for (int i = 0; i < n; ++i) {
-      const int slot = 2 * (c0 + i) + (i == 0);
-      const float4 v =
-          *(reinterpret_cast<const float4*>(a.part_o + ((int64_t)slot * kPmRows + row) * kPmDv) + t);
-      const float wi = w[i];
-      o.x = fmaf(wi, v.x, o.x);
-      o.y = fmaf(wi, v.y, o.y);
-      o.z = fmaf(wi, v.z, o.z);
-      o.w = fmaf(wi, v.w, o.w);
+      for (int h = 0; h < kHeld; ++h) {
+        const int i = h * 32 + lane;
+        ml[h] = make_float2(-inf, 0.f);
+        if (i < n) ml[h] = a.part_ml[(int64_t)(2 * (c0 + i) + (i == 0)) * kPmRows + row];
+      }
+      m[r] = -inf;
+#pragma unroll
+      for (int h = 0; h < kHeld; ++h) m[r] = fmaxf(m[r], ml[h].x);
+#pragma unroll
+      for (int d = 16; d > 0; d >>= 1) m[r] = fmaxf(m[r], __shfl_xor_sync(0xffffffffu, m[r], d));
+      l[r] = 0.f;
+#pragma unroll
+      for (int h = 0; h < kHeld; ++h) {
+        w[r][h] = ml[h].x == -inf ? 0.f : ex2(ml[h].x - m[r]);
+        l[r] = fmaf(w[r][h], ml[h].y, l[r]);
+      }
+#pragma unroll
+      for (int d = 16; d > 0; d >>= 1) l[r] += __shfl_xor_sync(0xffffffffu, l[r], d);
     }
-    const float inv = l == 0.f ? 0.f : 1.f / l;
-    *out = make_uint2(bf16x2(o.x * inv, o.y * inv), bf16x2(o.z * inv, o.w * inv));
-    if (t == 0 && a.lse) a.lse[grow] = l == 0.f ? -inf : (m + log2f(l)) * 0.6931471805599453f;
-    __syncthreads();                                 // the next row writes the same places
+    float4 o[ROWS];
+#pragma unroll
+    for (int r = 0; r < ROWS; ++r) o[r] = make_float4(0.f, 0.f, 0.f, 0.f);
+    const float4* part = reinterpret_cast<const float4*>(a.part_o) + t;   // 4 values a thread
+#pragma unroll
+    for (int h = 0; h < kHeld; ++h) {
+#pragma unroll 1
+      for (int i = 32 * h; i < min(n, 32 * h + 32); i += kAhead) {
+        float4 v[kAhead][ROWS];
+#pragma unroll
+        for (int k = 0; k < kAhead; ++k)
+#pragma unroll
+          for (int r = 0; r < ROWS; ++r) {
+            const int c = min(i + k, n - 1), row = min(row0 + r, last_row - 1);
+            const int64_t at = (int64_t)(2 * (c0 + c) + (c == 0)) * kPmRows + row;
+            v[k][r] = part[at * (kPmDv / 4)];
+          }
+#pragma unroll
+        for (int k = 0; k < kAhead; ++k)
+#pragma unroll
+          for (int r = 0; r < ROWS; ++r) {
+            const float held = __shfl_sync(0xffffffffu, w[r][h], (i + k) & 31);
+            const float wi = i + k < n ? held : 0.f;
+            o[r].x = fmaf(wi, v[k][r].x, o[r].x);
+            o[r].y = fmaf(wi, v[k][r].y, o[r].y);
+            o[r].z = fmaf(wi, v[k][r].z, o[r].z);
+            o[r].w = fmaf(wi, v[k][r].w, o[r].w);
+          }
+      }
+    }
+#pragma unroll
+    for (int r = 0; r < ROWS; ++r) {
+      if (row0 + r >= last_row) break;
+      const int64_t grow = (int64_t)pr.b * a.n_q * a.heads + pr.row0 + row0 + r;
+      const float inv = l[r] == 0.f ? 0.f : 1.f / l[r];
+      *(reinterpret_cast<uint2*>(a.out + grow * kPmDv) + t) =
+          make_uint2(bf16x2(o[r].x * inv, o[r].y * inv), bf16x2(o[r].z * inv, o[r].w * inv));
+      if (t == 0 && a.lse)
+        a.lse[grow] = l[r] == 0.f ? -inf : (m[r] + log2f(l[r])) * 0.6931471805599453f;
+    }
   }
 }
 
