@@ -37,14 +37,14 @@
 //
 // Measured (B200, warm and back to back; a copy runs at 6545 GB/s there, the library's
 // large bf16 product at 1658 TFLOP/s in a burst and at 1394 for seconds):
-//   one token of 128 heads over 32 x 131072 positions   1.34 ms, 3.6 TB/s and 870 TFLOP/s
-//     at once: the chip is at its 1000 W and lowers the SM clock to 1.30 of 1.97 GHz.
+//   one token of 128 heads over 32 x 131072 positions   1.31 ms, 3.7 TB/s and 890 TFLOP/s
+//     at once: the chip is at its 1000 W and lowers the SM clock to 1.3 of 1.97 GHz.
 //     Alone the bytes would take 0.74 ms, the products 0.84 at the sustained rate.
-//   512 tokens of 128 heads behind 8192 positions   1.05 ms, 1158 TFLOP/s (0.83 of the
-//     sustained rate) at 988 W and 1.53 GHz.
-//   4 tokens of 64 heads over 24 x up to 16001 e4m3 positions   0.15 ms, 380 TFLOP/s: a
-//     tile takes 6200 clocks against 3500 of the prompt's, as its rows are converted in
-//     shared memory: written and read as codes, written and read as bf16.
+//   512 tokens of 128 heads behind 8192 positions   1.01 ms, 1190 TFLOP/s (0.86 of the
+//     sustained rate), at the power limit too.
+//   4 tokens of 64 heads over 24 sequences of 16384 e4m3 positions   0.295 ms, 740 TFLOP/s
+//     (bf16 rows 0.28): a tile takes 5000 clocks, as its rows are written and read as codes,
+//     written and read as bf16 in shared memory; up to 16001 and 4 tokens   0.12 ms.
 //   one token of 16 heads over 1000 positions   16 us: two launches, a plan and a join.
 #pragma once
 #include "cache.cuh"
@@ -493,7 +493,7 @@ __global__ void __cluster_dims__(2, 1, 1)
           ok = ok && wait(&T->q_ready, qc & 1, 53);
           for (int i = 0; i < s.n && ok; ++i, ++sc) {
             const int b = sc & 1;
-            bool seen = mbar_try_wait(&T->k_ready[slot], parity);
+            bool seen = mbar_seen(&T->k_ready[slot], parity);
             ok = wait(&T->s_empty[b], ((sc >> 1) & 1) ^ 1, 51);
             if (!ok) break;
             tc_fence_after();
@@ -507,7 +507,7 @@ __global__ void __cluster_dims__(2, 1, 1)
                 slot = 0;
                 parity ^= 1;
               }
-              seen = mbar_try_wait(&T->k_ready[slot], parity);
+              seen = mbar_seen(&T->k_ready[slot], parity);
 #pragma unroll
               for (int c = 0; c < Ring::kChunks; ++c)
 #pragma unroll
@@ -547,7 +547,7 @@ __global__ void __cluster_dims__(2, 1, 1)
         for (int i = 0; i < s.n && ok; ++i, ++pc) {
           ok = wait(&T->p_full, pc & 1, 55);
           if (!ok) break;
-          bool seen = mbar_try_wait(&T->v_ready[slot], parity);
+          bool seen = mbar_seen(&T->v_ready[slot], parity);
           tc_fence_after();
 #pragma unroll 1
           for (int v = 0; v < 4; ++v) {
@@ -558,7 +558,7 @@ __global__ void __cluster_dims__(2, 1, 1)
               slot = 0;
               parity ^= 1;
             }
-            seen = mbar_try_wait(&T->v_ready[slot], parity);
+            seen = mbar_seen(&T->v_ready[slot], parity);
 #pragma unroll
             for (int kk = 0; kk < 2; ++kk) {         // 16 positions
               const int k16 = v * 2 + kk;
@@ -902,7 +902,7 @@ __global__ void __cluster_dims__(2, 1, 1)
     // mate there (with nothing else to wait for), so neither is left behind.
     // This is the longest chain of a tile, and it is short code on purpose: the roles of a
     // CTA share its instruction cache, and unrolled masks and rescales made every role
-    // wait for instructions (42 % of all stalls, and 1.63 ms where it is now 1.34).
+    // wait for instructions (42 % of all stalls, and the 128K batch above took 1.63 ms).
     const int t = threadIdx.x, half = t >> 6, row = t & 63;
     const uint32_t lane_off = (uint32_t)(warp * 32) << 16;
     const float inf = __int_as_float(0x7f800000);

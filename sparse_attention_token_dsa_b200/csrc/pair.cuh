@@ -32,6 +32,20 @@ __device__ __forceinline__ void mbar_arrive_cluster(uint32_t bar) {
                : "memory");
 }
 
+// Whether a phase is complete, without waiting for it (mbar_try_wait may suspend its thread
+// for up to 20 us, too long for a look ahead that nobody has to wait for).
+__device__ __forceinline__ bool mbar_seen(uint64_t* bar, uint32_t parity) {
+  uint32_t ok;
+  asm volatile(
+      "{\n\t.reg .pred p;\n\t"
+      "mbarrier.test_wait.parity.shared::cta.b64 p, [%1], %2;\n\t"
+      "selp.u32 %0, 1, 0, p;\n\t}"
+      : "=r"(ok)
+      : "r"(smem_u32(bar)), "r"(parity)
+      : "memory");
+  return ok != 0;
+}
+
 // As mbar_wait, with the polling out of line: a kernel with a role for every warp has
 // dozens of waits, and inlined polls pushed its loops out of the instruction cache.
 __device__ __noinline__ bool mbar_poll(uint64_t* bar, uint32_t parity, volatile int* abort,

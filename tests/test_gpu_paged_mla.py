@@ -185,6 +185,17 @@ def test_long_sequence_beside_short_ones(B, heads, form):
     p.check(*p.run(B))
 
 
+@pytest.mark.parametrize("form,heads,n_q", [("bf16", 16, 1), ("e4m3", 16, 1), ("e4m3", 64, 3)])
+def test_many_short_sequences_between_long_ones(B, form, heads, n_q):
+    """Shares long enough for a pair's extra units, ends of shares among those of the short
+    ones, pairs that begin and end with a share."""
+    short = [0, 1, 127, 128, 129, 300, 64, 2] * 8
+    k_lens = [90001] + short + [128 * 20] * 6 + [70000] + short[:11] + [17]
+    q_lens = None if n_q == 1 else [1 + i % n_q for i in range(len(k_lens))]
+    p = Problem(B, 23, k_lens, q_lens, n_q, heads, 64, form)
+    p.check(*p.run(B))
+
+
 def test_long_prompt_chunk_sampled(B):
     p = Problem(B, 9, [9000], None, 400, 128, 64, "bf16")
     out, lse = p.run(B)
