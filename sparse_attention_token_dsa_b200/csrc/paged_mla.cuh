@@ -26,8 +26,7 @@
 // short sequences, few rows and many use the whole GPU, and the lengths stay on the device.
 // Going from one pair to the next drains the pipeline and costs about two tiles' time, so
 // in long shares a pair counts as two tiles more than it has (24 ragged sequences with a
-// few short ones among them: 124 -> 121 us; with no allowance the cluster that met the
-// short ones ended 30 % after the others).
+// few short ones among them: 124 -> 121 us).
 //
 // Softmax: fp32, one thread for a row's 64 of 128 positions; the running maximum is raised
 // lazily (by more than 2^8), P is rounded to bf16 for the second product (the matrix
@@ -37,14 +36,15 @@
 //
 // Measured (B200, warm and back to back; a copy runs at 6545 GB/s there, the library's
 // large bf16 product at 1658 TFLOP/s in a burst and at 1394 for seconds):
-//   one token of 128 heads over 32 x 131072 positions   1.31 ms, 3.7 TB/s and 890 TFLOP/s
-//     at once: the chip is at its 1000 W and lowers the SM clock to 1.3 of 1.97 GHz.
-//     Alone the bytes would take 0.74 ms, the products 0.84 at the sustained rate.
-//   512 tokens of 128 heads behind 8192 positions   1.01 ms, 1190 TFLOP/s (0.86 of the
+//   one token of 128 heads over 32 x 131072 positions   1.2 to 1.3 ms, 3.6 to 4.0 TB/s and
+//     870 to 960 TFLOP/s at once: the chip is at its 1000 W and lowers the SM clock to 1.3
+//     of 1.97 GHz.  Alone the bytes would take 0.74 ms, the products 0.84 at the sustained
+//     rate.
+//   512 tokens of 128 heads behind 8192 positions   1.00 ms, 1200 TFLOP/s (0.86 of the
 //     sustained rate), at the power limit too.
-//   4 tokens of 64 heads over 24 sequences of 16384 e4m3 positions   0.295 ms, 740 TFLOP/s
-//     (bf16 rows 0.28): a tile takes 5000 clocks, as its rows are written and read as codes,
-//     written and read as bf16 in shared memory; up to 16001 and 4 tokens   0.12 ms.
+//   4 tokens of 64 heads over 24 sequences of 16384 e4m3 positions   0.285 ms, 770 TFLOP/s
+//     (bf16 rows 0.25), at the power limit: a tile's rows are written and read as codes,
+//     written and read as bf16 in shared memory.  Up to 4 tokens and 16001   0.11 ms.
 //   one token of 16 heads over 1000 positions   16 us: two launches, a plan and a join.
 #pragma once
 #include "cache.cuh"
@@ -1021,8 +1021,8 @@ __global__ void __cluster_dims__(2, 1, 1)
           a.plan[1 + s.p] = s.first;
       }
       // O goes out through the warp's own part of P (32 rows x 128 bytes, free now), so that
-      // a store covers whole lines of four rows: a store of each lane's own row, 32 lines
-      // an instruction, took 16 us a tile of rows.
+      // a store covers whole lines of four rows (stores of each lane's own row, 32 lines an
+      // instruction, took 12000 clocks a tile of rows where this takes 8000).
       const float inv = l_run == 0.f ? 0.f : 1.f / l_run;
       uint8_t* stage = Ps + warp * 4096;
       const int first = rank * 64 + (warp & 1) * 32; // row of the tile of lane 0
