@@ -26,7 +26,7 @@
 // short sequences, few rows and many use the whole GPU, and the lengths stay on the device.
 // Going from one pair to the next drains the pipeline and costs about two tiles' time, so
 // in long shares a pair counts as two tiles more than it has (24 ragged sequences with a
-// few short ones among them: 124 -> 121 us).
+// few short ones among them: 119 -> 115 us; three or four tiles do as well).
 //
 // Softmax: fp32, one thread for a row's 64 of 128 positions; the running maximum is raised
 // lazily (by more than 2^8), P is rounded to bf16 for the second product (the matrix
