@@ -364,10 +364,10 @@ int dsa_index_host(const dsa_problem* p, const void* q_host, const float* q_scal
                    int32_t* idx_host, float* score_host, int32_t chunk_rows, void* staging,
                    size_t staging_bytes, void* stream);
 
-/* Operand preparation for the FP8 path: per-row scale a = amax/448 (amax == 0
- * gives a = 1), code = round-to-nearest-even, saturating e4m3 of x/a, both
- * divisions in IEEE fp32 ("PaperTrace 2.2.2", section 2.3 "from formula to
- * FP8 cache": k^ = round(k/a), FP8 data plus a scale).
+/* Operand preparation for the FP8 path: per-row scale a = amax/448 (1 where that
+ * quotient is 0 in fp32: amax == 0 or below 2^-141), code = round-to-nearest-even,
+ * saturating e4m3 of x/a, both divisions in IEEE fp32 ("PaperTrace 2.2.2", section
+ * 2.3 "from formula to FP8 cache": k^ = round(k/a), FP8 data plus a scale).
  *   x [rows, cols] (x_dtype F32 or BF16), out [rows, cols] uint8, out_scale [rows]. */
 int dsa_quantize_e4m3(const void* x, int32_t x_dtype, int64_t rows, int32_t cols,
                       uint8_t* out, float* out_scale, void* stream);
@@ -449,8 +449,8 @@ typedef struct {
 /* Write n_tokens rows into the cache: row t of x (dim_q + dim_raw values of x_dtype
  * DSA_BF16 or DSA_F32, x_stride elements apart) goes to slots[t] = page * page_size + row
  * (device int64; a slot outside the cache, such as -1, skips the token).  No two tokens
- * may have the same slot; n_tokens below 2^31.  Scales: amax / 448 over the group, as dsa_quantize_e4m3 (an
- * all-zero group has scale 1), or with DSA_FLAG_POW2_SCALE the least power of two that is
+ * may have the same slot; n_tokens below 2^31.  Scales: amax / 448 over the group, as
+ * dsa_quantize_e4m3 (1 where that quotient is 0), or with DSA_FLAG_POW2_SCALE the least power of two that is
  * at least that, which makes scale * code exact in bf16 (for dsa_paged_mla).
  * rope (optional, else NULL with pos and freq NULL): rotates the rot_dim values at
  * rope->offset of the row before they are stored, from x in fp32 with no rounding

@@ -173,8 +173,8 @@ uint8_t orc_e4m3_encode(float x) {
   return sign | (uint8_t)(((E + 7) << 3) | mm);
 }
 
-/* Operand preparation: per-row scale a = amax / 448 in fp32 (amax == 0 gives
- * a = 1), code = e4m3(x / a) with the division in fp32.  [FP8] */
+/* Operand preparation: per-row scale a = amax / 448 in fp32 (1 where that is 0:
+ * amax == 0, or so small that the quotient rounds to 0), code = e4m3(x / a) with the division in fp32.  [FP8] */
 int orc_quantize_rows(const void* x, int32_t x_dtype, int64_t rows, int32_t cols, uint8_t* out,
                       float* out_scale) {
   if (x_dtype != ORC_F32 && x_dtype != ORC_BF16) return ORC_ERR;
@@ -192,7 +192,8 @@ int orc_quantize_rows(const void* x, int32_t x_dtype, int64_t rows, int32_t cols
       float av = fabsf(v);
       if (av > amax) amax = av;
     }
-    volatile float a = (amax > 0.0f) ? amax / (MUT(14) ? 240.0f : 448.0f) : 1.0f;
+    volatile float a = amax / (MUT(14) ? 240.0f : 448.0f);
+    if (!(a > 0.0f)) a = 1.0f;
     out_scale[r] = a;
     for (int32_t c = 0; c < cols; ++c) {
       float v;
@@ -213,7 +214,7 @@ int orc_quantize_rows(const void* x, int32_t x_dtype, int64_t rows, int32_t cols
  * the query is converted to the e4m3 compute type in two parts ([FP8]: the
  * query is converted to the compute type in registers, the dot products
  * accumulate in higher precision).  Reading: per (row, head) vector x of dim
- * values, s = amax|x| / 448 in fp32 (amax == 0 gives s = 1), v = x / s in fp32,
+ * values, s = amax|x| / 448 in fp32 (1 where that is 0), v = x / s in fp32,
  * hi = e4m3(v), lo = e4m3(v - hi) with the subtraction in fp32; the operand
  * value is s * (hi + lo), written here exactly in fp64.
  *   x [vecs, dim] (F32 or BF16), out [vecs, dim] fp64. */
@@ -232,7 +233,8 @@ int orc_split_query(const void* x, int32_t x_dtype, int64_t vecs, int32_t dim, d
       }
       if (fabsf(v) > amax) amax = fabsf(v);
     }
-    volatile float sc = (amax > 0.0f) ? amax / 448.0f : 1.0f;
+    volatile float sc = amax / 448.0f;
+    if (!(sc > 0.0f)) sc = 1.0f;
     for (int32_t c = 0; c < dim; ++c) {
       float v;
       if (x_dtype == ORC_F32) {

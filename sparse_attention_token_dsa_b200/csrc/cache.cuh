@@ -330,13 +330,12 @@ __device__ __forceinline__ uint2 codes8(const float (&v)[8], F f) {
 // Scale of a group and its codes: two runs of 8 values a lane.
 __device__ __forceinline__ float quantise(const float (&v)[2][8], float amax, bool pow2,
                                           uint2 (&code)[2]) {
-  float s = 1.f;
   if (pow2) {
     // amax = m 2^e with m in [1/2, 1), 448 = 0.875 2^9
     int e;
     const float m = frexpf(amax, &e);
     e = amax > 3.0e38f ? 120 : max(m > 0.875f ? e - 8 : e - 9, -126);
-    float inv = 1.f;
+    float s = 1.f, inv = 1.f;
     if (amax > 0.f) {
       s = __int_as_float((e + 127) << 23);
       inv = __int_as_float((127 - e) << 23);         // 2^-e
@@ -345,7 +344,7 @@ __device__ __forceinline__ float quantise(const float (&v)[2][8], float amax, bo
     for (int h = 0; h < 2; ++h) code[h] = codes8(v[h], [&](float x) { return x * inv; });
     return s;
   }
-  if (amax > 0.f) s = __fdiv_rn(amax, 448.f);
+  const float s = e4m3_scale(amax);
   if (s > 0x1p-90f && s < 0x1p90f) {
     // The IEEE quotient by Markstein's method: from the correctly rounded reciprocal y,
     // q = x y, its exact remainder r = x - q s, and q + r y rounds to x / s.  (Where x is so

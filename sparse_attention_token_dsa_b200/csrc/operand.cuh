@@ -44,6 +44,14 @@ __device__ __forceinline__ uint8_t e4m3_rn_sat(float v) {
   return (uint8_t)__nv_cvt_float_to_fp8(v, __NV_SATFINITE, __NV_E4M3);
 }
 
+// Scale of a group of e4m3 codes from its largest magnitude: amax / 448, or 1 where that is 0:
+// a group of zeros, or of values so small (amax < 2^-141) that the quotient rounds to 0, which
+// as a scale would turn the group's zeros into NaN.
+__device__ __forceinline__ float e4m3_scale(float amax) {
+  const float a = __fdiv_rn(amax, 448.f);
+  return a > 0.f ? a : 1.f;
+}
+
 __device__ __forceinline__ float e4m3_value(uint8_t c) {
   __half_raw h = __nv_cvt_fp8_to_halfraw((__nv_fp8_storage_t)c, __NV_E4M3);
   return __half2float(__half(h));

@@ -23,7 +23,7 @@ __global__ void quantize_rows_kernel(const void* __restrict__ x, int dtype, int6
   for (int c = lane; c < cols; c += 32) amax = fmaxf(amax, fabsf(load_as_f32(x, dtype, base + c)));
 #pragma unroll
   for (int off = 16; off > 0; off >>= 1) amax = fmaxf(amax, __shfl_xor_sync(0xffffffffu, amax, off));
-  const float a = amax > 0.f ? __fdiv_rn(amax, 448.0f) : 1.0f;
+  const float a = e4m3_scale(amax);
   if (lane == 0) out_scale[row] = a;
   for (int c = lane; c < cols; c += 32) out[base + c] = e4m3_rn_sat(__fdiv_rn(load_as_f32(x, dtype, base + c), a));
 }
@@ -49,7 +49,7 @@ __global__ void split_query_kernel(const void* __restrict__ q, int dtype, int64_
   for (int c = lane; c < d; c += 32) amax = fmaxf(amax, fabsf(load_as_f32(q, dtype, src + c)));
 #pragma unroll
   for (int off = 16; off > 0; off >>= 1) amax = fmaxf(amax, __shfl_xor_sync(0xffffffffu, amax, off));
-  const float s = amax > 0.f ? __fdiv_rn(amax, 448.0f) : 1.0f;
+  const float s = e4m3_scale(amax);
   if (lane == 0) head_scale[rh] = s;
   uint8_t* hi = parts + rh * (int64_t)d;
   uint8_t* lo = parts + (rows * H + rh) * (int64_t)d;

@@ -162,6 +162,24 @@ def test_quantizer_matches_oracle_bit_exact(B):
         assert np.array_equal(codes.cpu().numpy(), rc)
 
 
+def test_split_query_of_magnitudes_without_a_scale(B):
+    """A query head so small that amax / 448 rounds to 0: its scale is 1 and its values are
+    zeros, so the scores are those of a zero head (a scale of 0 made them NaN)."""
+    import torch
+    g = torch.Generator(device="cuda").manual_seed(31)
+    q = torch.randn(1, 4, 32, 128, device="cuda", generator=g)
+    w = torch.randn(1, 4, 32, device="cuda", generator=g)
+    kc, ks = B.dsa_quantize_e4m3(torch.randn(1, 300, 128, device="cuda", generator=g))
+    kc = kc.view(torch.float8_e4m3fn)
+    q[:, 1, 3] = q[:, 2, 5] = 0.0
+    flags = B.DSA_FLAG_CHECK | B.DSA_FLAG_SORTED
+    want = B.dsa_index(q, kc, w, 32, k_scale=ks, flags=flags)
+    q[:, 1, 3, 7], q[:, 2, 5, 9] = 2.0 ** -149, -2.0 ** -142
+    got = B.dsa_index(q, kc, w, 32, k_scale=ks, flags=flags)
+    assert torch.isfinite(want[1][0, 3]).all()
+    assert torch.equal(got[0], want[0]) and torch.equal(got[1], want[1])
+
+
 def _fp8_problem(p, B):
     """GPU-quantised operands (checked bit-exact against the oracle's quantiser)."""
     qd, kd = dev(p.q), dev(p.k)

@@ -280,6 +280,30 @@ def test_write_of_values_at_the_ends(B, pow2):
     assert bool((y[4] == 1.0).all()) and bool(torch.isfinite(y[5]).all())
 
 
+@pytest.mark.parametrize("pow2", [False, True])
+def test_write_of_groups_whose_scale_would_be_zero(B, pow2):
+    """amax / 448 rounds to 0 below 2^-141: the scale is then 1, so zeros stay zeros; the
+    quantiser holds the same."""
+    x = torch.zeros(4, 128)
+    for r, power in enumerate((-149, -142, -141, -140)):
+        x[r, 3], x[r, 7] = 2.0 ** power, -2.0 ** power
+    cache = B.PagedCache.empty(1, 16, 128, 0)
+    B.cache_write(cache, x.cuda(), torch.arange(4, device="cuda"), pow2=pow2)
+    y = B.cache_read(cache, torch.zeros(1, 1, dtype=torch.int32, device="cuda"), 4,
+                     dtype=torch.float32)[0].cpu()
+    scale = cache.scale[0, :4, 0].cpu()
+    assert bool((scale > 0).all())
+    if pow2:                            # 2^-126 is the least: all of these are under its 2^-10
+        assert bool((scale == 2.0 ** -126).all()) and bool((y == 0).all())
+        return
+    assert scale.tolist() == [1.0, 1.0, 2.0 ** -149, 2.0 ** -149]
+    assert bool((y[:2] == 0).all()) and torch.equal(y[2], x[2])
+    assert bool((y[3, [0, 1, 2, 4, 5, 6]] == 0).all()) and bool(torch.isfinite(y[3]).all())
+    codes, sc = B.dsa_quantize_e4m3(x.cuda())
+    assert torch.equal(codes.cpu(), cache.codes.view(torch.uint8)[0, :4].cpu())
+    assert torch.equal(sc.cpu(), scale)
+
+
 @pytest.mark.parametrize("form,offset,rot", [("latent", 512, 64), ("bf16", 512, 64), ("index", 0, 64),
                                              ("latent", 448, 128), ("wide", 248, 32)])
 @pytest.mark.parametrize("interleaved", [False, True])

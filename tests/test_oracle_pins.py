@@ -405,6 +405,22 @@ def test_quantize_scale_definition(oracle_mod):
     assert np.all(codes[1] == 0)
 
 
+@pytest.mark.parametrize("power", [-149, -142, -141])
+def test_quantize_scale_that_rounds_to_zero(oracle_mod, power):
+    """amax / 448 rounds to 0 in fp32 below 2^-141 (448 = 2^8.8, fp32 ends at 2^-149, half
+    of that rounds to 0): the scale is then 1, not 0, whose quotients are NaN at zeros."""
+    x = np.zeros((1, 128), np.float32)
+    x[0, 3], x[0, 7] = np.ldexp(np.float32(1), power), -np.ldexp(np.float32(1), power)
+    codes, sc = oracle_mod.quantize_rows(x, F32)
+    if power < -141:
+        assert sc[0] == 1.0 and np.all((codes & 0x7F) == 0)
+        assert np.all(oracle_mod.split_query(x, F32) == 0.0)
+    else:
+        assert sc[0] == np.float32(2.0 ** -149) and codes[0, 3] == 0x78 and codes[0, 7] == 0xF8
+        assert np.all(codes[0, [0, 1, 2, 4, 5, 6]] == 0)
+        assert np.array_equal(oracle_mod.split_query(x, F32), x.astype(np.float64))
+
+
 def test_fp8_margin_bound_keeps_set(oracle_mod):
     """2E < m  =>  the top-k set is unchanged by key quantisation, with
     E = eps * sum_j |w_j| ||q_j||, eps = max_s ||k_s - k^_s||, m = I(k) - I(k+1).
