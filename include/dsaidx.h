@@ -491,10 +491,11 @@ int dsa_cache_read_codes(const dsa_cache* c, const int32_t* block_table, int32_t
  *   out [batch, n_q, heads, 512] bf16; out_lse [batch, n_q, heads] fp32 or NULL; tokens at
  *     or behind q_len[b] are padding: their rows of both are left as they were
  * A token that sees no position (k_len 0, or k_len < q_len for the first ones) gets out 0
- * and lse -inf.  Rows of the cache behind k_len may hold anything; a non-finite value
- * before it makes the outputs of its sequence's tokens unspecified, also of those it is
- * not visible to.  A block table entry outside [0, n_pages) that covers k_len is recorded
- * as DSA_ERR_INVALID in the status word and read as zeros.
+ * and lse -inf.  Rows of the cache behind k_len may hold anything; a NaN before it (a code
+ * 0x7f or 0xff among them) makes all outputs of the tokens that see it NaN, and a non-finite
+ * value leaves those of its sequence's other tokens unspecified.  A block table entry
+ * outside [0, n_pages) that covers k_len is recorded as DSA_ERR_INVALID in the status word
+ * and read as zeros.
  * The softmax weights enter the value product in bf16 (fp32 accumulation); logits, maxima,
  * denominators and partial outputs are fp32.  Results do not depend on the run: the split
  * over positions follows from the lengths alone, and partials are joined in their order.

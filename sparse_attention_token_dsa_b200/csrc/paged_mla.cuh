@@ -299,14 +299,28 @@ __device__ __noinline__ void four_units_any(const uint4* codes, uint8_t* const* 
         bf16x2(v[8], v[9]), bf16x2(v[10], v[11]), bf16x2(v[12], v[13]), bf16x2(v[14], v[15]));
   }
 }
+// Whether one of 8 codes is a NaN (0x7f, 0xff): its lower seven bits carry into the eighth.
+__device__ __forceinline__ uint32_t nan_codes(uint32_t a, uint32_t b, uint32_t so_far) {
+  return so_far | ((a & 0x7f7f7f7fu) + 0x01010101u) | ((b & 0x7f7f7f7fu) + 0x01010101u);
+}
 // Four units of 16 codes in shared memory a lane, from(u) to to(u, 0) and to(u, 1).  The
 // warp has read all of them before it writes the first, as values may take codes' places.
-template <typename From, typename To>
+// NANS: a lane that holds a NaN code takes the way of any scale, as the short one would make
+// 480 times the scale of it (the look costs the e4m3 batch 2 %).  K is looked at and V is not: a
+// NaN logit makes all outputs of the tokens that see its position NaN, and those of the others
+// need V finite.
+template <bool NANS, typename From, typename To>
 __device__ __forceinline__ void four_units(bool exact, uint32_t f, float scale, From from, To to) {
   uint4 w[4];
 #pragma unroll
   for (int u = 0; u < 4; ++u) w[u] = *reinterpret_cast<const uint4*>(from(u));
   __syncwarp();
+  if (NANS) {
+    uint32_t nan = 0;
+#pragma unroll
+    for (int u = 0; u < 4; ++u) nan = nan_codes(w[u].z, w[u].w, nan_codes(w[u].x, w[u].y, nan));
+    exact = exact && (nan & 0x80808080u) == 0;
+  }
   if (exact) {
 #pragma unroll
     for (int u = 0; u < 4; ++u) {
@@ -831,7 +845,7 @@ __global__ void __cluster_dims__(2, 1, 1)
               for (int h = 0; h < 2; ++h) {          // row h * 32 + lane
                 uint8_t* to = Ks + slot * kPmChunk + (h * 32 + lane) * 128;
                 const uint8_t* from = Ks + slot * kPmChunk + kPmChunk / 2 + (h * 32 + lane) * 64;
-                four_units(
+                four_units<true>(
                     exact, h ? f1 : f0, h ? s1 : s0,
                     [&](int u) { return from + ((u ^ (lane >> 1 & 3)) << 4); },
                     [&](int u, int e) { return to + (((2 * u + e) ^ (lane & 7)) << 4); });
@@ -884,7 +898,7 @@ __global__ void __cluster_dims__(2, 1, 1)
               for (int h = 0; h < 2; ++h) {          // block of 64 values
                 const uint8_t* from = Vs + v * kPmSlice + b * 8192 + 4096 + lane * 128;
                 uint8_t* to = Vs + v * kPmSlice + b * 8192 + h * 4096 + lane * 128;
-                four_units(
+                four_units<false>(
                     exact, f, sc, [&](int u) { return from + (((4 * h + u) ^ (lane & 7)) << 4); },
                     [&](int u, int e) { return to + (((2 * u + e) ^ (lane & 7)) << 4); });
               }

@@ -234,6 +234,44 @@ def test_every_code_and_scale_exactly(B, power):
     assert torch.equal(out[0, 0].float(), want.expand(16, 512)) and bool((lse == 0).all())
 
 
+@pytest.mark.parametrize("form", ["bf16", "e4m3", "anyscale"])
+@pytest.mark.parametrize("column", [0, 191, 511, 575])
+def test_a_nan_stays_one(B, form, column):
+    """A NaN in a cached row makes the outputs of the tokens that see it NaN, whatever the
+    row's form (e4m3: the codes 0x7f and 0xff), and no other sequence's.  With codes and
+    powers of two the tokens before it are right as well: only its logits are NaN."""
+    p = Problem(B, 19, [700, 700, 140], None, 3, 16, 64, form)
+    want = p.run(B)
+    for at, code in ((5, 0x7f), (130, 0xff), (698, 0x7f)):
+        page, row = p.table[1, at // 64].long(), at % 64
+        bits = form != "bf16" and column < 512
+        plane = p.cache.codes.view(torch.uint8) if bits else p.cache.raw
+        at_column = column if bits or form == "bf16" else column - 512
+        keep = plane[page, row, at_column].clone()
+        plane[page, row, at_column] = code if bits else float("nan")
+        out, lse = p.run(B)
+        plane[page, row, at_column] = keep
+        for b in (0, 2):
+            assert torch.equal(out[b], want[0][b]) and torch.equal(lse[b], want[1][b])
+        first = max(0, at - (700 - 3))
+        assert bool(out[1, first:].isnan().all()) and bool(lse[1, first:].isnan().all())
+        if form == "e4m3":
+            assert torch.equal(out[1, :first], want[0][1, :first])
+            assert torch.equal(lse[1, :first], want[1][1, :first])
+    again = p.run(B)
+    assert torch.equal(again[0], want[0]) and torch.equal(again[1], want[1])
+
+
+def test_nan_codes_behind_the_length(B):
+    """Rows of a sequence's last page behind its length hold NaN codes next to live rows."""
+    p = Problem(B, 20, [70, 129, 300], None, 2, 48, 64, "e4m3")
+    codes = p.cache.codes.view(torch.uint8)
+    for b, n in enumerate(p.k_lens):
+        page = p.table[b, (n - 1) // 64].long()
+        codes[page, (n - 1) % 64 + 1:] = 0xff
+    p.check(*p.run(B))
+
+
 def test_no_lse_and_clamped_lengths(B):
     """out_lse is optional at the C entry; lengths outside their range are clamped."""
     p = Problem(B, 11, [128, 100], None, 2, 16, 64, "bf16")
