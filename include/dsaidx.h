@@ -463,7 +463,8 @@ int dsa_cache_write(const dsa_cache* c, const void* x, int32_t x_dtype, int64_t 
 
 /* Read positions [0, n_k) of each sequence into contiguous rows; rows at or behind
  * k_len[b] (device int32, NULL: n_k) are left as they were.  n_k <= max_pages * page_size,
- * batch <= 65535, n_k <= 2^30; out on a 16-byte boundary.
+ * batch 1 .. 65535, n_k 0 .. 2^30 (0: nothing is read, and pointers may be NULL); out on a
+ * 16-byte boundary.
  *   dsa_cache_read        out [batch, n_k, dim_q + dim_raw] of out_dtype DSA_BF16 (the kv
  *                         of dsa_sparse_mla) or DSA_F32
  *   dsa_cache_read_codes  out [batch, n_k, dim_q] e4m3 codes and out_scale [batch, n_k,
@@ -499,9 +500,10 @@ int dsa_cache_read_codes(const dsa_cache* c, const int32_t* block_table, int32_t
  * The softmax weights enter the value product in bf16 (fp32 accumulation); logits, maxima,
  * denominators and partial outputs are fp32.  Results do not depend on the run: the split
  * over positions follows from the lengths alone, and partials are joined in their order.
- * Supported: dim_qk 576, dim_v 512, heads 1 .. 128, max_pages * page_size <= 2^24, scale
- * positive, batch * n_q * heads below 2^31 and, in tiles of 128, rows times positions of
- * the whole batch below 2^28; q and out on 16-byte boundaries.
+ * Supported: batch, n_q and max_pages at least 1, dim_qk 576, dim_v 512, heads 1 .. 128,
+ * max_pages * page_size <= 2^24, scale positive, batch * n_q * heads below 2^31 and, in
+ * tiles of 128, rows times positions of the whole batch below 2^28; q and out on 16-byte
+ * boundaries.
  * workspace: dsa_paged_mla_workspace_size() bytes, 16-byte aligned (status word first). */
 typedef struct {
   int32_t batch;

@@ -143,12 +143,14 @@ int read_args(const dsa_cache* c, const int32_t* table, int32_t batch, int32_t m
               CacheReadArgs* a, dim3* grid) {
   const int v = validate_cache(c);
   if (v != DSA_OK) return v;
-  if (!table || !out || batch < 1 || n_k < 0 || max_pages < 0) return DSA_ERR_INVALID;
-  if (!aligned(table, 4) || !aligned(k_len, 4)) return DSA_ERR_INVALID;
-  if ((int64_t)max_pages * c->page_size < n_k || !aligned16(out)) return DSA_ERR_INVALID;
+  if (batch < 1 || n_k < 0 || max_pages < 0) return DSA_ERR_INVALID;
+  if ((int64_t)max_pages * c->page_size < n_k) return DSA_ERR_INVALID;
   if (batch > 65535 || n_k > (1 << 30)) return DSA_ERR_UNSUPPORTED;
   *grid = dim3(row_blocks(n_k, few ? 4 : 1), (unsigned)batch,
                few ? chunks_of(c) : (chunks_of(c) + at_once - 1) / at_once);
+  if (n_k == 0) return DSA_OK;                       // (nothing to read has no address)
+  if (!table || !out) return DSA_ERR_INVALID;
+  if (!aligned(table, 4) || !aligned(k_len, 4) || !aligned16(out)) return DSA_ERR_INVALID;
   a->c = planes(c);
   a->table = table;
   a->k_len = k_len;
@@ -396,9 +398,10 @@ int dsa_cache_read_codes(const dsa_cache* c, const int32_t* block_table, int32_t
   const int v = read_args(c, block_table, batch, max_pages, n_k, k_len, out, few, kCacheBatch, &a,
                           &blocks);
   if (v != DSA_OK) return v;
-  if (!out_scale || !aligned(out_scale, 4) || c->dim_q == 0) return DSA_ERR_INVALID;
+  if (c->dim_q == 0) return DSA_ERR_INVALID;
   if (c->dim_raw) return DSA_ERR_UNSUPPORTED;
   if (blocks.x == 0) return DSA_OK;
+  if (!out_scale || !aligned(out_scale, 4)) return DSA_ERR_INVALID;
   a.out_scale = out_scale;
   auto kern = few ? cache_read_codes_kernel<4> : cache_read_codes_kernel<1>;
   kern<<<blocks, kCacheThreads, 0, reinterpret_cast<cudaStream_t>(stream)>>>(a);

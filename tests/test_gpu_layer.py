@@ -359,6 +359,23 @@ def test_offsets_past_32_bits(B):
     assert torch.equal(out[0, page - 1], x[0]) and torch.equal(out[0, page - 500], x[1])
 
 
+def test_reading_no_positions(B):
+    """n_k = 0, with and without pages in the table: empty rows, nothing refused (an empty
+    tensor has no address)."""
+    lens = torch.zeros(2, dtype=torch.int32, device="cuda")
+    for pages in (3, 0):
+        table = torch.zeros(2, pages, dtype=torch.int32, device="cuda")
+        for form in FORMS:
+            cache, _ = fresh(B, form)
+            width = sum(FORMS[form])
+            for dtype in (torch.bfloat16, torch.float32):
+                assert B.cache_read(cache, table, 0, lens, dtype=dtype).shape == (2, 0, width)
+        cache, _ = fresh(B, "index")
+        codes, scale = B.cache_read_codes(cache, table, 0, lens)
+        assert codes.shape == (2, 0, 128) and scale.shape == (2, 0)
+    torch.cuda.synchronize()
+
+
 def test_streams_and_graphs(B):
     """Another stream, and a captured call replayed on new inputs."""
     g = torch.Generator().manual_seed(5)

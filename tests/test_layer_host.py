@@ -174,6 +174,22 @@ def test_cache_read_refusals(B):
     assert codes(C.byref(latent), FAKE, 1, 4, 100, None, FAKE, FAKE, None) == -1
 
 
+def test_reading_no_positions(B):
+    """n_k = 0: nothing to do and nothing looked at (an empty tensor has no address); what is
+    wrong with the call otherwise is still refused."""
+    index = cache(B, dim_q=128, dim_raw=0, raw=None, raw_page_stride=0, codes_page_stride=64 * 128)
+    read, codes = B.lib.dsa_cache_read, B.lib.dsa_cache_read_codes
+    for pages in (4, 0):
+        for c in (cache(B), index):
+            for dtype in (B.DSA_BF16, B.DSA_F32):
+                assert read(C.byref(c), None, 2, pages, 0, None, None, dtype, None) == 0
+        assert codes(C.byref(index), None, 2, pages, 0, None, None, None, None) == 0
+    c = cache(B)
+    assert read(C.byref(c), None, 0, 4, 0, None, None, B.DSA_BF16, None) == -1
+    assert read(C.byref(c), None, 1, 4, 0, None, None, 2, None) == -2
+    assert codes(C.byref(c), None, 1, 4, 0, None, None, None, None) == -2
+
+
 def test_binding_refuses_host_tensors(B):
     import torch
     x = torch.zeros(4, 8, 128, dtype=torch.bfloat16)
