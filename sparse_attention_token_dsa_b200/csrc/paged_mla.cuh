@@ -475,10 +475,14 @@ __global__ void __cluster_dims__(2, 1, 1)
   auto wait = [&](uint64_t* bar, uint32_t parity, int where) -> bool {
     return mbar_wait_far(bar, parity, abort, state, where);
   };
-  // The result of `wait`, asked for earlier: a slot's barrier is looked at before the
-  // matrix instructions of the slot before it are issued.
+  // The matrix warps' waits, on barriers where both CTAs arrive (pair_acquire follows where
+  // they announce shared memory).  A slot's barrier is looked at (`seen`) before the matrix
+  // instructions of the slot before it are issued.
+  auto wait_pair = [&](uint64_t* bar, uint32_t parity, int where) -> bool {
+    return mbar_wait_far<true>(bar, parity, abort, state, where);
+  };
   auto wait_seen = [&](bool seen, uint64_t* bar, uint32_t parity, int where) -> bool {
-    return seen || mbar_poll(bar, parity, abort, state, where);
+    return seen || mbar_poll<true>(bar, parity, abort, state, where);
   };
 
   // The roles of warps 4 and up (but for the conversion of codes) run in one lane.
@@ -502,13 +506,14 @@ __global__ void __cluster_dims__(2, 1, 1)
           tma_load_2d(Qs + c * kPmChunk, &qmap, &T->q_full, c * 64, row);
         ok = wait(&T->q_full, qc & 1, 58);
         if (!ok) mbar_wait_drain(&T->q_full, qc & 1);
-        else mbar_arrive_cluster(q_ready);
+        else pair_publish(q_ready);
         if (rank == 0) {
-          ok = ok && wait(&T->q_ready, qc & 1, 53);
+          ok = ok && wait_pair(&T->q_ready, qc & 1, 53);
+          pair_acquire();
           for (int i = 0; i < s.n && ok; ++i, ++sc) {
             const int b = sc & 1;
             bool seen = mbar_seen(&T->k_ready[slot], parity);
-            ok = wait(&T->s_empty[b], ((sc >> 1) & 1) ^ 1, 51);
+            ok = wait_pair(&T->s_empty[b], ((sc >> 1) & 1) ^ 1, 51);
             if (!ok) break;
             tc_fence_after();
             const uint32_t d = tmem + 256 + b * 64;
@@ -516,6 +521,7 @@ __global__ void __cluster_dims__(2, 1, 1)
             for (int k = 0; k < 9; k += Ring::kChunks) {
               ok = ok && wait_seen(seen, &T->k_ready[slot], parity, 52);
               if (!ok) break;
+              pair_acquire();
               const int cur = slot;
               if (++slot == Ring::kKSlots) {
                 slot = 0;
@@ -557,9 +563,9 @@ __global__ void __cluster_dims__(2, 1, 1)
       int slot = 0, parity = 0;                      // of the next V slot
       bool ok = true;
       while (ok && pm_next(a, walk, s)) {
-        ok = wait(&T->o_empty, (qc & 1) ^ 1, 54);
+        ok = wait_pair(&T->o_empty, (qc & 1) ^ 1, 54);
         for (int i = 0; i < s.n && ok; ++i, ++pc) {
-          ok = wait(&T->p_full, pc & 1, 55);
+          ok = wait_pair(&T->p_full, pc & 1, 55);
           if (!ok) break;
           bool seen = mbar_seen(&T->v_ready[slot], parity);
           tc_fence_after();
@@ -567,6 +573,7 @@ __global__ void __cluster_dims__(2, 1, 1)
           for (int v = 0; v < 4; ++v) {
             ok = ok && wait_seen(seen, &T->v_ready[slot], parity, 56);
             if (!ok) break;
+            pair_acquire();                          // (also for P, before the first slot)
             const int cur = slot;
             if (++slot == Ring::kVSlots) {
               slot = 0;
@@ -680,7 +687,7 @@ __global__ void __cluster_dims__(2, 1, 1)
           for (int i = 0; i < s.n && ok; ++i, ++n)
             for (int k = 0; k < Ring::kKSlots && ok; ++k) {
               ok = wait(&T->k_full[k], n & 1, 59);
-              if (ok) mbar_arrive_cluster(k_ready + k * 8);
+              if (ok) pair_publish(k_ready + k * 8);
             }
       } else if (warp == 9) {
         // V slots to the matrix warp, after zeroing the rows behind k_len
@@ -703,7 +710,7 @@ __global__ void __cluster_dims__(2, 1, 1)
                 fence_proxy_async_smem();
                 __syncwarp();
               }
-              if (lane == 0) mbar_arrive_cluster(v_ready + v * 8);
+              if (lane == 0) pair_publish(v_ready + v * 8);
             }
           }
         }
@@ -786,7 +793,7 @@ __global__ void __cluster_dims__(2, 1, 1)
       auto ready = [&](uint32_t bar) {
         fence_proxy_async_smem();
         __syncwarp();
-        if (lane == 0) mbar_arrive_cluster(bar);
+        if (lane == 0) pair_publish(bar);
       };
       if (warp < 8 + kPmLoaders) {
         // K: a warp takes every fourth chunk, a lane two of its rows
@@ -829,7 +836,7 @@ __global__ void __cluster_dims__(2, 1, 1)
               ok = wait(&T->k_full[0], n & 1, 60);
               ok = __all_sync(0xffffffffu, ok);
               if (!ok) break;
-              if (lane == 0) mbar_arrive_cluster(k_ready);
+              if (lane == 0) pair_publish(k_ready);
             }
 #pragma unroll 1
             for (int j = 0; j < 2; ++j) {
@@ -1018,7 +1025,7 @@ __global__ void __cluster_dims__(2, 1, 1)
         fence_proxy_async_smem();
         tc_fence_before();
         __syncwarp();
-        if (lane == 0) mbar_arrive_cluster(p_full);
+        if (lane == 0) pair_publish(p_full);
       }
       wait_all(&T->pv_done, (sc - 1) & 1, 68);
       tc_fence_after();

@@ -21,26 +21,37 @@ __device__ __forceinline__ uint32_t in_cta(const void* p, uint32_t rank) {
   asm volatile("mapa.shared::cluster.u32 %0, %1, %2;" : "=r"(a) : "r"(smem_u32(p)), "r"(rank));
   return a;
 }
-// Arrive on a barrier of the cluster.  Relaxed: a release over the cluster costs about a
-// thousand clocks a call (the attention kernel's 128K decode batch took 5.84 ms with it and
-// 1.84 without), and nothing here needs it.  What the arrival announces is either no memory at all (a slot
-// read by the tensor core, TMEM read back) or shared memory of the arriving thread's own
-// CTA that the async proxy reads: written by TMA and observed on a barrier, or by this
-// warp before a proxy fence, which orders it with the async proxy itself.
+// Arrive on a barrier of the cluster.  Relaxed, so only for what announces no shared memory:
+// TMEM read back, which tcgen05.fence orders with the arrival.
 __device__ __forceinline__ void mbar_arrive_cluster(uint32_t bar) {
   asm volatile("mbarrier.arrive.relaxed.cluster.shared::cluster.b64 _, [%0];" ::"r"(bar)
                : "memory");
 }
 
+// Arrive for shared memory of this CTA that the pair's matrix instructions may read: written by
+// threads (which have fenced it for the async proxy and met the arriving one since) or by TMA
+// (complete on a barrier that this thread has seen).  The release and its counterpart behind
+// the wait, pair_acquire, order shared memory alone.  A release of all memory over the cluster
+// holds its thread for about 700 clocks: with it a prompt chunk took 1.42 ms where it takes
+// 1.00 (and 0.99 with nothing ordered), the 128K decode batch 1.64 for 1.33, 24 ragged
+// sequences of e4m3 rows 153 us for 118.
+__device__ __forceinline__ void pair_publish(uint32_t bar) {
+  asm volatile("fence.release.sync_restrict::shared::cta.cluster;" ::: "memory");
+  mbar_arrive_cluster(bar);
+}
+__device__ __forceinline__ void pair_acquire() {
+  asm volatile("fence.acquire.sync_restrict::shared::cluster.cluster;" ::: "memory");
+}
+
 // Whether a phase is complete, without waiting for it (mbar_try_wait may suspend its thread
 // for up to 20 us, too long for a look ahead that nobody has to wait for: it held back the
 // matrix instructions behind it, the last ones of a cluster for all that time, and a batch
-// of 24 ragged sequences took 131 us where it takes 104).
+// of 24 ragged sequences took 131 us where it took 104).  Relaxed, over the cluster.
 __device__ __forceinline__ bool mbar_seen(uint64_t* bar, uint32_t parity) {
   uint32_t ok;
   asm volatile(
       "{\n\t.reg .pred p;\n\t"
-      "mbarrier.test_wait.parity.shared::cta.b64 p, [%1], %2;\n\t"
+      "mbarrier.test_wait.parity.relaxed.cluster.shared::cta.b64 p, [%1], %2;\n\t"
       "selp.u32 %0, 1, 0, p;\n\t}"
       : "=r"(ok)
       : "r"(smem_u32(bar)), "r"(parity)
@@ -50,13 +61,16 @@ __device__ __forceinline__ bool mbar_seen(uint64_t* bar, uint32_t parity) {
 
 // As mbar_wait, with the polling out of line: a kernel with a role for every warp has
 // dozens of waits, and inlined polls pushed its loops out of the instruction cache.
+template <bool CLUSTER>
 __device__ __noinline__ bool mbar_poll(uint64_t* bar, uint32_t parity, volatile int* abort,
                                        int32_t* status, int where) {
-  return mbar_wait(bar, parity, abort, status, where);
+  return mbar_wait<CLUSTER>(bar, parity, abort, status, where);
 }
+template <bool CLUSTER = false>
 __device__ __forceinline__ bool mbar_wait_far(uint64_t* bar, uint32_t parity, volatile int* abort,
                                               int32_t* status, int where) {
-  return mbar_try_wait(bar, parity) || mbar_poll(bar, parity, abort, status, where);
+  return mbar_try_wait<CLUSTER>(bar, parity) ||
+         mbar_poll<CLUSTER>(bar, parity, abort, status, where);
 }
 
 // ------------------------------------------------------------ cta_group::2 --

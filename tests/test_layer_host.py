@@ -202,3 +202,27 @@ def test_binding_refuses_host_tensors(B):
         B.PagedCache()
     with pytest.raises(TypeError):
         B.PagedCache(raw=[1, 2])
+
+
+def test_arrivals_that_announce_shared_memory_release():
+    """No run can show a missing release between two CTAs, so the source is read: relaxed
+    arrivals on the pair's barriers announce TMEM alone, every other one goes through
+    pair_publish (a release of shared memory), and pair_acquire stands between each wait of
+    the matrix warps for such a barrier and the products."""
+    import os
+    import re
+    from sparse_attention_token_dsa_b200 import build
+    text = open(os.path.join(build.CSRC, "paged_mla.cuh")).read()
+    relaxed = re.findall(r"mbar_arrive_cluster\((\w+)", text)
+    assert sorted(relaxed) == ["o_empty", "s_empty"]
+    assert sorted(re.findall(r"pair_publish\((\w+)", text)) == ["bar", "k_ready", "k_ready", "p_full",
+                                                               "q_ready", "v_ready"]
+    assert sorted(re.findall(r"ready\((\w+) \+ \w+ \* 8\);", text)) == ["k_ready", "v_ready"]   # codes
+    waits = [m.start() for m in re.finditer(r"wait_(?:pair|seen)\((?:seen, )?&T->(?:q_ready|k_ready|p_full|v_ready)",
+                                            text)]
+    assert len(waits) == 4
+    for at in waits:
+        assert 0 < text.index("pair_acquire()", at) < text.index("pair_mma_bf16(", at)
+    pair = open(os.path.join(build.CSRC, "pair.cuh")).read()
+    publish = pair[pair.index("void pair_publish"):pair.index("void pair_acquire")]
+    assert publish.index("fence.release.sync_restrict::shared::cta.cluster") < publish.index("mbar_arrive_cluster(")
