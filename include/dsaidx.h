@@ -130,7 +130,9 @@ enum {
  * the scan's first CTA withholds one stage of keys, so its bounded waits run
  * out.  The call then records DSA_ERR_TIMEOUT, every role of that CTA drains
  * its own copies and MMAs and exits, the select writes padding rows, and the
- * GPU context stays usable for the next call. */
+ * GPU context stays usable for the next call.  dsa_paged_mla does the same: a loader of its
+ * first cluster stops after one tile of 128 positions (a cluster with a single tile runs
+ * through); the outputs of a call that ran out of time are unspecified. */
 #define DSA_FLAG_TEST_STALL 0x80000000u
 
 typedef struct {

@@ -470,6 +470,9 @@ int dsa_paged_mla(const dsa_paged_mla_problem* p, const dsa_cache* c, const void
   a.states = reinterpret_cast<int32_t*>(ws + pl.off_states);
   a.clusters = pl.clusters;
   a.plan = reinterpret_cast<int32_t*>(ws + pl.off_plan);
+  const bool stall = (p->flags & DSA_FLAG_TEST_STALL) != 0;
+  a.wait_kilocycles = (int32_t)((stall ? kTestWaitCycles : kWaitCycles) >> 10);
+  a.stall = stall;
   a.part_ml = reinterpret_cast<float2*>(ws + pl.off_ml);
   a.part_o = reinterpret_cast<float*>(ws + pl.off_o);
   const int smem = (int)paged_mla_smem_bytes();

@@ -80,6 +80,7 @@ constexpr float kPmLazy = 8.f;          // log2 headroom before the maximum is r
 constexpr int kPmLoaders = 4;           // warps that convert e4m3 rows, for K and for V
 constexpr int kPmThreadsRaw = 32 * 10;  // softmax 4, S, PV, K, V, relays of K and V
 constexpr int kPmThreadsCodes = 32 * (8 + 2 * kPmLoaders);   // 8 as above, converting K 4, V 4
+constexpr long long kPmGraceCycles = 200000;         // about 0.1 ms
 constexpr int kPmJoinThreads = 128;
 constexpr int kPmJoinBlocks = 148 * 8;  // of the join, resident at once
 
@@ -93,6 +94,9 @@ struct PagedMlaArgs {
   int32_t pairs;           // batch * row_tiles
   int32_t clusters;
   int32_t join_rows;       // rows that a block of the join takes
+  int32_t wait_kilocycles; // limit of a wait
+  int32_t stall;           // DSA_FLAG_TEST_STALL: in the first cluster CTA 1 loads V (bf16
+                           // rows), or CTA 0 K (e4m3), for one tile only
   float scale_log2;        // softmax scale * log2(e)
   uint16_t* out;           // [batch][n_q][heads][512] bf16
   float* lse;              // [batch][n_q][heads] or null
@@ -111,7 +115,7 @@ struct PagedMlaTail {
   float peer[2][128];      // maxima (and at the end denominators) of a row's two threads
   int32_t start_pair, start_off, count, share, extra;
   uint32_t tmem_base;
-  int32_t abort;
+  WaitLimit limit;
 };
 
 constexpr size_t paged_mla_smem_bytes() {
@@ -363,8 +367,8 @@ struct VLayout {
 // Abort path: let a slot's last copies land.  `n` tiles were begun; the slot's last fill
 // belongs to the n-th or, where the loader gave up before it, to the one before, which
 // the wait's limit then covers.
-__device__ __forceinline__ void drain_slot(uint64_t* full, uint32_t n) {
-  mbar_wait_drain(full, (n & 1) ^ 1, kWaitCycles / 64);
+__device__ __forceinline__ void drain_slot(uint64_t* full, uint32_t n, volatile WaitLimit* limit) {
+  mbar_wait_drain(full, (n & 1) ^ 1, min(wait_cycles(limit), kWaitCycles / 64));
 }
 
 template <bool CODES>
@@ -410,7 +414,8 @@ __global__ void __cluster_dims__(2, 1, 1)
       mbar_init(&T->s_empty[i], 8);
       mbar_init(&T->drain[i], 1);
     }
-    T->abort = 0;
+    T->limit.abort = 0;
+    T->limit.kilocycles = a.wait_kilocycles;
     if (rank == 0) state[0] = DSA_OK;
     fence_barrier_init();
     prefetch_tmap(&qmap);
@@ -468,21 +473,23 @@ __global__ void __cluster_dims__(2, 1, 1)
   cluster_sync();
   tc_fence_after();
   const uint32_t tmem = T->tmem_base;
-  volatile int* abort = &T->abort;
+  volatile WaitLimit* limit = &T->limit;
+  // tiles that a loader stops after (tests of the timeout path; else none)
+  const uint32_t stop = a.stall && cl == 0 && rank == (CODES ? 0 : 1) ? 1u : 0xffffffffu;
   PmWalk walk{T->start_pair, T->start_off, T->count, cl * T->share, T->extra, 2 * cl};
   PmSegment s;
 
   auto wait = [&](uint64_t* bar, uint32_t parity, int where) -> bool {
-    return mbar_wait_far(bar, parity, abort, state, where);
+    return mbar_wait_far(bar, parity, limit, state, where);
   };
   // The matrix warps' waits, on barriers where both CTAs arrive (pair_acquire follows where
   // they announce shared memory).  A slot's barrier is looked at (`seen`) before the matrix
   // instructions of the slot before it are issued.
   auto wait_pair = [&](uint64_t* bar, uint32_t parity, int where) -> bool {
-    return mbar_wait_far<true>(bar, parity, abort, state, where);
+    return mbar_wait_far<true>(bar, parity, limit, state, where);
   };
   auto wait_seen = [&](bool seen, uint64_t* bar, uint32_t parity, int where) -> bool {
-    return seen || mbar_poll<true>(bar, parity, abort, state, where);
+    return seen || mbar_poll<true>(bar, parity, limit, state, where);
   };
 
   // The roles of warps 4 and up (but for the conversion of codes) run in one lane.
@@ -655,13 +662,17 @@ __global__ void __cluster_dims__(2, 1, 1)
         // the MMAs have come before the CTA may end
         for (int k = 0; k < Ring::kKSlots && n; ++k)
           if (ok) wait(&T->k_empty[k], (n & 1) ^ 1, 64);
-          else drain_slot(&T->k_full[k], n);
+          else drain_slot(&T->k_full[k], n, limit);
       } else if (warp == 7 && elect_one()) {
         const int rows = min(1 << shift, 32);
         while (ok && pm_next(a, walk, s)) {
           table = a.table + (int64_t)s.pair.b * a.max_pages;
 #pragma unroll 1
           for (int i = s.t0; i < s.t0 + s.n && ok; ++i, ++n) {
+            if (n == stop) {
+              ok = false;
+              break;
+            }
 #pragma unroll 1
             for (int v = 0; v < Ring::kVSlots; ++v) {
               const int key = i * kPmKeys + v * 32;
@@ -678,7 +689,7 @@ __global__ void __cluster_dims__(2, 1, 1)
         }
         for (int v = 0; v < Ring::kVSlots && n; ++v)
           if (ok) wait(&T->v_empty[v], (n & 1) ^ 1, 65);
-          else drain_slot(&T->v_full[v], n);
+          else drain_slot(&T->v_full[v], n, limit);
       } else if (warp == 8 && elect_one()) {
         // K slots to the matrix warp (in CTA 0).  The slots' own barriers stay in the CTA
         // that issued the copies, so either CTA can wait for its own before it ends.
@@ -723,6 +734,10 @@ __global__ void __cluster_dims__(2, 1, 1)
           table = a.table + (int64_t)s.pair.b * a.max_pages;
 #pragma unroll 1
           for (int i = s.t0; i < s.t0 + s.n && ok; ++i, ++n) {
+            if (n == stop) {
+              ok = false;
+              break;
+            }
             const int key = i * kPmKeys + 64 * rank;
             const int z0 = page_at(key), z1 = rows < 64 ? page_at(key + rows) : 0;
             const int z2 = rows < 32 ? page_at(key + 32) : 0, z3 = rows < 32 ? page_at(key + 48) : 0;
@@ -748,7 +763,7 @@ __global__ void __cluster_dims__(2, 1, 1)
         }
         for (int k = 0; k < Ring::kKSlots && n; ++k)
           if (ok) wait(&T->k_empty[k], (n & 1) ^ 1, 64);
-          else drain_slot(&T->k_full[k], n);
+          else drain_slot(&T->k_full[k], n, limit);
       }
     } else if (warp == 7) {
       // the codes of V, in slices of 32 positions
@@ -777,7 +792,7 @@ __global__ void __cluster_dims__(2, 1, 1)
         }
         for (int v = 0; v < Ring::kVSlots && n; ++v)
           if (ok) wait(&T->v_empty[v], (n & 1) ^ 1, 65);
-          else drain_slot(&T->v_full[v], n);
+          else drain_slot(&T->v_full[v], n, limit);
       }
     } else {
       // Conversion of codes in their slots.  Scales are loaded a tile ahead and their rows'
@@ -937,7 +952,7 @@ __global__ void __cluster_dims__(2, 1, 1)
       return T->peer[at][t ^ 64];
     };
     auto wait_all = [&](uint64_t* bar, uint32_t parity, int where) {
-      if (ok) ok = mbar_wait_far(bar, parity, abort, state, where);
+      if (ok) ok = mbar_wait_far(bar, parity, limit, state, where);
       ok = __all_sync(0xffffffffu, ok);
     };
     while (pm_next(a, walk, s)) {
@@ -1101,6 +1116,12 @@ __global__ void __cluster_dims__(2, 1, 1)
   tc_fence_before();
   __syncthreads();
   asm volatile("griddepcontrol.launch_dependents;");   // the join may be set up meanwhile
+  // a CTA that gave up lets its last arrivals in the other one land before either ends
+  // (otherwise that one has waited for all of them)
+  if (limit->abort) {
+    const long long t0 = clock64();
+    while (clock64() - t0 < kPmGraceCycles) {}
+  }
   __syncwarp();
   cluster_sync();
   if (warp == 4) {

@@ -59,18 +59,27 @@ __device__ __forceinline__ bool mbar_seen(uint64_t* bar, uint32_t parity) {
   return ok != 0;
 }
 
+// What the waits of a CTA share: whether one of them has given up, and how long each may last.
+struct WaitLimit {
+  int32_t abort;
+  int32_t kilocycles;      // SM clocks / 1024
+};
+__device__ __forceinline__ long long wait_cycles(volatile WaitLimit* w) {
+  return (long long)w->kilocycles << 10;
+}
 // As mbar_wait, with the polling out of line: a kernel with a role for every warp has
 // dozens of waits, and inlined polls pushed its loops out of the instruction cache.
 template <bool CLUSTER>
-__device__ __noinline__ bool mbar_poll(uint64_t* bar, uint32_t parity, volatile int* abort,
+__device__ __noinline__ bool mbar_poll(uint64_t* bar, uint32_t parity, volatile WaitLimit* limit,
                                        int32_t* status, int where) {
-  return mbar_wait<CLUSTER>(bar, parity, abort, status, where);
+  return mbar_wait<CLUSTER>(bar, parity, &limit->abort, status, where, wait_cycles(limit));
 }
 template <bool CLUSTER = false>
-__device__ __forceinline__ bool mbar_wait_far(uint64_t* bar, uint32_t parity, volatile int* abort,
-                                              int32_t* status, int where) {
+__device__ __forceinline__ bool mbar_wait_far(uint64_t* bar, uint32_t parity,
+                                              volatile WaitLimit* limit, int32_t* status,
+                                              int where) {
   return mbar_try_wait<CLUSTER>(bar, parity) ||
-         mbar_poll<CLUSTER>(bar, parity, abort, status, where);
+         mbar_poll<CLUSTER>(bar, parity, limit, status, where);
 }
 
 // ------------------------------------------------------------ cta_group::2 --

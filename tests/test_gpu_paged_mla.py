@@ -314,6 +314,32 @@ def test_page_outside_the_cache_is_reported(B, form):
     assert B.dsa_read_status(ws) == 0
 
 
+@pytest.mark.parametrize("form", ["bf16", "e4m3"])
+def test_expired_wait_returns_timeout_then_next_call_is_right(B, form):
+    """DSA_FLAG_TEST_STALL: a loader of the first cluster stops after a tile and every wait
+    lasts at most about a millisecond.  The call returns DSA_ERR_TIMEOUT within a fraction of a
+    second, every role having drained its copies and products, and the next call on the same
+    stream and workspace is right, as are tokens and rows around it."""
+    import time
+    p = Problem(B, 25, [74 * 128 * 3 + 5, 300], [1, 1], 2, 16, 64, form)
+    ws = torch.empty(B.paged_mla_workspace_size(2, 2, 16, p.table.shape[1], 64), dtype=torch.uint8,
+                     device="cuda")
+    want = p.run(B, workspace=ws)
+    p.check(*want)
+    for _ in range(3):
+        torch.cuda.synchronize()
+        t0 = time.perf_counter()
+        with pytest.raises(B.DsaError) as e:
+            p.run(B, workspace=ws, flags=B.DSA_FLAG_CHECK | B.DSA_FLAG_TEST_STALL)
+        took = time.perf_counter() - t0
+        assert e.value.status == B.DSA_ERR_TIMEOUT
+        assert took < 1.0, f"the failed call took {took:.3f} s"
+        assert B.dsa_read_status(ws) == B.DSA_ERR_TIMEOUT
+        got = p.run(B, workspace=ws)
+        assert torch.equal(got[0], want[0]) and torch.equal(got[1], want[1])
+        assert B.dsa_read_status(ws) == B.DSA_OK
+
+
 def test_equals_sparse_mla_over_every_position(B):
     """The selection of all positions gives the same attention (both within their bounds;
     sparse_mla's denominator sums rounded weights: 2^-8)."""
