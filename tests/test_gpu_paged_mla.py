@@ -272,6 +272,31 @@ def test_nan_codes_behind_the_length(B):
     p.check(*p.run(B))
 
 
+def test_no_position_is_lost_or_counted_twice(B):
+    """q = 0: every weight is 1, and with one 1 in each row (column s // 32 mod 512) an output
+    counts its positions exactly: n / total, a power of two here, so a slice of 32 positions
+    that is lost or taken twice changes it by an eighth."""
+    for form in ("bf16", "e4m3"):
+        n, page = 131072, 64
+        g = torch.Generator(device="cuda").manual_seed(24)
+        table = torch.randperm(n // page, device="cuda", generator=g).to(torch.int32)[None]
+        s = torch.arange(n, device="cuda")
+        slot = table[0].long()[s // page] * page + s % page
+        cache = B.PagedCache.empty(n // page, page, *((0, 576) if form == "bf16" else (512, 64)))
+        one = 1.0 if form == "bf16" else 0x38
+        plane = cache.raw if form == "bf16" else cache.codes.view(torch.uint8)
+        plane.view(n, -1)[slot, s // 32 % 512] = one
+        for heads, n_q in ((16, 1), (128, 1)):
+            q = torch.zeros(1, n_q, heads, 576, dtype=torch.bfloat16, device="cuda")
+            for length in (n, n // 2):
+                k_len = torch.tensor([length], dtype=torch.int32, device="cuda")
+                out, lse = B.paged_mla(q, cache, table, k_len, 1.0, flags=B.DSA_FLAG_CHECK)
+                assert bool((out.float() == 1 / 512).all()), (form, heads, length)
+                # log2 and the product with ln 2: under two steps of fp32, 2^-22
+                exact = torch.log(torch.tensor(float(length)).double())
+                assert bool(((lse.double().cpu() - exact).abs() <= 2.0 ** -22 * exact).all())
+
+
 def test_no_lse_and_clamped_lengths(B):
     """out_lse is optional at the C entry; lengths outside their range are clamped."""
     p = Problem(B, 11, [128, 100], None, 2, 16, 64, "bf16")
