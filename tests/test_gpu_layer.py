@@ -88,6 +88,31 @@ def test_rope_far_positions(B):
     assert torch.equal(y[3].cpu(), x[3])
 
 
+@pytest.mark.parametrize("interleaved", [False, True])
+def test_rope_cosines_and_sines(B, interleaved):
+    """x = (1, 0) turned is (cos t, sin t): as the fp32 functions have them, which are off by at
+    most one step, 2^-24 below 1, plus one rounding (2^-25).  Rounding the angle to 32 bits
+    first adds up to pi 2^-25 (half a step of
+    a fraction of a turn from 1/4 to 1/2 is 2^-26)."""
+    g = torch.Generator().manual_seed(41)
+    pos = torch.randint(0, 1 << 20, (4096,), generator=g).to(torch.int32)
+    freq = B.rope_frequencies(64)
+    x = torch.zeros(4096, 1, 64)
+    first = slice(0, 64, 2) if interleaved else slice(0, 32)
+    x[..., first] = 1.0
+    want, _ = turned(x.double(), pos, freq.cpu(), 0, interleaved, 1.0, 1.0)
+    y = B.rope(x.cuda(), pos.cuda(), freq, interleaved=interleaved).double().cpu()
+    worst = float((y - want).abs().max())
+    print("largest error:", worst, "=", worst * 2 ** 24, "steps")
+    assert worst <= 1.55 * 2.0 ** -24
+    # written to a cache as bf16: half a step of that beside it
+    raw = torch.zeros(256, 16, 64, dtype=torch.bfloat16, device="cuda")
+    B.cache_write(B.PagedCache(raw=raw), x[:, 0].cuda(), torch.arange(4096, device="cuda"), freq=freq,
+                  pos=pos.cuda(), interleaved=interleaved)
+    got = raw.view(4096, 64).double().cpu()
+    assert bool(((got - want[:, 0]).abs() <= 2.0 ** -8 * want[:, 0].abs() * 1.001 + 1.55 * 2.0 ** -24).all())
+
+
 def test_rope_strides_and_surroundings(B):
     """A part of a wider buffer, heads before tokens, a broadcast input; what lies
     around the output stays as it was."""
