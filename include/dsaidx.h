@@ -451,9 +451,10 @@ typedef struct {
 /* Write n_tokens rows into the cache: row t of x (dim_q + dim_raw values of x_dtype
  * DSA_BF16 or DSA_F32, x_stride elements apart) goes to slots[t] = page * page_size + row
  * (device int64; a slot outside the cache, such as -1, skips the token).  No two tokens
- * may have the same slot; n_tokens below 2^31.  Scales: amax / 448 over the group, as
- * dsa_quantize_e4m3 (1 where that quotient is 0), or with DSA_FLAG_POW2_SCALE the least power of two that is
- * at least that, which makes scale * code exact in bf16 (for dsa_paged_mla).
+ * may have the same slot, and x lies outside the cache; n_tokens below 2^31.  Scales:
+ * amax / 448 over the group, as dsa_quantize_e4m3 (1 where that quotient is 0), or with
+ * DSA_FLAG_POW2_SCALE the least power of two that is at least that, which makes
+ * scale * code exact in bf16 (for dsa_paged_mla).
  * rope (optional, else NULL with pos and freq NULL): rotates the rot_dim values at
  * rope->offset of the row before they are stored, from x in fp32 with no rounding
  * between; offset a multiple of 8, rot_dim of 16; uses offset, rot_dim, mscale and

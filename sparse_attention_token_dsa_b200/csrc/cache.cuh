@@ -107,9 +107,11 @@ constexpr int kRopeBatch = 3;    // units a thread holds at once
 // three units before it uses any, and the block forms the cosines and sines of its
 // tokens (once for all heads) while they are in flight.  Rows that are not aligned to
 // 16 bytes take the same path one pair at a time (VEC = false).
-// Measured (B200, copy 6545 GB/s): 8192 tokens x 64 heads x 128 bf16 values, 64 of them
-// rotated in halves, 48 us, 5.6 TB/s; 2049 tokens x 64 heads x 576 fp32 values, interleaved,
-// 95 us, 6.4 TB/s.  Four units and 4 blocks an SM took 51 and 96 us, two and 6 54 and 99.
+// Measured (B200, copy 6545 GB/s; here and below replays of a graph over three inputs in turn):
+// 8192 tokens x 64 heads x 128 bf16 values, 64 of them rotated in halves, 47 us, 5.7 TB/s; 2049
+// tokens x 64 heads x 576 fp32 values, interleaved, 94 us, 6.4 TB/s.  Four units and 4 blocks an
+// SM took 51 and 96 us, two and 6 54 and 99.  At 5 blocks the half layouts spill 24 and 32 bytes
+// a thread; at 4, with nothing spilled, the two took 47 and 104 us.
 template <typename T, bool VEC, bool INTER>
 __global__ void __launch_bounds__(kRopeThreads, 5) rope_kernel(const RopeArgs a) {
   using R = RowType<T>;
@@ -373,9 +375,10 @@ __device__ __forceinline__ float quantise(const float (&v)[2][8], float amax, bo
 // nothing is reread.  A scale that is a power of two makes code * scale exact in bf16, so
 // attention on the tensor cores reads the quantised values without a second rounding;
 // e4m3 being a floating format, it costs at most one binade at the bottom of its range.
-// Measured (B200): 131072 keys of 128 values 10.3 us, 5.0 TB/s (with the values waiting
-// for the slots 12.3, and one row at a time 14.4); 8191 latent rows of 512 + 64 values, the
-// 64 rotated, 6.2 us and 32 of them 4.2: launch and latency.
+// Measured (B200): 131072 keys of 128 values 11.5 us, 4.5 TB/s, and 524288 of them 36 us, 5.7
+// TB/s (the same 131072 again and again 10.3; with the values waiting for the slots 12.3, and
+// one row at a time 14.4); 8191 latent rows of 512 + 64 values, the 64 rotated, 5.3 us and 32
+// of them 3.1: launch and latency.
 template <typename T, bool VEC, bool TURN, int ROWS>
 __global__ void __launch_bounds__(kCacheThreads) cache_write_kernel(const CacheWriteArgs a) {
   constexpr int BATCH = ROWS > 1 ? ROWS : kCacheBatch, CHUNKS = BATCH / ROWS;
@@ -504,9 +507,10 @@ __device__ __forceinline__ void rows_to_read(const CacheReadArgs& a, int (&s)[RO
 // (blockIdx.z: which five; a latent row is one run) or one chunk of each of four rows, and
 // hold them at once, two runs of 8 values a lane, 64 apart, so that each store of the 8
 // lanes is one contiguous run (16 codes a lane took 24 us where this takes 20).
-// Measured (B200): 49 thousand latent rows of 512 e4m3 + 64 bf16 values to bf16 19.7 us,
-// 4.5 TB/s, and four times as many 52 us, 5.2 TB/s.  Runs of four chunks took 22.6 us: the
-// second run of a row holds 64 values and looks its page up again.
+// Measured (B200): 65536 latent rows of 512 e4m3 + 64 bf16 values (1808 bytes read and
+// written) to bf16 21.3 us, 5.6 TB/s, and 262144 rows 75 us, 6.3 TB/s; two ragged sequences of
+// up to 32768, 49 thousand rows, 18 us.  Runs of four chunks took a seventh longer: the second
+// run of a row holds 64 values and looks its page up again.
 template <typename T, int ROWS>
 __global__ void __launch_bounds__(kCacheThreads) cache_read_kernel(const CacheReadArgs a) {
   constexpr int BATCH = ROWS > 1 ? ROWS : kReadBatch, CHUNKS = BATCH / ROWS;
@@ -564,7 +568,8 @@ __global__ void __launch_bounds__(kCacheThreads) cache_read_kernel(const CacheRe
 }
 
 // Codes and scales as they stand (the operands of the indexer's e4m3 scan).  Measured
-// (B200): 32 sequences, 270 thousand keys of 128 codes, 12.3 us, 5.8 TB/s.
+// (B200): 32 sequences of 16384 keys of 128 codes 23.8 us, 5.8 TB/s; of up to 16384, 270
+// thousand keys, 14.7 us.
 template <int ROWS>
 __global__ void __launch_bounds__(kCacheThreads) cache_read_codes_kernel(const CacheReadArgs a) {
   constexpr int CHUNKS = kCacheBatch / ROWS;

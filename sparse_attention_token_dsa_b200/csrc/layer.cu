@@ -487,6 +487,11 @@ int dsa_paged_mla(const dsa_paged_mla_problem* p, const dsa_cache* c, const void
   cudaLaunchConfig_t join{};
   const int64_t most = rows < kPmRows ? rows : kPmRows;
   const bool many = pl.pairs * most > kPmJoinBlocks;   // more rows than the GPU holds blocks
+  // Rows a block: with few pairs one, as the GPU holds a block for each row; with many pairs
+  // more, as most pairs were read by one cluster and their blocks only find that out.  Within
+  // 4 % of the best of 1 to 64 (graph replays, us: 4 pairs 24 with 1, 27 with 4, 68 with 32; 32
+  // pairs 64 with 4, 74 with 1 or 32; 100 pairs 125 with 4 or 8, 131 with 32, 145 with 1; 512
+  // pairs 154 with 8 or 32, 158 with 4, 210 with 1).
   a.join_rows = pl.pairs >= 256 ? 32 : (pl.pairs >= 64 ? 8 : (many ? 4 : 1));
   join.gridDim = dim3((unsigned)pl.pairs, (unsigned)((most + a.join_rows - 1) / a.join_rows));
   join.blockDim = dim3(kPmJoinThreads);

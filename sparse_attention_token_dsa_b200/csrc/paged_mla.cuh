@@ -34,18 +34,23 @@
 // Rows of the cache behind k_len hold anything, also NaN: their scores are replaced and
 // their V rows zeroed, as 0 x NaN would not vanish in the product.
 //
-// Measured (B200, warm and back to back; a copy runs at 6545 GB/s there, the library's
-// large bf16 product at 1658 TFLOP/s in a burst and at 1394 for seconds):
-//   one token of 128 heads over 32 x 131072 positions   1.2 to 1.3 ms, 3.6 to 4.0 TB/s and
-//     870 to 960 TFLOP/s at once: the chip is at its 1000 W and lowers the SM clock to 1.3
-//     of 1.97 GHz.  Alone the bytes would take 0.74 ms, the products 0.84 at the sustained
-//     rate.
-//   512 tokens of 128 heads behind 8192 positions   1.00 ms, 1200 TFLOP/s (0.86 of the
-//     sustained rate), at the power limit too.
-//   4 tokens of 64 heads over 24 sequences of 16384 e4m3 positions   0.285 ms, 770 TFLOP/s
-//     (bf16 rows 0.25), at the power limit: a tile's rows are written and read as codes,
-//     written and read as bf16 in shared memory.  Up to 4 tokens and 16001   0.11 ms.
-//   one token of 16 heads over 1000 positions   16 us: two launches, a plan and a join.
+// Measured (B200, warm and back to back, on several boxes; a copy runs at 6545 GB/s there, the
+// library's large bf16 product at 1658 TFLOP/s in a burst and at 1394 for seconds):
+//   one token of 128 heads over 32 x 131072 positions   1.17 to 1.33 ms, 3.6 to 4.1 TB/s and
+//     880 to 1000 TFLOP/s at once, at the chip's 1000 W with the SM clock at 1.05 of 1.97 GHz
+//     (3000 clocks a tile).  Calls 60 ms apart, which run at 1.97 GHz and 270 W, 1.03 ms, 4.7
+//     TB/s: 4600 clocks a tile, so then it is the rows' way from memory through a ring of one
+//     tile that bounds it.  Alone the bytes would take 0.74 ms, the products 0.84 at the
+//     sustained rate.
+//   512 tokens of 128 heads behind 8192 positions   0.97 to 1.00 ms, 1200 to 1240 TFLOP/s (0.86
+//     to 0.89 of the sustained rate), at the power limit, 1.46 GHz; 60 ms apart 0.86 ms.  Over
+//     e4m3 rows 1.35 to 1.40 ms.
+//   4 tokens of 64 heads over 24 sequences of 16384 e4m3 positions   0.285 to 0.30 ms, 750
+//     TFLOP/s (bf16 rows 0.256), at the power limit, 1.67 GHz: a tile's rows are written and
+//     read as codes, written and read as bf16 in shared memory.  Up to 4 tokens and 16001
+//     113 to 120 us; one token of 128 heads over the same 87.
+//   one token of 16 heads over 1000 positions   14 us replayed, 16 called: two launches, a plan
+//     and a join.
 #pragma once
 #include "cache.cuh"
 #include "pair.cuh"
