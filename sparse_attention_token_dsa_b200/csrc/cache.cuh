@@ -7,9 +7,10 @@
 // radians a position.  The transpose, which is also the gradient, turns by -t.
 // The angle of a far position has no digits left in 32 bits, so turns = p (f / 2 pi)
 // is formed in 64 bits and its whole part is dropped.  The remaining fraction goes to
-// sincospif rounded to 32 bits, and what the rounding took turns the result once more to
-// first order: without that the angle's error is as large as the function's own (largest
-// error of a cosine 1.9 steps of 2^-24, with it 1.25).
+// sincospif rounded to 32 bits, and for results in 32 bits what the rounding took turns them
+// once more to first order: without that the angle's error is as large as the function's own
+// (largest error of a cosine 1.9 steps of 2^-24, with it 1.25).  Results in fewer bits do
+// without it (8192 x 64 heads of bf16 values 46 us for 47).
 //
 // The paged cache holds a row's first dim_q values as e4m3 codes in groups of 128 with
 // one fp32 scale a group, and its last dim_raw values as bf16, in three planes
@@ -70,12 +71,15 @@ struct RowType<__nv_bfloat16> {
 };
 
 // cos and sin of position * freq.
+template <bool WHOLE = false>
 __device__ __forceinline__ float2 turn_of(int32_t position, double freq) {
   const double turns = (double)position * (freq * 0.15915494309189533577);   // 1 / (2 pi)
   const double part = turns - rint(turns);                                   // [-1/2, 1/2]
-  const float near = (float)part, rest = (float)(part - near) * 6.2831853f;  // rest in radians
+  const float near = (float)part;
   float s, c;
   sincospif(2.f * near, &s, &c);
+  if constexpr (!WHOLE) return make_float2(c, s);
+  const float rest = (float)(part - near) * 6.2831853f;                      // in radians
   return make_float2(fmaf(-s, rest, c), fmaf(c, rest, s));
 }
 
@@ -108,7 +112,7 @@ constexpr int kRopeBatch = 3;    // units a thread holds at once
 // tokens (once for all heads) while they are in flight.  Rows that are not aligned to
 // 16 bytes take the same path one pair at a time (VEC = false).
 // Measured (B200, copy 6545 GB/s; here and below replays of a graph over three inputs in turn):
-// 8192 tokens x 64 heads x 128 bf16 values, 64 of them rotated in halves, 47 us, 5.7 TB/s; 2049
+// 8192 tokens x 64 heads x 128 bf16 values, 64 of them rotated in halves, 46 us, 5.8 TB/s; 2049
 // tokens x 64 heads x 576 fp32 values, interleaved, 94 us, 6.4 TB/s.  Four units and 4 blocks an
 // SM took 51 and 96 us, two and 6 54 and 99.  At 5 blocks the half layouts spill 24 and 32 bytes
 // a thread; at 4, with nothing spilled, the two took 47 and 104 us.
@@ -168,7 +172,7 @@ __global__ void __launch_bounds__(kRopeThreads, 5) rope_kernel(const RopeArgs a)
     if (!ready) {
       for (int i = threadIdx.x; i < nt * half; i += kRopeThreads) {
         const int tl = i / half, pair = i - tl * half;
-        const float2 cs = turn_of(a.pos[t0 + tl], a.freq[pair]);
+        const float2 cs = turn_of<sizeof(T) == 4>(a.pos[t0 + tl], a.freq[pair]);
         const int at = VEC ? (pair % P / 2 * a.pairs + pair / P) * 2 + (pair & 1) : pair;
         turns[tl * half + at] = make_float2(cs.x * a.mscale, cs.y * a.mscale * a.sign);
       }

@@ -105,12 +105,13 @@ def test_rope_cosines_and_sines(B, interleaved):
     worst = float((y - want).abs().max())
     print("largest error:", worst, "=", worst * 2 ** 24, "steps")
     assert worst <= 1.55 * 2.0 ** -24
-    # written to a cache as bf16: half a step of that beside it
+    # written to a cache as bf16: half a step of that, and the angle in 32 bits
     raw = torch.zeros(256, 16, 64, dtype=torch.bfloat16, device="cuda")
     B.cache_write(B.PagedCache(raw=raw), x[:, 0].cuda(), torch.arange(4096, device="cuda"), freq=freq,
                   pos=pos.cuda(), interleaved=interleaved)
     got = raw.view(4096, 64).double().cpu()
-    assert bool(((got - want[:, 0]).abs() <= 2.0 ** -8 * want[:, 0].abs() * 1.001 + 1.55 * 2.0 ** -24).all())
+    assert bool(((got - want[:, 0]).abs() <= 2.0 ** -8 * want[:, 0].abs() * 1.001
+                 + (1.55 + 3.1416 / 2) * 2.0 ** -24).all())
 
 
 def test_rope_strides_and_surroundings(B):
