@@ -32,7 +32,7 @@ __device__ __forceinline__ void mbar_arrive_cluster(uint32_t bar) {
 // threads (which have fenced it for the async proxy and met the arriving one since) or by TMA
 // (complete on a barrier that this thread has seen).  The release and its counterpart behind
 // the wait, pair_acquire, order shared memory alone.  A release of all memory over the cluster
-// holds its thread for about 700 clocks: with it a prompt chunk took 1.42 ms where it takes
+// holds its thread for hundreds of clocks: with it a prompt chunk took 1.42 ms where it takes
 // 1.00 (and 0.99 with nothing ordered), the 128K decode batch 1.64 for 1.33, 24 ragged
 // sequences of e4m3 rows 153 us for 118.
 __device__ __forceinline__ void pair_publish(uint32_t bar) {
